@@ -349,6 +349,43 @@ gmlp_status gmlp_grouped_mlp_wgrad(const gmlp_bwd_args* args, hipStream_t stream
  * second Hadamard-amax pass [NV, Description]. */
 gmlp_status gmlp_last_launch_counts(int32_t* counts, int32_t n);
 
+/* ------------------------------------------------------------------ grouped products on bf16 / fp16 */
+
+typedef enum { GMLP_BF16 = 0, GMLP_FP16 = 1 } gmlp_dtype;
+
+/* One grouped product on 16-bit operands, rows grouped by m_splits (device int32 [G]), fp32
+ * accumulation on the matrix cores, one rounding to nearest even at the end:
+ *   FPROP  c[r, n] = sum_k a[r, k] b[g, n, k]       a [M, k], b [G, n, k], c [M, n]
+ *   DGRAD  c[r, n] = sum_k a[r, k] b[g, k, n]       a [M, k], b [G, k, n], c [M, n]
+ *   WGRAD  c[g, n, k] = sum_{r in g} a[r, n] b[r, k]  a [M, n], b [M, k], c [G, n, k]
+ * (DGRAD reads the same weight [G, N, K] as FPROP with k = N, n = K.)  The last dimension of every
+ * tensor is contiguous; lda, ldb, ldc are the row strides and b_stride (FPROP, DGRAD), c_stride
+ * (WGRAD) the group strides, in elements; every size, stride and element alignment is taken
+ * (multiples of 16 bytes run on the fast kernels).  Sizes n, k >= 1, row strides < 2^20.
+ * out_dtype: 0 the operands' type, GMLP_OUT_FP32, GMLP_OUT_FP32_ACCUMULATE (the last two WGRAD
+ * only, else GMLP_UNSUPPORTED); an empty group's c[g] is zero, or left as it is when accumulating.
+ * Rows of c behind the last group (splits that sum short of M) are zeroed when zero_rest != 0,
+ * else left as they are.  Splits are clamped on the device as everywhere (gmlp_read_device_flags
+ * on ws).  c must not overlap a or b.
+ * ws: >= gmlp_grouped_matmul_ws_bytes for the same sizes, 16-byte aligned; two calls that may run
+ * at the same time need two. */
+typedef struct {
+  int32_t layout;             /* gmlp_gemm_layout */
+  int32_t dtype;              /* gmlp_dtype of a and b */
+  int32_t out_dtype;
+  int32_t zero_rest;
+  const void* a; int64_t lda;
+  const void* b; int64_t ldb; int64_t b_stride;
+  void* c; int64_t ldc; int64_t c_stride;
+  const int32_t* m_splits;
+  int32_t G;
+  int64_t M, n, k;
+  void* ws; size_t ws_bytes;
+} gmlp_grouped_matmul_args;
+
+gmlp_status gmlp_grouped_matmul_ws_bytes(int32_t layout, int32_t G, int64_t M, int64_t n, int64_t k, size_t* bytes);
+gmlp_status gmlp_grouped_matmul(const gmlp_grouped_matmul_args* args, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

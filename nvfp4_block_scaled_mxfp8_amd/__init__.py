@@ -706,3 +706,8 @@ def grouped_mlp(x, probs, w1, w2, m_splits, activation, rec, w1q=None, w2q=None,
     w2q = w2q if w2q is not None else weight_quantize(w2.detach(), rec)
     return GroupedMLPFunction.apply(x, probs, w1, w2, m_splits, w1q, w2q, activation, rec, recompute,
                                     accumulate_main_grad)
+
+
+# ----------------------------------------------------------------------------- bf16 / fp16 operators
+from .matmul import (OUT_SAME, GroupedMatmulArgs, GroupedMatmulFunction, grouped_matmul,  # noqa: E402
+                     grouped_matmul_dgrad, grouped_matmul_forward, grouped_matmul_wgrad, grouped_matmul_ws_bytes)

@@ -162,4 +162,31 @@ hipError_t launch_gemm(const GemmArgs& g, hipStream_t s);
 int gemm_fprop_ntiles_n(const GemmArgs& g);   // N tiles of an FPROP launch (dprob partial count)
 hipError_t launch_dprob_reduce(const float* part, int nparts, int64_t M, float* out, hipStream_t s);
 
+// ----------------------------------------------------------------------------- 16-bit grouped products
+enum MmType { MM_BF16 = 0, MM_FP16 = 1 };
+enum MmLayout { MM_FPROP = 0, MM_WGRAD = 1, MM_DGRAD = 2 };
+enum MmOut { MM_OUT_SAME = 0, MM_OUT_FP32 = 1, MM_OUT_ACC32 = 2 };
+
+// One grouped product on 16-bit operands (group g owns rows [r_g, r_g + m_g)):
+//   FPROP  C[r, n] = sum_k A[r, k] B_g[n, k]        A [M, k], B_g [n, k]
+//   DGRAD  C[r, n] = sum_k A[r, k] B_g[k, n]        A [M, k], B_g [k, n]
+//   WGRAD  C_g[n, k] = sum_{r in g} A[r, n] B[r, k]   A [M, n], B [M, k]
+// Strides in elements, the last dimension contiguous.
+struct MmArgs {
+  int layout, type, out;
+  const void* a;
+  const void* b;
+  void* c;
+  int64_t lda, ldb, ldc;
+  int64_t b_stride;       // FPROP, DGRAD: from B_g to B_{g+1}
+  int64_t c_stride;       // WGRAD: from C_g to C_{g+1}
+  const int32_t* m_splits;
+  int G;
+  int64_t M;
+  int n, k;
+  int zero_rest;          // FPROP, DGRAD: rows of C behind the last group are written as zeros
+  uint32_t* flags;        // bits as SplitTables::flags
+};
+hipError_t launch_grouped_matmul(const MmArgs& a, hipStream_t s);
+
 }  // namespace gmlp

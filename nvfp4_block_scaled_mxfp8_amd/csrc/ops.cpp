@@ -1,0 +1,104 @@
+// C ABI of the operators on bf16 / fp16 tensors: validation, workspace carving and launches.
+#include "gmlp.h"
+#include "kernels.h"
+#include "planner.h"
+
+#include <algorithm>
+
+using namespace gmlp;
+
+namespace {
+
+constexpr int64_t kMaxRows = 1LL << 30;
+constexpr int64_t kMaxLd = 1LL << 20;      // a tile's rows then span less than 2^31 bytes
+
+gmlp_status fine() { return set_error(GMLP_OK, "%s", ""); }
+gmlp_status launched(hipError_t e, const char* what) {
+  if (e == hipSuccess) return fine();
+  return set_error(GMLP_HIP_ERROR, "system: launching %s failed: %s", what, hipGetErrorString(e));
+}
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+gmlp_status check_dtype(int32_t t) {
+  if (t != GMLP_BF16 && t != GMLP_FP16) return set_error(GMLP_UNSUPPORTED, "dtype: bf16 or fp16 is required, got %d", t);
+  return GMLP_OK;
+}
+
+constexpr size_t kMmWsBytes = 256;
+
+gmlp_status check_mm_sizes(int32_t layout, int32_t G, int64_t M, int64_t n, int64_t k) {
+  if (layout != GMLP_GEMM_FPROP && layout != GMLP_GEMM_WGRAD && layout != GMLP_GEMM_DGRAD)
+    return set_error(GMLP_INVALID_ARG, "layout: unknown layout %d", layout);
+  if (G < 1) return set_error(GMLP_INVALID_ARG, "dims: number of groups must be >= 1, got %d", G);
+  if (M < 0 || M > kMaxRows) return set_error(GMLP_UNSUPPORTED, "dims: M = %lld rows is out of range", (long long)M);
+  if (n < 1 || k < 1 || n >= kMaxLd || k >= kMaxLd)
+    return set_error(GMLP_UNSUPPORTED, "dims: n and k must be in [1, 2^20), got %lld and %lld", (long long)n, (long long)k);
+  // the smallest tile's launch must fit one grid
+  const int64_t tn = (n + 63) / 64, tk = (k + 63) / 64;
+  const double tiles = layout == GMLP_GEMM_WGRAD ? (double)G * tn * tk
+                                                 : (double)((M + 63 * std::min<int64_t>((int64_t)G + 1, M)) / 64) * tn;
+  if (tiles > 2147483647.0) return set_error(GMLP_UNSUPPORTED, "dims: %d groups of %lld x %lld exceed one launch", G, (long long)n, (long long)k);
+  return GMLP_OK;
+}
+
+}  // namespace
+
+extern "C" gmlp_status gmlp_grouped_matmul_ws_bytes(int32_t layout, int32_t G, int64_t M, int64_t n, int64_t k,
+                                                    size_t* bytes) {
+  if (!bytes) return set_error(GMLP_INVALID_ARG, "null pointer argument");
+  const gmlp_status st = check_mm_sizes(layout, G, M, n, k);
+  if (st != GMLP_OK) return st;
+  *bytes = kMmWsBytes;
+  return fine();
+}
+
+extern "C" gmlp_status gmlp_grouped_matmul(const gmlp_grouped_matmul_args* p, hipStream_t stream) {
+  if (!p) return set_error(GMLP_INVALID_ARG, "null pointer argument");
+  gmlp_status st = check_dtype(p->dtype);
+  if (st != GMLP_OK) return st;
+  size_t need = 0;
+  if ((st = gmlp_grouped_matmul_ws_bytes(p->layout, p->G, p->M, p->n, p->k, &need)) != GMLP_OK) return st;
+  const bool wgrad = p->layout == GMLP_GEMM_WGRAD;
+  if (p->out_dtype != 0 && p->out_dtype != GMLP_OUT_FP32 && p->out_dtype != GMLP_OUT_FP32_ACCUMULATE)
+    return set_error(GMLP_INVALID_ARG, "out_dtype: unknown value %d", p->out_dtype);
+  if (p->out_dtype != 0 && !wgrad)
+    return set_error(GMLP_UNSUPPORTED, "out_dtype: fp32 outputs are for weight gradients only");
+  if (!p->m_splits || (p->M > 0 && (!p->a || !p->b)) || ((wgrad || p->M > 0) && !p->c))
+    return set_error(GMLP_INVALID_ARG, "null pointer argument");
+  if (!aligned2(p->a) || !aligned2(p->b) || !aligned4(p->m_splits) || !(p->out_dtype ? aligned4(p->c) : aligned2(p->c)))
+    return set_error(GMLP_INVALID_ARG, "a tensor is not aligned to its elements");
+  const int64_t acols = wgrad ? p->n : p->k;
+  const int64_t bcols = p->layout == GMLP_GEMM_DGRAD ? p->n : p->k;
+  const int64_t ccols = wgrad ? p->k : p->n;
+  if (p->lda < acols || p->ldb < bcols || p->ldc < ccols || p->lda >= kMaxLd || p->ldb >= kMaxLd || p->ldc >= kMaxLd)
+    return set_error(GMLP_INVALID_ARG, "strides: row strides must be at least the row's length and below 2^20");
+  const int64_t brows = p->layout == GMLP_GEMM_DGRAD ? p->k : p->n;
+  if (!wgrad && p->G > 1 && p->b_stride < (brows - 1) * p->ldb + bcols)
+    return set_error(GMLP_INVALID_ARG, "strides: the groups' weights overlap");
+  if (wgrad && p->G > 1 && p->c_stride < (p->n - 1) * p->ldc + p->k)
+    return set_error(GMLP_INVALID_ARG, "strides: the groups' outputs overlap");
+  if (!p->ws || p->ws_bytes < need || !aligned16(p->ws))
+    return set_error(GMLP_WORKSPACE, "workspace: %zu bytes, 16-byte aligned, are needed", need);
+  MmArgs a{};
+  a.layout = p->layout;
+  a.type = p->dtype;
+  a.out = p->out_dtype;
+  a.a = p->a;
+  a.b = p->b;
+  a.c = p->c;
+  a.lda = p->lda;
+  a.ldb = p->ldb;
+  a.ldc = p->ldc;
+  a.b_stride = p->b_stride;
+  a.c_stride = p->c_stride;
+  a.m_splits = p->m_splits;
+  a.G = p->G;
+  a.M = p->M;
+  a.n = (int)p->n;
+  a.k = (int)p->k;
+  a.zero_rest = p->zero_rest != 0;
+  a.flags = static_cast<uint32_t*>(p->ws);
+  return launched(launch_grouped_matmul(a, stream), "grouped matmul");
+}
