@@ -8,6 +8,12 @@
 
 namespace gmlp {
 
+#ifndef GMM_T
+#define GMM_T 256
+#define GMM_WM 2
+#define GMM_WN 4
+#endif
+
 // ----------------------------------------------------------------------------- any alignment
 // 64 x 64 tile, 4 waves of 32 x 32, 32-deep stages through registers into LDS, every element
 // checked.  Takes every stride, size and alignment; what the 16-byte loads of the other kernels
@@ -97,6 +103,304 @@ __global__ __launch_bounds__(256) void gmm_any_kernel(MmArgs p) {
   }
 }
 
+// ----------------------------------------------------------------------------- ring kernel
+// Tiles of TM x TN (TM == TN), NWM x NWN waves, contraction in stages of 64.  A stage is two units,
+// A's and B's 64-deep slabs of the tile (TM x 128 bytes each), and the units of all stages run
+// through a ring of five LDS slots filled by buffer-to-LDS DMA: while stage s is read, both units
+// of stage s + 1 and A of s + 2 are on their way.  One barrier a stage: at it every wave has the
+// stage's last fragments in registers and its share of the next stage's units has landed, so the
+// two slots read last are refilled and the next stage's first fragments read while the last
+// sixteen-deep step's MFMAs run.
+//
+// A unit whose operand is contiguous along the contraction (x, dy and FPROP's w) holds rows of 128
+// bytes, 16-byte chunks XOR-swizzled by row so that 16 consecutive rows meet all 16 bank groups;
+// fragments are ds_read_b128.  A unit whose operand has the contraction along its rows in memory
+// (DGRAD's w, both of WGRAD's) holds 64 rows of TM elements as they are in memory; its fragments
+// are transposed on the way out by ds_read_b64_tr_b16 (16 lanes read four rows of 16 elements and
+// get one column of four each), chunks XORed by (row % 4) so that the four rows fall into four
+// different 64-byte windows of the banks.
+//
+// Rows, columns and contraction past the operand's end read as zero by the buffer range check;
+// a contraction tail inside a row (k % 64) is cut per lane in the last stage.
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+
+__device__ __forceinline__ int sgpr(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t sgpr64(uint64_t v) {
+  return (uint64_t)(uint32_t)sgpr((int)(uint32_t)v) | ((uint64_t)(uint32_t)sgpr((int)(uint32_t)(v >> 32)) << 32);
+}
+// 16 bytes per lane from a buffer into LDS at m0 + 16 lane.  Inline asm, as the compiler would wait
+// for every outstanding DMA before each LDS read; the kernel counts them itself.
+__device__ __forceinline__ void dma16(v4i rsrc, uint32_t voff, uint32_t soff, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               :: "v"(voff), "s"(rsrc), "s"(soff), "s"(m0) : "memory");
+}
+template <int VM>
+__device__ __forceinline__ void wait_stage() {      // all LDS reads back, at most VM DMAs in flight
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"(VM) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+constexpr uint32_t kNoLane = 0x80000000u;            // past every range: the lane reads zeros
+
+// One operand's stream of units.
+template <bool TR, int T, int NT>
+struct Feed {
+  static constexpr int kDma = T * 128 / (NT * 16);   // DMAs per unit and wave
+  uint64_t base;                // address of the current stage's unit
+  int64_t rest;                 // !TR: bytes of all but the last valid row;  TR: bytes behind the current stage's first row
+  int32_t left;                 // contraction elements from the current stage on (clamped)
+  uint32_t voff, vtail;         // lane offset; in the last stage
+  uint32_t step;                // bytes between a wave's DMAs of one unit
+  uint32_t row_bytes;           // 2 ld
+  uint32_t cols_bytes;          // TR: bytes from the tile's first column to the end of a row
+
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int valid, int64_t kn, int tid) {
+    base = sgpr64((uint64_t)(uintptr_t)p);
+    row_bytes = (uint32_t)(2 * ld);
+    left = sgpr((int)min(kn, (int64_t)0x40000000));
+    if (!TR) {
+      const int r = tid >> 3, c = (tid & 7) ^ ((r >> 1) & 7);
+      voff = r * row_bytes + c * 16;
+      vtail = 8 * c < ((left + 63) % 64 + 1) ? voff : kNoLane;
+      step = (NT / 8) * row_bytes;
+      rest = (int64_t)(valid - 1) * row_bytes;
+    } else {
+      constexpr int CPR = T / 8;
+      const int r = tid / CPR, c = (tid % CPR) ^ ((r & 3) << 2);
+      voff = 8 * c < valid ? r * row_bytes + c * 16 : kNoLane;
+      vtail = voff;
+      step = (NT / CPR) * row_bytes;
+      cols_bytes = 2 * min(valid, T);
+    }
+  }
+  // The unit's descriptor, then on to the next stage.
+  __device__ __forceinline__ void next(v4i& rsrc, uint32_t& v) {
+    int32_t n;
+    if (!TR) n = left > 0 ? (int32_t)rest + 2 * left : 0;
+    else n = left > 0 ? (int32_t)min((uint64_t)(uint32_t)(left - 1) * row_bytes + cols_bytes, (uint64_t)0x7FFFFFFF) : 0;
+    rsrc = v4i{(int)(uint32_t)base, (int)((uint32_t)(base >> 32) & 0xFFFFu), n, 0x00020000};
+    v = left <= 64 ? vtail : voff;
+    base += TR ? 64ull * row_bytes : 128ull;
+    left -= 64;
+  }
+  __device__ __forceinline__ void issue(uint32_t slot, int wave) {
+    v4i rsrc;
+    uint32_t v;
+    next(rsrc, v);
+#pragma unroll
+    for (int i = 0; i < kDma; ++i) dma16(rsrc, v, (uint32_t)sgpr(i * step), (uint32_t)sgpr(slot + i * NT * 16 + wave * 1024));
+  }
+};
+
+// Fragments of one 16-deep step: N tiles of 32 rows (columns) of the unit from row `first`.
+template <bool TR, int T, int N>
+struct Frags {
+  uint32_t off[4];              // lane offsets: !TR by step, TR by tile
+  __device__ __forceinline__ void init(int first, int lane) {
+    if (!TR) {
+      const int r = lane & 31, j = lane >> 5;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) off[s] = (first + r) * 128 + (((2 * s + j) ^ ((r >> 1) & 7)) << 4);
+    } else {
+      const int i = lane & 15, r = i >> 2, j = lane >> 5;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int chunk = ((first / 8 + 4 * t + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1)) ^ (r << 2));
+        off[t] = (8 * j + r) * (T * 2) + chunk * 16 + (i & 1) * 8;
+      }
+    }
+  }
+  __device__ __forceinline__ void read(uint32_t unit, int s, v4i* f) const {
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+      if (!TR) {
+        f[t] = *(const __attribute__((address_space(3))) v4i*)(uintptr_t)(unit + off[s] + t * 32 * 128);
+      } else {
+        const uint32_t a = unit + off[t] + s * 16 * (T * 2);
+        const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)a);
+        const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)(a + 4 * (T * 2)));
+        const v2i l2 = __builtin_bit_cast(v2i, lo), h2 = __builtin_bit_cast(v2i, hi);
+        f[t] = v4i{l2.x, l2.y, h2.x, h2.y};
+      }
+    }
+  }
+};
+
+template <int TYPE, int LAYOUT, int OUT, int T, int NWM, int NWN>
+__global__ __launch_bounds__(64 * NWM * NWN, 2) void gmm_ring_kernel(MmArgs p) {
+  using E = Elem<TYPE>;
+  constexpr int NT = 64 * NWM * NWN, SLOT = T * 128;
+  constexpr bool AT = LAYOUT == MM_WGRAD, BT = LAYOUT != MM_FPROP;
+  constexpr int WM = T / NWM, WN = T / NWN, NA = WM / 32, NB = WN / 32;
+  static_assert(WN == 64, "the epilogue stages rows of 64 columns");
+  __shared__ __align__(1024) uint8_t lds[5 * SLOT];
+  const int tid = threadIdx.x, lane = tid & 63, wave = sgpr(tid >> 6);
+  if (blockIdx.x == 0 && wave == 0) {
+    const uint32_t f = wave_split_flags(p.m_splits, p.G, p.M, lane);
+    if (lane == 0) *p.flags = f;
+  }
+  const uint16_t* A = static_cast<const uint16_t*>(p.a);
+  const uint16_t* B = static_cast<const uint16_t*>(p.b);
+  int64_t crow0, kn;
+  int arows, bcols, col0, ncols;
+  if (LAYOUT == MM_WGRAD) {
+    const uint32_t ntm = (p.n + T - 1) / T, ntn = (p.k + T - 1) / T, tpg = ntm * ntn;
+    uint32_t g, t;
+    if (tpg >= 64) {                     // XCD x takes the x-th eighth of every group's tiles
+      const uint32_t per = (tpg + 7) / 8, x = blockIdx.x & 7, l = blockIdx.x >> 3;
+      g = l / per;
+      t = x * per + l % per;
+      if (t >= tpg || (int)g >= p.G) return;
+    } else {
+      g = blockIdx.x / tpg;
+      t = blockIdx.x % tpg;
+      if ((int)g >= p.G) return;
+    }
+    const RowTile rt = find_group_rows(p.m_splits, p.G, (uint32_t)p.M, (int)g, lane);
+    constexpr uint32_t GR = 4;           // four row tiles to a column sweep
+    const uint32_t grp = t / (GR * ntn), rem = t % (GR * ntn), rh = min(GR, ntm - grp * GR);
+    const int tm = (int)((grp * GR + rem % rh) * T);
+    col0 = (int)(rem / rh * T);
+    arows = p.n - tm;
+    ncols = p.k;
+    kn = rt.m;
+    if (OUT == MM_OUT_ACC32 && kn == 0) return;
+    A += (int64_t)rt.row0 * p.lda + tm;
+    B += (int64_t)rt.row0 * p.ldb + col0;
+    crow0 = tm;
+    p.c = static_cast<uint8_t*>(p.c) + (int64_t)g * p.c_stride * (OUT == MM_OUT_SAME ? 2 : 4);
+  } else {
+    const uint32_t ntn = (p.n + T - 1) / T;
+    const uint32_t total = row_tiles_total(p.m_splits, p.G, (uint32_t)p.M, T, ntn, p.zero_rest, lane);
+    const uint32_t per = (total + 7) / 8, l = blockIdx.x >> 3;     // XCD x takes the x-th eighth of the tiles
+    if (l >= per) return;
+    const RowTile rt = find_row_tile(p.m_splits, p.G, (uint32_t)p.M, T, ntn, p.zero_rest, (blockIdx.x & 7) * per + l, lane);
+    if (rt.g < 0) return;
+    constexpr uint32_t GR = 4;
+    const uint32_t ntm = (rt.m + T - 1) / T;
+    const uint32_t grp = rt.t / (GR * ntn), rem = rt.t % (GR * ntn), rh = min(GR, ntm - grp * GR);
+    const uint32_t tm = (grp * GR + rem % rh) * T;
+    col0 = (int)(rem / rh * T);
+    arows = (int)(rt.m - tm);
+    ncols = p.n;
+    kn = rt.g < p.G ? p.k : 0;
+    crow0 = (int64_t)rt.row0 + tm;
+    A += crow0 * p.lda;
+    if (rt.g < p.G) B += (int64_t)rt.g * p.b_stride + (LAYOUT == MM_FPROP ? (int64_t)col0 * p.ldb : (int64_t)col0);
+  }
+  arows = sgpr(min(arows, T));
+  bcols = sgpr(min(ncols - col0, T));
+
+  const int wm = wave / NWN, wn = wave % NWN;
+  v16f acc[NA][NB];
+#pragma unroll
+  for (int i = 0; i < NA; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = v16f{};
+
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+  const int nst = sgpr((int)((kn + 63) / 64));
+  if (nst > 0) {
+    Feed<AT, T, NT> fa;
+    Feed<BT, T, NT> fb;
+    fa.init(A, p.lda, arows, kn, tid);
+    fb.init(B, p.ldb, bcols, kn, tid);
+    Frags<AT, T, NA> ra;
+    Frags<BT, T, NB> rb;
+    ra.init(wm * WM, lane);
+    rb.init(wn * WN, lane);
+    constexpr int P = Feed<AT, T, NT>::kDma;
+    fa.issue(lds0 + 0 * SLOT, wave);
+    fb.issue(lds0 + 1 * SLOT, wave);
+    fa.issue(lds0 + 2 * SLOT, wave);
+    fb.issue(lds0 + 3 * SLOT, wave);
+    fa.issue(lds0 + 4 * SLOT, wave);
+    uint32_t ua = lds0, ub = lds0 + SLOT;       // the stage's units
+    const uint32_t end = lds0 + 5 * SLOT;
+    v4i a[2][NA], b[2][NB];
+    wait_stage<3 * P>();
+    ra.read(ua, 0, a[0]);
+    rb.read(ub, 0, b[0]);
+    for (int s = 0; s < nst; ++s) {
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const int cur = ks & 1, nxt = cur ^ 1;
+        if (ks < 3) {
+          ra.read(ua, ks + 1, a[nxt]);
+          rb.read(ub, ks + 1, b[nxt]);
+        } else {
+          wait_stage<P>();
+          fb.issue(ua, wave);                     // B of stage s + 2 into A's slot, A of s + 3 into B's
+          fa.issue(ub, wave);
+          ua += 2 * SLOT;
+          ub += 2 * SLOT;
+          if (ua >= end) ua -= 5 * SLOT;
+          if (ub >= end) ub -= 5 * SLOT;
+          ra.read(ua, 0, a[nxt]);
+          rb.read(ub, 0, b[nxt]);
+        }
+        // the transposed product: a lane then holds consecutive columns of one row
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+#pragma unroll
+          for (int j = 0; j < NB; ++j) acc[i][j] = E::mma32(b[cur][j], a[cur][i], acc[i][j]);
+      }
+    }
+    wait_stage<0>();
+  }
+
+  // acc[i][j][e]: row 32 i + lane % 32, column 32 j + 8 (e / 4) + 4 (lane / 32) + e % 4 of the wave's
+  // tile.  Each wave stages its own rows of 128 bytes and stores whole ones.
+  const uint32_t reg = lds0 + wave * (WM * 128);
+  const int m = lane & 31, h = lane >> 5, msw = (m >> 1) & 7;
+  const int sr = lane >> 3, sc = lane & 7;
+  typedef __attribute__((address_space(3))) v4i lds_v4i;
+  typedef __attribute__((address_space(3))) v2i lds_v2i;
+  constexpr int PASSES = OUT == MM_OUT_SAME ? 1 : NB;
+#pragma unroll
+  for (int ps = 0; ps < PASSES; ++ps) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const uint32_t row = reg + (32 * i + m) * 128;
+      if constexpr (OUT == MM_OUT_SAME) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const v2i v{(int)E::down2(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
+                         (int)E::down2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
+            *(lds_v2i*)(uintptr_t)(row + (((4 * j + q) ^ msw) << 4) + h * 8) = v;
+          }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const v4f v{acc[i][ps][4 * q], acc[i][ps][4 * q + 1], acc[i][ps][4 * q + 2], acc[i][ps][4 * q + 3]};
+          *(lds_v4i*)(uintptr_t)(row + (((2 * q + h) ^ msw) << 4)) = __builtin_bit_cast(v4i, v);
+        }
+      }
+    }
+#pragma unroll
+    for (int r0 = 0; r0 < WM; r0 += 8) {
+      const int r = r0 + sr, tr = wm * WM + r;
+      const v4i v = *(lds_v4i*)(uintptr_t)(reg + r * 128 + ((sc ^ ((r >> 1) & 7)) << 4));
+      if constexpr (OUT == MM_OUT_SAME) {
+        const int c = wn * WN + sc * 8;
+        if (tr < arows && c < bcols)
+          *reinterpret_cast<v4i*>(static_cast<uint16_t*>(p.c) + (crow0 + tr) * p.ldc + col0 + c) = v;
+      } else {
+        const int c = wn * WN + ps * 32 + sc * 4;
+        if (tr < arows && c < bcols) {
+          v4f* dst = reinterpret_cast<v4f*>(static_cast<float*>(p.c) + (crow0 + tr) * p.ldc + col0 + c);
+          const v4f f = __builtin_bit_cast(v4f, v);
+          if (OUT == MM_OUT_FP32) *dst = f;
+          else *dst = *dst + f;
+        }
+      }
+    }
+  }
+}
+
 // The most row tiles of height h that any splits of M rows give: at most min(G + 1, M) runs of rows
 // (the groups and the rows behind them), each with less than one tile of padding.
 static int64_t row_tiles_bound(const MmArgs& p, int h) {
@@ -114,13 +418,40 @@ static hipError_t run_any(const MmArgs& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int TYPE, int LAYOUT, int OUT, int T, int NWM, int NWN>
+static hipError_t run_ring(const MmArgs& p, hipStream_t s) {
+  int64_t grid;
+  if (LAYOUT == MM_WGRAD) {
+    const int64_t tpg = (int64_t)((p.n + T - 1) / T) * ((p.k + T - 1) / T);
+    grid = tpg >= 64 ? 8 * ((tpg + 7) / 8) * p.G : tpg * p.G;
+  } else {
+    grid = 8 * ((row_tiles_bound(p, T) * ((p.n + T - 1) / T) + 7) / 8);
+  }
+  grid = std::max<int64_t>(grid, 8);
+  auto* k = gmm_ring_kernel<TYPE, LAYOUT, OUT, T, NWM, NWN>;
+  hipLaunchKernelGGL(k, dim3((uint32_t)grid), dim3(64 * NWM * NWN), 0, s, p);
+  return hipGetLastError();
+}
+
+// 16-byte loads and stores throughout.
+static bool vec_ok(const MmArgs& p) {
+  const uintptr_t addr = reinterpret_cast<uintptr_t>(p.a) | reinterpret_cast<uintptr_t>(p.b) | reinterpret_cast<uintptr_t>(p.c);
+  return (addr & 15) == 0 && ((p.n | p.k | p.lda | p.ldb | p.ldc | p.b_stride | p.c_stride) & 7) == 0;
+}
+
+template <int TYPE, int LAYOUT, int OUT>
+static hipError_t run_sized(const MmArgs& p, hipStream_t s) {
+  if (!vec_ok(p)) return run_any<TYPE, LAYOUT, OUT>(p, s);
+  return run_ring<TYPE, LAYOUT, OUT, GMM_T, GMM_WM, GMM_WN>(p, s);
+}
+
 template <int TYPE>
 static hipError_t run_type(const MmArgs& p, hipStream_t s) {
-  if (p.layout == MM_FPROP) return run_any<TYPE, MM_FPROP, MM_OUT_SAME>(p, s);
-  if (p.layout == MM_DGRAD) return run_any<TYPE, MM_DGRAD, MM_OUT_SAME>(p, s);
-  if (p.out == MM_OUT_SAME) return run_any<TYPE, MM_WGRAD, MM_OUT_SAME>(p, s);
-  if (p.out == MM_OUT_FP32) return run_any<TYPE, MM_WGRAD, MM_OUT_FP32>(p, s);
-  return run_any<TYPE, MM_WGRAD, MM_OUT_ACC32>(p, s);
+  if (p.layout == MM_FPROP) return run_sized<TYPE, MM_FPROP, MM_OUT_SAME>(p, s);
+  if (p.layout == MM_DGRAD) return run_sized<TYPE, MM_DGRAD, MM_OUT_SAME>(p, s);
+  if (p.out == MM_OUT_SAME) return run_sized<TYPE, MM_WGRAD, MM_OUT_SAME>(p, s);
+  if (p.out == MM_OUT_FP32) return run_sized<TYPE, MM_WGRAD, MM_OUT_FP32>(p, s);
+  return run_sized<TYPE, MM_WGRAD, MM_OUT_ACC32>(p, s);
 }
 
 hipError_t launch_grouped_matmul(const MmArgs& p, hipStream_t s) {
