@@ -386,6 +386,45 @@ typedef struct {
 gmlp_status gmlp_grouped_matmul_ws_bytes(int32_t layout, int32_t G, int64_t M, int64_t n, int64_t k, size_t* bytes);
 gmlp_status gmlp_grouped_matmul(const gmlp_grouped_matmul_args* args, hipStream_t stream);
 
+/* ------------------------------------------------------------------ expert dispatch and combine */
+
+/* The order that brings T tokens with k experts each to rows grouped by expert, as grouped_mlp and
+ * gmlp_grouped_matmul take them: a stable counting sort of the n = T k slots of experts (device
+ * int32, slot t k + j).  m_splits [E] = slots per expert; rows [n] = the slot's row, -1 for an expert
+ * outside [0, E) (the slot is dropped); order [n] (may be NULL) = the slot at each row, -1 behind the
+ * last used row.  1 <= E <= 1024, n < 2^30.  ws: >= gmlp_dispatch_plan_ws_bytes (16-byte aligned;
+ * may be NULL where that is 0). */
+gmlp_status gmlp_dispatch_plan_ws_bytes(int64_t n, int32_t E, size_t* bytes);
+gmlp_status gmlp_dispatch_plan(const int32_t* experts, int64_t n, int32_t E, int32_t* m_splits, int32_t* rows,
+                               int32_t* order, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Moves between token order [T, H] and expert order [T k, H] (bf16 or fp16, row strides in elements,
+ * the last dimension contiguous), rows [T, k] from gmlp_dispatch_plan; a row outside [0, T k) is
+ * dropped.  probs: fp32 [T, k], or NULL for 1.  Sums are taken in fp32 in the order of j and rounded
+ * once.
+ *   dispatch          dst[rows[t, j]] = probs[t, j] src[t]        (src by token; also combine's gradient for v)
+ *   combine           dst[t] = sum_j probs[t, j] src[rows[t, j]]  (src by row; also dispatch's gradient)
+ *   combine_dprobs    dprobs[t, j] = sum_h src[t, h] src2[rows[t, j], h]   (0 for a dropped slot)
+ * Rows of dispatch's dst behind the sum of m_splits [E] are zeroed when zero_rest != 0, else left as
+ * they are.  Outputs must not overlap inputs. */
+typedef struct {
+  int32_t dtype;              /* gmlp_dtype */
+  int32_t zero_rest;
+  const void* src; int64_t ld_src;
+  const void* src2; int64_t ld_src2;
+  void* dst; int64_t ld_dst;
+  int64_t T, H;
+  int32_t k;
+  int32_t E;
+  const int32_t* rows;
+  const int32_t* m_splits;    /* dispatch with zero_rest only */
+  const float* probs;
+  float* dprobs;              /* combine_dprobs */
+} gmlp_move_args;
+gmlp_status gmlp_dispatch(const gmlp_move_args* args, hipStream_t stream);
+gmlp_status gmlp_combine(const gmlp_move_args* args, hipStream_t stream);
+gmlp_status gmlp_combine_dprobs(const gmlp_move_args* args, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

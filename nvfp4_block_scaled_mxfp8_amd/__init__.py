@@ -711,3 +711,6 @@ def grouped_mlp(x, probs, w1, w2, m_splits, activation, rec, w1q=None, w2q=None,
 # ----------------------------------------------------------------------------- bf16 / fp16 operators
 from .matmul import (OUT_SAME, GroupedMatmulArgs, GroupedMatmulFunction, grouped_matmul,  # noqa: E402
                      grouped_matmul_dgrad, grouped_matmul_forward, grouped_matmul_wgrad, grouped_matmul_ws_bytes)
+from .expert_dispatch import (CombineFunction, DispatchFunction, DispatchPlan, MoveArgs, combine,  # noqa: E402
+                       combine_backward, combine_forward, dispatch, dispatch_backward, dispatch_forward,
+                       dispatch_plan)

@@ -1,0 +1,326 @@
+// The order of rows by group (a stable counting sort), and the moves between token order and expert
+// order: dispatch, combine and their gradients.  All of it is bound by memory (or, in a decode
+// step, by the launch): every tensor is read and written once, 16 bytes per lane.
+#include "mm_common.h"
+
+#include <algorithm>
+
+namespace gmlp {
+
+// ----------------------------------------------------------------------------- group order
+// A block takes a contiguous chunk of the slots, each of its 16 waves a contiguous part of that, 64
+// slots at a time.  Within a wave the lanes with the same id find each other by one ballot per bit
+// of the id; a wave's running position per group sits in LDS.  So positions depend on nothing but
+// the ids: the sort is stable and every run gives the same order.
+//   counting pass (several blocks): the chunk's slots per group -> ws[block][G]
+//   placing pass: a group's first position (the slots of lower groups, and of this group in earlier
+//   blocks and waves), then one walk that places every slot.
+constexpr int OT = 1024, OW = OT / 64;
+
+__device__ __forceinline__ uint64_t same_id_lanes(int id, int bits, bool in) {
+  uint64_t m = __ballot(in);
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t v = __ballot((id >> b) & 1);
+    m &= ((id >> b) & 1) ? v : ~v;
+  }
+  return m;
+}
+
+template <bool PLACE>
+__global__ __launch_bounds__(OT) void order_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, int G,
+                                                   int bits, int nblocks, int32_t* __restrict__ ws,
+                                                   int32_t* __restrict__ count, int32_t* __restrict__ rows,
+                                                   int32_t* __restrict__ order) {
+  __shared__ int32_t at[OW][kOrderMaxGroups];      // a wave's slots per group, then its next position
+  __shared__ int32_t part[OW];
+  __shared__ int32_t s_total;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t lo = (int64_t)blockIdx.x * chunk, hi = min(lo + chunk, n);
+  const int64_t wchunk = chunk / OW;               // chunk is a multiple of OT
+  const int64_t wlo = lo + wave * wchunk, whi = min(wlo + wchunk, hi);
+  for (int g = lane; g < G; g += 64) at[wave][g] = 0;
+  // LDS within a wave is in order; other waves read at[][] only after the barrier
+  for (int64_t i = wlo; i < whi; i += 64) {
+    const int id = i + lane < whi ? ids[i + lane] : -1;
+    if ((uint32_t)id < (uint32_t)G) atomicAdd(&at[wave][id], 1);
+  }
+  __syncthreads();
+  // the block's slots of group tid (G <= OT), as a running sum over its waves
+  int32_t mine = 0, before = 0, all = 0;
+  if (tid < G) {
+    for (int w = 0; w < OW; ++w) {
+      const int32_t v = at[w][tid];
+      at[w][tid] = mine;
+      mine += v;
+    }
+    if (!PLACE) {
+      ws[(int64_t)blockIdx.x * G + tid] = mine;
+    } else if (nblocks > 1) {
+      for (int b = 0; b < nblocks; ++b) {
+        const int32_t v = ws[(int64_t)b * G + tid];
+        before += b < (int)blockIdx.x ? v : 0;
+        all += v;
+      }
+    } else {
+      all = mine;
+    }
+  }
+  if (!PLACE) return;
+  // first position of each group: exclusive scan of `all` over the block
+  int32_t incl = all;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int32_t u = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 63) part[wave] = incl;
+  __syncthreads();
+  int32_t base = 0;
+  for (int w = 0; w < wave; ++w) base += part[w];
+  if (tid == OT - 1) s_total = base + incl;
+  if (tid < G) {
+    const int32_t first = base + incl - all + before;
+    for (int w = 0; w < OW; ++w) at[w][tid] += first;
+    if (blockIdx.x == 0) count[tid] = all;
+  }
+  __syncthreads();
+  for (int64_t i = wlo; i < whi; i += 64) {
+    const int64_t slot = i + lane;
+    const int id = slot < whi ? ids[slot] : -1;
+    const bool in = (uint32_t)id < (uint32_t)G;
+    const uint64_t peers = same_id_lanes(id, bits, in);
+    const int rank = __popcll(peers & ((1ull << lane) - 1));
+    const int32_t pos = in ? at[wave][id] + rank : -1;
+    if (in && rank == 0) at[wave][id] = pos + __popcll(peers);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");      // the next 64 slots read what the leaders wrote
+    if (slot < whi) {
+      if (rows) rows[slot] = pos;
+      if (order && in) order[pos] = (int32_t)slot;
+    }
+  }
+  if (order)
+    for (int64_t i = s_total + (int64_t)blockIdx.x * OT + tid; i < n; i += (int64_t)gridDim.x * OT) order[i] = -1;
+}
+
+static int64_t order_chunk(int64_t n) {
+  const int64_t per = (n + kOrderMaxBlocks - 1) / kOrderMaxBlocks;
+  return std::max<int64_t>((per + OT - 1) / OT, 1) * OT;
+}
+int order_blocks(int64_t n) { return (int)std::max<int64_t>((n + order_chunk(n) - 1) / order_chunk(n), 1); }
+
+hipError_t launch_group_order(const int32_t* ids, int64_t n, int G, int32_t* count, int32_t* rows, int32_t* order,
+                              int32_t* ws, hipStream_t s) {
+  const int nb = order_blocks(n);
+  const int64_t chunk = order_chunk(n);
+  int bits = 0;
+  while ((1 << bits) < G) ++bits;
+  if (nb > 1)
+    hipLaunchKernelGGL(order_kernel<false>, dim3(nb), dim3(OT), 0, s, ids, n, chunk, G, bits, nb, ws, count, rows, order);
+  hipLaunchKernelGGL(order_kernel<true>, dim3(nb), dim3(OT), 0, s, ids, n, chunk, G, bits, nb, ws, count, rows, order);
+  return hipGetLastError();
+}
+
+// ----------------------------------------------------------------------------- moves
+// A thread owns V consecutive elements (16 bytes; one where rows are not 16-byte aligned) of one
+// token's row and its k rows on the other side.
+constexpr int MT = 256;
+
+template <int V>
+struct Chunk {
+  uint16_t e[V];
+};
+template <int V>
+__device__ __forceinline__ Chunk<V> load_chunk(const uint16_t* p) {
+  if constexpr (V == 8) return __builtin_bit_cast(Chunk<8>, *reinterpret_cast<const v4i*>(p));
+  Chunk<V> c;
+  c.e[0] = *p;
+  return c;
+}
+template <int V>
+__device__ __forceinline__ void store_chunk(uint16_t* p, const Chunk<V>& c) {
+  if constexpr (V == 8) *reinterpret_cast<v4i*>(p) = __builtin_bit_cast(v4i, c);
+  else *p = c.e[0];
+}
+
+// Token and column chunk of a thread: whole tokens per block where a row has fewer chunks than
+// threads, else blocks per token.
+struct Place {
+  int64_t t;
+  int c;
+};
+__device__ __forceinline__ Place place_of(int chunks, int64_t T, int64_t block, int tid) {
+  Place p;
+  if (chunks >= MT) {
+    const int per = (chunks + MT - 1) / MT;
+    p.t = block / per;
+    p.c = (int)(block % per) * MT + tid;
+    if (p.c >= chunks || p.t >= T) p.t = -1;
+  } else {
+    const int per = MT / chunks;
+    p.t = block * per + tid / chunks;
+    p.c = tid % chunks;
+    if (tid / chunks >= per || p.t >= T) p.t = -1;
+  }
+  return p;
+}
+static int64_t place_blocks(int chunks, int64_t T) {
+  return chunks >= MT ? T * ((chunks + MT - 1) / MT) : (T + MT / chunks - 1) / (MT / chunks);
+}
+
+constexpr int kRestBlocks = 64;      // blocks that clear the rows behind the last used one
+
+template <int TYPE, int V, bool SCALE>
+__global__ __launch_bounds__(MT) void dispatch_kernel(MoveArgs p, int chunks, int64_t blocks) {
+  using E = Elem<TYPE>;
+  uint16_t* dst = static_cast<uint16_t*>(p.dst);
+  const int64_t M = p.T * p.k;
+  if ((int64_t)blockIdx.x >= blocks) {
+    long long used = 0;
+    for (int e = threadIdx.x & 63; e < p.E; e += 64) used += max(p.count[e], 0);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) used += __shfl_xor(used, o, 64);
+    const Chunk<V> zero = {};
+    for (int64_t r = used + (blockIdx.x - blocks); r < M; r += kRestBlocks)
+      for (int c = threadIdx.x; c < chunks; c += MT) store_chunk<V>(dst + r * p.ld_dst + c * V, zero);
+    return;
+  }
+  const Place w = place_of(chunks, p.T, blockIdx.x, threadIdx.x);
+  if (w.t < 0) return;
+  const Chunk<V> x = load_chunk<V>(static_cast<const uint16_t*>(p.src) + w.t * p.ld_src + w.c * V);
+  for (int j = 0; j < p.k; ++j) {
+    const int32_t r = p.rows[w.t * p.k + j];
+    if ((uint64_t)(int64_t)r >= (uint64_t)M) continue;
+    Chunk<V> y = x;
+    if (SCALE) {
+      const float f = p.probs[w.t * p.k + j];
+#pragma unroll
+      for (int i = 0; i < V; ++i) y.e[i] = E::down(f * E::up(x.e[i]));
+    }
+    store_chunk<V>(dst + r * p.ld_dst + w.c * V, y);
+  }
+}
+
+template <int TYPE, int V, bool SCALE>
+__global__ __launch_bounds__(MT) void combine_kernel(MoveArgs p, int chunks) {
+  using E = Elem<TYPE>;
+  const uint16_t* src = static_cast<const uint16_t*>(p.src);
+  const int64_t M = p.T * p.k;
+  const Place w = place_of(chunks, p.T, blockIdx.x, threadIdx.x);
+  if (w.t < 0) return;
+  float acc[V] = {};
+  for (int j0 = 0; j0 < p.k; j0 += 8) {      // eight rows' loads in flight
+    Chunk<V> x[8];
+    float f[8];
+    bool live[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool in = j0 + j < p.k;
+      const int32_t r = in ? p.rows[w.t * p.k + j0 + j] : -1;
+      live[j] = (uint64_t)(int64_t)r < (uint64_t)M;
+      f[j] = SCALE && in ? p.probs[w.t * p.k + j0 + j] : 1.0f;
+      if (live[j]) x[j] = load_chunk<V>(src + r * p.ld_src + w.c * V);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (live[j])
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(f[j], E::up(x[j].e[i]), acc[i]);
+  }
+  Chunk<V> y;
+#pragma unroll
+  for (int i = 0; i < V; ++i) y.e[i] = E::down(acc[i]);
+  store_chunk<V>(static_cast<uint16_t*>(p.dst) + w.t * p.ld_dst + w.c * V, y);
+}
+
+// One block per token: the products of its gradient with its k rows, in fp32, summed by thread, by
+// wave and over the waves in order.
+template <int TYPE, int V>
+__global__ __launch_bounds__(MT) void combine_dprobs_kernel(MoveArgs p, int chunks) {
+  using E = Elem<TYPE>;
+  __shared__ float red[MT / 64][8];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t t = blockIdx.x, M = p.T * p.k;
+  const uint16_t* dy = static_cast<const uint16_t*>(p.src) + t * p.ld_src;
+  const uint16_t* v = static_cast<const uint16_t*>(p.src2);
+  for (int j0 = 0; j0 < p.k; j0 += 8) {
+    float acc[8] = {};
+    int32_t r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      r[j] = j0 + j < p.k ? p.rows[t * p.k + j0 + j] : -1;
+      if ((uint64_t)(int64_t)r[j] >= (uint64_t)M) r[j] = -1;
+    }
+    for (int c = tid; c < chunks; c += MT) {
+      const Chunk<V> d = load_chunk<V>(dy + c * V);
+      Chunk<V> x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (r[j] >= 0) x[j] = load_chunk<V>(v + r[j] * p.ld_src2 + c * V);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (r[j] >= 0)
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[j] = fmaf(E::up(d.e[i]), E::up(x[j].e[i]), acc[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) acc[j] += __shfl_xor(acc[j], o, 64);
+      if (lane == 0) red[wave][j] = acc[j];
+    }
+    __syncthreads();
+    if (tid < 8 && j0 + tid < p.k) {
+      float s = 0.0f;
+      for (int w = 0; w < MT / 64; ++w) s += red[w][tid];
+      p.dprobs[t * p.k + j0 + tid] = s;
+    }
+    __syncthreads();
+  }
+}
+
+static bool rows16(const void* p, int64_t ld, int H) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ((ld | H) & 7) == 0;
+}
+static hipError_t grid_ok(int64_t blocks) { return blocks <= 0x7FFFFFFF ? hipSuccess : hipErrorInvalidValue; }
+
+template <int TYPE, int V>
+static hipError_t run_dispatch(const MoveArgs& p, hipStream_t s) {
+  const int chunks = (p.H + V - 1) / V;
+  const int64_t blocks = place_blocks(chunks, p.T), grid = blocks + (p.zero_rest ? kRestBlocks : 0);
+  if (hipError_t e = grid_ok(grid)) return e;
+  if (p.probs) hipLaunchKernelGGL((dispatch_kernel<TYPE, V, true>), dim3((uint32_t)grid), dim3(MT), 0, s, p, chunks, blocks);
+  else hipLaunchKernelGGL((dispatch_kernel<TYPE, V, false>), dim3((uint32_t)grid), dim3(MT), 0, s, p, chunks, blocks);
+  return hipGetLastError();
+}
+template <int TYPE, int V>
+static hipError_t run_combine(const MoveArgs& p, hipStream_t s) {
+  const int chunks = (p.H + V - 1) / V;
+  const int64_t grid = place_blocks(chunks, p.T);
+  if (hipError_t e = grid_ok(grid)) return e;
+  if (p.probs) hipLaunchKernelGGL((combine_kernel<TYPE, V, true>), dim3((uint32_t)grid), dim3(MT), 0, s, p, chunks);
+  else hipLaunchKernelGGL((combine_kernel<TYPE, V, false>), dim3((uint32_t)grid), dim3(MT), 0, s, p, chunks);
+  return hipGetLastError();
+}
+template <int TYPE, int V>
+static hipError_t run_dprobs(const MoveArgs& p, hipStream_t s) {
+  hipLaunchKernelGGL((combine_dprobs_kernel<TYPE, V>), dim3((uint32_t)p.T), dim3(MT), 0, s, p, (p.H + V - 1) / V);
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch(const MoveArgs& p, hipStream_t s) {
+  const bool v = rows16(p.src, p.ld_src, p.H) && rows16(p.dst, p.ld_dst, p.H);
+  if (p.type == MM_BF16) return v ? run_dispatch<MM_BF16, 8>(p, s) : run_dispatch<MM_BF16, 1>(p, s);
+  return v ? run_dispatch<MM_FP16, 8>(p, s) : run_dispatch<MM_FP16, 1>(p, s);
+}
+hipError_t launch_combine(const MoveArgs& p, hipStream_t s) {
+  const bool v = rows16(p.src, p.ld_src, p.H) && rows16(p.dst, p.ld_dst, p.H);
+  if (p.type == MM_BF16) return v ? run_combine<MM_BF16, 8>(p, s) : run_combine<MM_BF16, 1>(p, s);
+  return v ? run_combine<MM_FP16, 8>(p, s) : run_combine<MM_FP16, 1>(p, s);
+}
+hipError_t launch_combine_dprobs(const MoveArgs& p, hipStream_t s) {
+  const bool v = rows16(p.src, p.ld_src, p.H) && rows16(p.src2, p.ld_src2, p.H);
+  if (p.type == MM_BF16) return v ? run_dprobs<MM_BF16, 8>(p, s) : run_dprobs<MM_BF16, 1>(p, s);
+  return v ? run_dprobs<MM_FP16, 8>(p, s) : run_dprobs<MM_FP16, 1>(p, s);
+}
+
+}  // namespace gmlp

@@ -189,4 +189,37 @@ struct MmArgs {
 };
 hipError_t launch_grouped_matmul(const MmArgs& a, hipStream_t s);
 
+// ----------------------------------------------------------------------------- group order
+// Stable counting sort of ids [n] into G groups (ids outside [0, G) belong to none).
+//   rows [n]   the position of slot i among all slots in group order, -1 outside (may be null)
+//   order [n]  the slot at each position, -1 behind the last (may be null)
+//   count [G]  slots per group
+constexpr int kOrderMaxGroups = 1024;
+constexpr int kOrderMaxBlocks = 256;
+int order_blocks(int64_t n);          // 1: no workspace; else order_blocks(n) x G int32
+hipError_t launch_group_order(const int32_t* ids, int64_t n, int G, int32_t* count, int32_t* rows, int32_t* order,
+                              int32_t* ws, hipStream_t s);
+
+// ----------------------------------------------------------------------------- expert dispatch
+// x, y, dy are by token [T, H], xg, v, dv by row in expert order [T k, H]; rows [T, k] the row of each
+// slot (one outside [0, T k) is dropped).  Strides in elements.
+struct MoveArgs {
+  int type;
+  const void* src;
+  const void* src2;
+  void* dst;
+  int64_t ld_src, ld_src2, ld_dst;
+  int64_t T;
+  int H, k;
+  const int32_t* rows;
+  const float* probs;        // [T, k] or null (1)
+  float* dprobs;
+  const int32_t* count;      // [E]: rows of dst in use (for zero_rest)
+  int E;
+  int zero_rest;
+};
+hipError_t launch_dispatch(const MoveArgs& a, hipStream_t s);            // dst[rows[t, j]] = probs src[t]
+hipError_t launch_combine(const MoveArgs& a, hipStream_t s);             // dst[t] = sum_j probs src[rows[t, j]]
+hipError_t launch_combine_dprobs(const MoveArgs& a, hipStream_t s);      // dprobs[t, j] = <src[t], src2[rows[t, j]]>
+
 }  // namespace gmlp

@@ -102,3 +102,90 @@ extern "C" gmlp_status gmlp_grouped_matmul(const gmlp_grouped_matmul_args* p, hi
   a.flags = static_cast<uint32_t*>(p->ws);
   return launched(launch_grouped_matmul(a, stream), "grouped matmul");
 }
+
+// ----------------------------------------------------------------------------- expert dispatch
+namespace {
+gmlp_status check_order(int64_t n, int32_t E) {
+  if (E < 1 || E > kOrderMaxGroups)
+    return set_error(GMLP_UNSUPPORTED, "dims: 1 to %d experts are supported, got %d", kOrderMaxGroups, E);
+  if (n < 0 || n >= kMaxRows) return set_error(GMLP_UNSUPPORTED, "dims: %lld slots are out of range", (long long)n);
+  return GMLP_OK;
+}
+size_t order_ws(int64_t n, int32_t E) {
+  const int b = order_blocks(n);
+  return b > 1 ? (size_t)b * E * sizeof(int32_t) : 0;
+}
+
+enum MoveKind { MOVE_DISPATCH, MOVE_COMBINE, MOVE_DPROBS };
+gmlp_status move(const gmlp_move_args* p, MoveKind kind, hipStream_t stream) {
+  if (!p) return set_error(GMLP_INVALID_ARG, "null pointer argument");
+  gmlp_status st = check_dtype(p->dtype);
+  if (st != GMLP_OK) return st;
+  if (p->T < 0 || p->k < 1 || p->T * (double)p->k >= (double)kMaxRows)
+    return set_error(GMLP_UNSUPPORTED, "dims: %lld tokens of %d slots are out of range", (long long)p->T, p->k);
+  if (p->H < 1 || p->H >= kMaxLd) return set_error(GMLP_UNSUPPORTED, "dims: H must be in [1, 2^20), got %lld", (long long)p->H);
+  if (p->T == 0) return fine();
+  const bool rest = kind == MOVE_DISPATCH && p->zero_rest;
+  if (!p->src || !p->rows || (kind == MOVE_DPROBS ? !p->src2 || !p->dprobs : !p->dst) || (rest && !p->m_splits))
+    return set_error(GMLP_INVALID_ARG, "null pointer argument");
+  if (rest && p->E < 1) return set_error(GMLP_INVALID_ARG, "dims: number of experts must be >= 1, got %d", p->E);
+  if (!aligned2(p->src) || !aligned2(p->src2) || !aligned2(p->dst) || !aligned4(p->rows) || !aligned4(p->probs) ||
+      !aligned4(p->dprobs) || !aligned4(p->m_splits))
+    return set_error(GMLP_INVALID_ARG, "a tensor is not aligned to its elements");
+  if (p->ld_src < p->H || (kind == MOVE_DPROBS ? p->ld_src2 : p->ld_dst) < p->H)
+    return set_error(GMLP_INVALID_ARG, "strides: row strides must be at least the row's length");
+  MoveArgs a{};
+  a.type = p->dtype;
+  a.src = p->src;
+  a.src2 = p->src2;
+  a.dst = p->dst;
+  a.ld_src = p->ld_src;
+  a.ld_src2 = p->ld_src2;
+  a.ld_dst = p->ld_dst;
+  a.T = p->T;
+  a.H = (int)p->H;
+  a.k = p->k;
+  a.rows = p->rows;
+  a.probs = p->probs;
+  a.dprobs = p->dprobs;
+  a.count = p->m_splits;
+  a.E = p->E;
+  a.zero_rest = rest;
+  if (kind == MOVE_DISPATCH) return launched(launch_dispatch(a, stream), "dispatch");
+  if (kind == MOVE_COMBINE) return launched(launch_combine(a, stream), "combine");
+  return launched(launch_combine_dprobs(a, stream), "combine dprobs");
+}
+}  // namespace
+
+extern "C" gmlp_status gmlp_dispatch_plan_ws_bytes(int64_t n, int32_t E, size_t* bytes) {
+  if (!bytes) return set_error(GMLP_INVALID_ARG, "null pointer argument");
+  const gmlp_status st = check_order(n, E);
+  if (st != GMLP_OK) return st;
+  *bytes = order_ws(n, E);
+  return fine();
+}
+
+extern "C" gmlp_status gmlp_dispatch_plan(const int32_t* experts, int64_t n, int32_t E, int32_t* m_splits,
+                                          int32_t* rows, int32_t* order, void* ws, size_t ws_bytes,
+                                          hipStream_t stream) {
+  const gmlp_status st = check_order(n, E);
+  if (st != GMLP_OK) return st;
+  if (!m_splits || (n > 0 && (!experts || !rows))) return set_error(GMLP_INVALID_ARG, "null pointer argument");
+  if (!aligned4(experts) || !aligned4(m_splits) || !aligned4(rows) || !aligned4(order))
+    return set_error(GMLP_INVALID_ARG, "a tensor is not aligned to its elements");
+  const size_t need = order_ws(n, E);
+  if (need && (!ws || ws_bytes < need || !aligned16(ws)))
+    return set_error(GMLP_WORKSPACE, "workspace: %zu bytes, 16-byte aligned, are needed", need);
+  return launched(launch_group_order(experts, n, E, m_splits, rows, order, static_cast<int32_t*>(ws), stream),
+                  "dispatch plan");
+}
+
+extern "C" gmlp_status gmlp_dispatch(const gmlp_move_args* args, hipStream_t stream) {
+  return move(args, MOVE_DISPATCH, stream);
+}
+extern "C" gmlp_status gmlp_combine(const gmlp_move_args* args, hipStream_t stream) {
+  return move(args, MOVE_COMBINE, stream);
+}
+extern "C" gmlp_status gmlp_combine_dprobs(const gmlp_move_args* args, hipStream_t stream) {
+  return move(args, MOVE_DPROBS, stream);
+}

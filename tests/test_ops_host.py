@@ -70,3 +70,69 @@ def test_grouped_matmul_null_arguments():
     assert g.lib().gmlp_grouped_matmul(None, None) == 1
     assert g.lib().gmlp_grouped_matmul_ws_bytes(0, 1, 1, 1, 1, None) == 1
     assert g.grouped_matmul_ws_bytes(g.GEMM_WGRAD, 128, 65536, 4096, 7168) >= 256
+
+
+def test_dispatch_binding_refusals():
+    with pytest.raises(TypeError, match="experts"):
+        g.dispatch_plan(torch.zeros((4, 2), dtype=torch.int64), 8)
+    with pytest.raises(TypeError, match="experts"):
+        g.dispatch_plan(torch.zeros(4, dtype=torch.int32), 8)
+    with pytest.raises(g.GmlpError, match="1 to 1024 experts"):
+        g.dispatch_plan(torch.zeros((4, 2), dtype=torch.int32), 1025)
+    with pytest.raises(g.GmlpError, match="1 to 1024 experts"):
+        g.dispatch_plan(torch.zeros((4, 2), dtype=torch.int32), 0)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        g.dispatch_plan(torch.zeros((4, 2), dtype=torch.int32), 8)
+    plan = g.DispatchPlan(torch.zeros(3, dtype=torch.int32), torch.zeros((4, 2), dtype=torch.int32))
+    with pytest.raises(ValueError, match="x: 4 rows"):
+        g.dispatch_forward(_t(5, 8), plan)
+    with pytest.raises(ValueError, match="v: 8 rows"):
+        g.combine_forward(_t(4, 8), plan)
+    with pytest.raises(TypeError, match="probs"):
+        g.combine_forward(_t(8, 8), plan, torch.zeros(4, 2, dtype=torch.float64))
+    with pytest.raises(TypeError, match="probs"):
+        g.combine_forward(_t(8, 8), plan, torch.zeros(8))
+    with pytest.raises(TypeError, match="bf16 or fp16"):
+        g.dispatch_forward(torch.zeros(4, 8), plan)
+    with pytest.raises(ValueError, match="out"):
+        g.dispatch_forward(_t(4, 8), plan, out=_t(8, 9))
+    with pytest.raises(ValueError, match="GPU tensor"):
+        g.dispatch_forward(_t(4, 8), plan)
+    with pytest.raises(TypeError, match="plan"):
+        g.dispatch_forward(_t(4, 8), None)
+
+
+def _mv(fn="gmlp_dispatch", **kw):
+    a = g.MoveArgs()
+    vals = dict(dtype=0, zero_rest=0, src=256, ld_src=8, src2=256, ld_src2=8, dst=256, ld_dst=8, T=4, H=8, k=2, E=3, rows=256,
+                m_splits=256, probs=256, dprobs=256)
+    vals.update(kw)
+    for k, v in vals.items():
+        setattr(a, k, v)
+    return getattr(g.lib(), fn)(ctypes.byref(a), None)
+
+
+@pytest.mark.parametrize("kw,status,why", [
+    (dict(dtype=5), 2, "dtype"), (dict(T=-1), 2, "tokens"), (dict(k=0), 2, "tokens"), (dict(T=1 << 30, k=1), 2, "tokens"),
+    (dict(H=0), 2, "H"), (dict(src=None), 1, "null"), (dict(dst=None), 1, "null"), (dict(rows=None), 1, "null"),
+    (dict(zero_rest=1, m_splits=None), 1, "null"), (dict(zero_rest=1, E=0), 1, "experts"), (dict(src=257), 1, "aligned"),
+    (dict(probs=258), 1, "aligned"), (dict(ld_src=7), 1, "strides"), (dict(ld_dst=7), 1, "strides"),
+    (dict(fn="gmlp_combine", dst=None), 1, "null"), (dict(fn="gmlp_combine_dprobs", dprobs=None), 1, "null"),
+    (dict(fn="gmlp_combine_dprobs", src2=None), 1, "null"), (dict(fn="gmlp_combine_dprobs", ld_src2=7), 1, "strides"),
+])
+def test_move_abi_refusals(kw, status, why):
+    assert _mv(**kw) == status and why in g.last_error(), g.last_error()
+
+
+def test_plan_abi_refusals():
+    L = g.lib()
+    p = ctypes.c_void_p(256)
+    n = ctypes.c_size_t(0)
+    assert L.gmlp_dispatch(None, None) == 1
+    assert L.gmlp_dispatch_plan_ws_bytes(8, 3, None) == 1
+    assert L.gmlp_dispatch_plan_ws_bytes(1 << 30, 3, ctypes.byref(n)) == 2
+    assert L.gmlp_dispatch_plan_ws_bytes(65536, 128, ctypes.byref(n)) == 0 and n.value == 64 * 128 * 4
+    assert L.gmlp_dispatch_plan(p, 65536, 128, p, p, None, None, 0, None) == 3
+    assert L.gmlp_dispatch_plan(p, 8, 3, None, p, None, None, 0, None) == 1
+    assert L.gmlp_dispatch_plan(None, 8, 3, p, p, None, None, 0, None) == 1
+    assert L.gmlp_dispatch_plan(ctypes.c_void_p(255), 8, 3, p, p, None, None, 0, None) == 1
