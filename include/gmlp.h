@@ -425,6 +425,65 @@ gmlp_status gmlp_dispatch(const gmlp_move_args* args, hipStream_t stream);
 gmlp_status gmlp_combine(const gmlp_move_args* args, hipStream_t stream);
 gmlp_status gmlp_combine_dprobs(const gmlp_move_args* args, hipStream_t stream);
 
+/* ------------------------------------------------------------------ low-rank adapters */
+
+/* Low-rank adapters of many requests at once beside a shared projection (bf16 or fp16): row m takes
+ * the adapter l = ids[m] (device int32 [M]; outside [0, L): none)
+ *   u[m] = a[l] x[m]                        fp32 [R]
+ *   y[m] = base[m] + scales[l] b[l] u[m]    rounded once; y = base for a row without an adapter
+ * and with dy the gradient for y
+ *   du[m] = scales[l] b[l]^T dy[m]          fp32 [R]
+ *   dx[m] = dx_add[m] + a[l]^T du[m]        da[l] = sum du[m] x[m]^T     db[l] = scales[l] sum dy[m] u[m]^T
+ * with the sums over the adapter's rows (an adapter without rows gets zeros).  u and du stay in
+ * fp32; as factors of the matrix products they enter as the sum of two 16-bit values, which keeps
+ * at least 16 of their bits.  a [L, R, K], b [L, N, R] with row strides lda, ldb and adapter
+ * strides a_stride, b_stride; x [M, K], base, y, dy [M, N], dx, dx_add [M, K] with row strides; the
+ * last dimension contiguous everywhere, da, db contiguous; strides in elements.  base and dx_add
+ * may be NULL (zeros) or the output itself; other overlaps are not allowed.  scales: device fp32
+ * [L], or NULL for 1.  1 <= R <= 128, 1 <= L <= 1023.
+ * The forward leaves in ctx the rows' order by adapter and u; the backward of the same M, K, N, R, L
+ * reads it (keep it untouched in between).  dx, da, db: NULL where not needed (x is read for da). */
+typedef struct {
+  const void* a; int64_t lda; int64_t a_stride;
+  const void* b; int64_t ldb; int64_t b_stride;
+  const float* scales;
+} gmlp_lora_weights;
+typedef struct {
+  size_t ctx_bytes;           /* forward to backward */
+  size_t fwd_ws_bytes;        /* scratch of one forward (0: ws may be NULL) */
+  size_t bwd_ws_bytes;        /* scratch of one backward */
+} gmlp_lora_sizes;
+typedef struct {
+  int32_t dtype;              /* gmlp_dtype */
+  int32_t R, L;
+  int64_t M, K, N;
+  const void* base; int64_t ldbase;
+  const void* x; int64_t ldx;
+  gmlp_lora_weights w;
+  const int32_t* ids;
+  void* y; int64_t ldy;
+  void* ctx; size_t ctx_bytes;
+  void* ws; size_t ws_bytes;
+} gmlp_lora_fwd_args;
+typedef struct {
+  int32_t dtype;
+  int32_t R, L;
+  int64_t M, K, N;
+  const void* dy; int64_t lddy;
+  const void* x; int64_t ldx;
+  gmlp_lora_weights w;
+  const void* dx_add; int64_t lddx_add;
+  void* dx; int64_t lddx;
+  void* da;
+  void* db;
+  const void* ctx; size_t ctx_bytes;
+  void* ws; size_t ws_bytes;
+} gmlp_lora_bwd_args;
+
+gmlp_status gmlp_lora_query_sizes(int64_t M, int64_t K, int64_t N, int32_t R, int32_t L, gmlp_lora_sizes* out);
+gmlp_status gmlp_lora_forward(const gmlp_lora_fwd_args* args, hipStream_t stream);
+gmlp_status gmlp_lora_backward(const gmlp_lora_bwd_args* args, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

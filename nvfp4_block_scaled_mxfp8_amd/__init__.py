@@ -714,3 +714,5 @@ from .matmul import (OUT_SAME, GroupedMatmulArgs, GroupedMatmulFunction, grouped
 from .expert_dispatch import (CombineFunction, DispatchFunction, DispatchPlan, MoveArgs, combine,  # noqa: E402
                        combine_backward, combine_forward, dispatch, dispatch_backward, dispatch_forward,
                        dispatch_plan)
+from .adapters import (LoraBwdArgs, LoraContext, LoraFunction, LoraFwdArgs, LoraSizes, LoraWeights, lora,  # noqa: E402
+                       lora_backward, lora_forward, lora_query_sizes)

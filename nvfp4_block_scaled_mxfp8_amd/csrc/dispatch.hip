@@ -28,7 +28,8 @@ __device__ __forceinline__ uint64_t same_id_lanes(int id, int bits, bool in) {
 
 template <bool PLACE>
 __global__ __launch_bounds__(OT) void order_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, int G,
-                                                   int bits, int nblocks, int32_t* __restrict__ ws,
+                                                   int bits, int nblocks, bool rest,
+                                                   int32_t* __restrict__ ws,
                                                    int32_t* __restrict__ count, int32_t* __restrict__ rows,
                                                    int32_t* __restrict__ order) {
   __shared__ int32_t at[OW][kOrderMaxGroups];      // a wave's slots per group, then its next position
@@ -41,7 +42,8 @@ __global__ __launch_bounds__(OT) void order_kernel(const int32_t* __restrict__ i
   for (int g = lane; g < G; g += 64) at[wave][g] = 0;
   // LDS within a wave is in order; other waves read at[][] only after the barrier
   for (int64_t i = wlo; i < whi; i += 64) {
-    const int id = i + lane < whi ? ids[i + lane] : -1;
+    int id = i + lane < whi ? ids[i + lane] : -1;
+    if (rest && i + lane < whi && (uint32_t)id >= (uint32_t)G) id = G - 1;
     if ((uint32_t)id < (uint32_t)G) atomicAdd(&at[wave][id], 1);
   }
   __syncthreads();
@@ -86,7 +88,8 @@ __global__ __launch_bounds__(OT) void order_kernel(const int32_t* __restrict__ i
   __syncthreads();
   for (int64_t i = wlo; i < whi; i += 64) {
     const int64_t slot = i + lane;
-    const int id = slot < whi ? ids[slot] : -1;
+    int id = slot < whi ? ids[slot] : -1;
+    if (rest && slot < whi && (uint32_t)id >= (uint32_t)G) id = G - 1;
     const bool in = (uint32_t)id < (uint32_t)G;
     const uint64_t peers = same_id_lanes(id, bits, in);
     const int rank = __popcll(peers & ((1ull << lane) - 1));
@@ -108,15 +111,15 @@ static int64_t order_chunk(int64_t n) {
 }
 int order_blocks(int64_t n) { return (int)std::max<int64_t>((n + order_chunk(n) - 1) / order_chunk(n), 1); }
 
-hipError_t launch_group_order(const int32_t* ids, int64_t n, int G, int32_t* count, int32_t* rows, int32_t* order,
-                              int32_t* ws, hipStream_t s) {
+hipError_t launch_group_order(const int32_t* ids, int64_t n, int G, bool rest, int32_t* count, int32_t* rows,
+                              int32_t* order, int32_t* ws, hipStream_t s) {
   const int nb = order_blocks(n);
   const int64_t chunk = order_chunk(n);
   int bits = 0;
   while ((1 << bits) < G) ++bits;
   if (nb > 1)
-    hipLaunchKernelGGL(order_kernel<false>, dim3(nb), dim3(OT), 0, s, ids, n, chunk, G, bits, nb, ws, count, rows, order);
-  hipLaunchKernelGGL(order_kernel<true>, dim3(nb), dim3(OT), 0, s, ids, n, chunk, G, bits, nb, ws, count, rows, order);
+    hipLaunchKernelGGL(order_kernel<false>, dim3(nb), dim3(OT), 0, s, ids, n, chunk, G, bits, nb, rest, ws, count, rows, order);
+  hipLaunchKernelGGL(order_kernel<true>, dim3(nb), dim3(OT), 0, s, ids, n, chunk, G, bits, nb, rest, ws, count, rows, order);
   return hipGetLastError();
 }
 

@@ -197,8 +197,67 @@ hipError_t launch_grouped_matmul(const MmArgs& a, hipStream_t s);
 constexpr int kOrderMaxGroups = 1024;
 constexpr int kOrderMaxBlocks = 256;
 int order_blocks(int64_t n);          // 1: no workspace; else order_blocks(n) x G int32
-hipError_t launch_group_order(const int32_t* ids, int64_t n, int G, int32_t* count, int32_t* rows, int32_t* order,
-                              int32_t* ws, hipStream_t s);
+// rest: ids outside [0, G - 1) count as group G - 1 (so every slot has a position).
+hipError_t launch_group_order(const int32_t* ids, int64_t n, int G, bool rest, int32_t* count, int32_t* rows,
+                              int32_t* order, int32_t* ws, hipStream_t s);
+
+// ----------------------------------------------------------------------------- low-rank adapters
+// Rows are taken in the order of their adapter: position p holds row order[p], count [L + 1] the
+// positions per adapter and (last) of the rows without one.  Strides in elements.
+constexpr int kLoraMaxRank = 128;
+constexpr int kLoraMaxAdapters = kOrderMaxGroups - 1;
+struct LoraRows {
+  const int32_t* count;
+  const int32_t* order;
+  int64_t M;
+  int L;
+};
+// v[z][p][r] = scale sum over the z-th part of c of X[row p, c] W_l[r, c]; W [L, R, C] (z < parts)
+struct LoraShrink {
+  int type, R;
+  LoraRows rows;
+  const void* x; int64_t ldx;
+  const void* w; int64_t ldw, w_stride;
+  int64_t C;
+  const float* scales;      // [L] or null (1)
+  float* v;
+  int parts;
+};
+hipError_t launch_lora_shrink(const LoraShrink& a, hipStream_t s);
+int lora_shrink_parts(int64_t M, int64_t C, int R, int L);
+// Y[row p, c] = base[row p, c] + scale sum_r (sum_z v[z][p][r]) W_l[c, r]; W [L, C, R]; base null: 0
+struct LoraExpand {
+  int type, R;
+  LoraRows rows;
+  const float* v;
+  int parts;
+  const void* w; int64_t ldw, w_stride;
+  int64_t C;
+  const float* scales;
+  const void* base; int64_t ldbase;
+  void* y; int64_t ldy;
+};
+hipError_t launch_lora_expand(const LoraExpand& a, hipStream_t s);
+// out_l = scale sum over l's rows of v[p, r] X[row p, c], as [R, C] (transposed: [C, R]), zero for an
+// adapter without rows; part: lora_outer_part_floats floats of scratch.
+struct LoraOuter {
+  int type, R;
+  LoraRows rows;
+  const float* v;
+  int parts;
+  const void* x; int64_t ldx;
+  int64_t C;
+  const float* scales;
+  void* out;
+  bool transposed;
+  float* part;
+};
+hipError_t launch_lora_outer(const LoraOuter& a, hipStream_t s);
+int64_t lora_outer_part_floats(int64_t M, int64_t C, int R, int L);
+hipError_t launch_zero16(void* p, int64_t n, hipStream_t s);
+// dst[l][c][r] = src[l][r][c] for adapters with rows; src [L, R, C], dst rows of ldd elements
+hipError_t launch_lora_transpose(const void* src, int64_t lds, int64_t src_stride, int64_t R, int64_t C, void* dst,
+                                 int64_t ldd, int64_t dst_stride, const int32_t* count, int L, hipStream_t s);
 
 // ----------------------------------------------------------------------------- expert dispatch
 // x, y, dy are by token [T, H], xg, v, dv by row in expert order [T k, H]; rows [T, k] the row of each

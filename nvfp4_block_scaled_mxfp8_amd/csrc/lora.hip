@@ -1,0 +1,552 @@
+// Low-rank adapters of many requests: v = W_l x (shrink), y = base + W_l v (expand), the adapters'
+// gradients sum_m v_m x_m^T (outer), each over rows taken in the order of their adapter.
+//
+// All three are bound by the read (and write) of the [M, C] tensors: 2 R flops per element read.
+// Rows of one adapter are consecutive positions; a workgroup takes a tile of positions of one
+// adapter and gathers their rows through `order`, so requests need not be sorted or equal in
+// length.  The rank-sized factor v stays in fp32 in memory and enters the 16-bit matrix products
+// as hi + lo, two values of the operands' type (at least 16 of its bits): one
+// V_MFMA_F32_16X16X32 takes 16 ranks, hi in its lower and lo in its upper sixteen contraction
+// steps, so the second half costs no further instruction where a rank tile is 16 wide.
+#include "mm_common.h"
+
+#include <algorithm>
+
+namespace gmlp {
+
+// ----------------------------------------------------------------------------- loads
+// Eight consecutive elements from p, of which `valid` exist.
+template <bool VEC>
+__device__ __forceinline__ v4i load8(const uint16_t* p, int valid) {
+  if constexpr (VEC) {
+    return valid > 0 ? *reinterpret_cast<const v4i*>(p) : v4i{0, 0, 0, 0};
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = 2 * i < valid ? p[2 * i] : 0u, hi = 2 * i + 1 < valid ? p[2 * i + 1] : 0u;
+      w[i] = lo | (hi << 16);
+    }
+    return v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+  }
+}
+
+// v as a factor of the 16-bit products: hi = T(v), lo = T(v - hi).
+template <int TYPE>
+__device__ __forceinline__ v4i split8(const float* v, bool lo) {
+  using E = Elem<TYPE>;
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float f[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float x = v[2 * i + e], h = E::up(E::down(x));
+      f[e] = !lo ? x : (__builtin_isfinite(h) ? x - h : 0.0f);
+    }
+    w[i] = E::down2(f[0], f[1]);
+  }
+  return v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+}
+// A power of two that brings a largest magnitude m to [2^14, 2^15) (fp16 operands: hi then never
+// overflows and lo resolves 2^-39 of m), 1 where m is zero or not finite.  Exponents are kept where
+// the factor and its inverse are normal numbers.
+__device__ __forceinline__ float fp16_scale(float m) {
+  const uint32_t ex = __float_as_uint(m) >> 23;
+  if (ex == 0 || ex >= 255) return 1.0f;
+  return __uint_as_float(min(253u, max(1u, 268u - min(ex, 267u))) << 23);
+}
+__device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u - (__float_as_uint(s) >> 23)) << 23); }
+
+// ----------------------------------------------------------------------------- shrink
+// RB x 16 positions by RT x 16 ranks per workgroup, the contraction in blocks of 32 SPB split over
+// the four waves (and over gridDim.y parts), fragments straight from memory with the next block's
+// loads in flight.  Waves are joined through LDS in order.
+template <int TYPE, bool VEC, int RB, int RT>
+__global__ __launch_bounds__(256) void lora_shrink_kernel(LoraShrink p) {
+  using E = Elem<TYPE>;
+  constexpr int SPB = RB + RT <= 3 ? 4 : RB + RT <= 6 ? 2 : 1;
+  constexpr int LD = RT * 16 + 4;
+  __shared__ __align__(16) float red[RB * 16 * LD];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const RowTile rt = find_row_tile(p.rows.count, p.rows.L, (uint32_t)p.rows.M, RB * 16, 1, false, blockIdx.x, lane);
+  if (rt.g < 0) return;
+  const int64_t pos0 = (int64_t)rt.row0 + rt.t * (RB * 16);
+  const int valid = min((int)(rt.m - rt.t * (RB * 16)), RB * 16);
+  const int q = lane & 15, j = lane >> 4;
+  const uint16_t* xr[RB];
+  const uint16_t* wr[RT];
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+    xr[b] = static_cast<const uint16_t*>(p.x) + p.rows.order[pos0 + min(16 * b + q, valid - 1)] * p.ldx + 8 * j;
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+    wr[t] = static_cast<const uint16_t*>(p.w) + rt.g * p.w_stride + min(16 * t + q, p.R - 1) * p.ldw + 8 * j;
+  v4f acc[RB][RT];
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[b][t] = v4f{0, 0, 0, 0};
+  const int64_t step = (int64_t)32 * SPB;
+  const int64_t nblk = (p.C + step - 1) / step;
+  v4i xf[2][SPB][RB], wf[2][SPB][RT];
+  auto fetch = [&](int64_t blk, int s) {
+    const int64_t c0 = blk * step;
+#pragma unroll
+    for (int k = 0; k < SPB; ++k) {
+      const int64_t c = c0 + 32 * k;
+      const int left = (int)min(p.C - c - 8 * j, (int64_t)8);
+#pragma unroll
+      for (int b = 0; b < RB; ++b) xf[s][k][b] = load8<VEC>(xr[b] + c, left);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) wf[s][k][t] = load8<VEC>(wr[t] + c, left);
+    }
+  };
+  auto mul = [&](int s) {
+#pragma unroll
+    for (int k = 0; k < SPB; ++k)
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[b][t] = E::mma16(wf[s][k][t], xf[s][k][b], acc[b][t]);
+  };
+  const int64_t stride = 4 * (int64_t)gridDim.y;
+  int64_t blk = (int64_t)blockIdx.y * 4 + wave;
+  if (blk < nblk) {
+    fetch(blk, 0);
+    while (true) {
+      if (blk + stride < nblk) fetch(blk + stride, 1);
+      mul(0);
+      blk += stride;
+      if (blk >= nblk) break;
+      if (blk + stride < nblk) fetch(blk + stride, 0);
+      mul(1);
+      blk += stride;
+      if (blk >= nblk) break;
+    }
+  }
+  // lane: position 16 b + q, ranks 16 t + 4 j + i
+  for (int w = 0; w < 4; ++w) {
+    if (wave == w) {
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          v4f* d = reinterpret_cast<v4f*>(red + (16 * b + q) * LD + 16 * t + 4 * j);
+          *d = w == 0 ? acc[b][t] : *d + acc[b][t];
+        }
+    }
+    __syncthreads();
+  }
+  const float sc = p.scales ? p.scales[rt.g] : 1.0f;
+  float* out = p.v + ((int64_t)blockIdx.y * p.rows.M + pos0) * p.R;
+  for (int i = tid; i < valid * p.R; i += 256) out[i] = sc * red[i / p.R * LD + i % p.R];
+}
+
+static int64_t tiles_bound(int64_t M, int groups, int64_t h) { return (M + (h - 1) * std::min<int64_t>(groups, M)) / h; }
+
+// Rows of a shrink tile: 16 while that leaves the device unfilled, else 32 (64 above 32 ranks, where
+// W would be read as often as X).
+static int shrink_rb(int64_t M, int R, int L) {
+  if (tiles_bound(M, L, 16) < 512) return 1;
+  return R > 32 ? 4 : 2;
+}
+// Parts of the contraction: enough workgroups for the device, none shorter than one block per wave.
+int lora_shrink_parts(int64_t M, int64_t C, int R, int L) {
+  const int64_t tiles = std::max<int64_t>(tiles_bound(M, L, 16 * shrink_rb(M, R, L)), 1);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, (C + 511) / 512, 16}));
+}
+
+template <int TYPE, bool VEC, int RB, int RT>
+static hipError_t run_shrink(const LoraShrink& p, hipStream_t s) {
+  const int64_t tiles = tiles_bound(p.rows.M, p.rows.L, 16 * RB);
+  hipLaunchKernelGGL((lora_shrink_kernel<TYPE, VEC, RB, RT>), dim3((uint32_t)tiles, p.parts), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+template <int TYPE, bool VEC, int RB>
+static hipError_t shrink_rank(const LoraShrink& p, hipStream_t s) {
+  if (p.R <= 16) return run_shrink<TYPE, VEC, RB, 1>(p, s);
+  if (p.R <= 32) return run_shrink<TYPE, VEC, RB, 2>(p, s);
+  if (p.R <= 64) return run_shrink<TYPE, VEC, RB, 4>(p, s);
+  return run_shrink<TYPE, VEC, RB, 8>(p, s);
+}
+template <int TYPE, bool VEC>
+static hipError_t shrink_rows(const LoraShrink& p, hipStream_t s) {
+  const int rb = shrink_rb(p.rows.M, p.R, p.rows.L);
+  if (rb == 1) return shrink_rank<TYPE, VEC, 1>(p, s);
+  if (rb == 2) return shrink_rank<TYPE, VEC, 2>(p, s);
+  return p.R <= 64 ? run_shrink<TYPE, VEC, 4, 4>(p, s) : run_shrink<TYPE, VEC, 4, 8>(p, s);
+}
+static bool vec16(const void* p, int64_t ld, int64_t cols) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ((ld | cols) & 7) == 0;
+}
+hipError_t launch_lora_shrink(const LoraShrink& p, hipStream_t s) {
+  const bool v = vec16(p.x, p.ldx, p.C) && vec16(p.w, p.ldw, p.w_stride);
+  if (p.type == MM_BF16) return v ? shrink_rows<MM_BF16, true>(p, s) : shrink_rows<MM_BF16, false>(p, s);
+  return v ? shrink_rows<MM_FP16, true>(p, s) : shrink_rows<MM_FP16, false>(p, s);
+}
+
+// ----------------------------------------------------------------------------- expand
+// A tile of positions by 256 columns, 64 per wave.  A wave keeps W_l's fragments of its columns in
+// registers and walks the positions 16 at a time.  The product is taken transposed with the
+// columns dealt so that a lane ends with 16 consecutive ones of one row: 32 bytes of base and y.
+template <int TYPE, bool VEC, bool VECW, int RT>
+__global__ __launch_bounds__(256) void lora_expand_kernel(LoraExpand p, int tile_rows) {
+  using E = Elem<TYPE>;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const RowTile rt = find_row_tile(p.rows.count, p.rows.L + 1, (uint32_t)p.rows.M, tile_rows, 1, false, blockIdx.x, lane);
+  if (rt.g < 0) return;
+  const bool rest = rt.g == p.rows.L;                    // rows without an adapter
+  if (rest && p.base == p.y) return;
+  const int64_t pos0 = (int64_t)rt.row0 + (int64_t)rt.t * tile_rows;
+  const int valid = min((int)(rt.m - rt.t * tile_rows), tile_rows);
+  const int q = lane & 15, j = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.y * 256 + wave * 64;
+  if (n0 >= p.C) return;
+  v4i wf[4][RT];
+  if (!rest) {
+    const uint16_t* w = static_cast<const uint16_t*>(p.w) + rt.g * p.w_stride;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const int64_t n = min(n0 + 16 * (q >> 2) + 4 * f + (q & 3), p.C - 1);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const int r = 16 * t + 8 * (j & 1);
+        wf[f][t] = load8<VECW>(w + n * p.ldw + r, min(p.R - r, 8));
+      }
+    }
+  }
+  const float sc = !rest && p.scales ? p.scales[rt.g] : 1.0f;
+  const int64_t c = n0 + 16 * j;
+  const int cols = (int)min(p.C - c, (int64_t)16);       // of this lane
+  for (int b = 0; b < valid; b += 16) {
+    const int at = min(b + q, valid - 1);
+    const bool live = b + q < valid;
+    const int64_t row = p.rows.order[pos0 + at];
+    v4i old[2] = {v4i{0, 0, 0, 0}, v4i{0, 0, 0, 0}};
+    if (p.base && live) {
+      const uint16_t* src = static_cast<const uint16_t*>(p.base) + row * p.ldbase + c;
+      old[0] = load8<VEC>(src, cols);
+      old[1] = load8<VEC>(src + 8, cols - 8);
+    }
+    v4f acc[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) acc[f] = v4f{0, 0, 0, 0};
+    float mul = sc;
+    if (!rest) {
+      float v[RT][8];
+      float top = 0.0f;
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const int r = 16 * t + 8 * (j & 1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[t][i] = 0.0f;
+        for (int z = 0; z < p.parts; ++z) {
+          const float* src = p.v + ((int64_t)z * p.rows.M + pos0 + at) * p.R + r;
+          if ((p.R & 3) == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 4)
+              if (r + i < p.R) {
+                const v4f x = *reinterpret_cast<const v4f*>(src + i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[t][i + e] += x[e];
+              }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (r + i < p.R) v[t][i] += src[i];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[t][i]));
+      }
+      if (TYPE == MM_FP16) {
+        const float s = fp16_scale(fmaxf(top, __shfl_xor(top, 16, 64)));
+        mul *= inverse_pow2(s);
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[t][i] *= s;
+      }
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const v4i u = split8<TYPE>(v[t], j >= 2);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) acc[f] = E::mma16(wf[f][t], u, acc[f]);
+      }
+    }
+    // mul is its row's: the accumulator's column is the lane's own position q
+    if (!live) continue;
+    uint16_t* dst = static_cast<uint16_t*>(p.y) + row * p.ldy + c;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint16_t o = (uint16_t)((uint32_t)old[h][i / 2] >> (16 * (i & 1)));
+        y[i] = rest ? 0.0f : mul * acc[2 * h + i / 4][i & 3];
+        y[i] = p.base ? E::up(o) + y[i] : y[i];
+      }
+      v4i out;
+      if (rest) out = old[h];                            // bit for bit
+      else
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = (int)E::down2(y[2 * i], y[2 * i + 1]);
+      if constexpr (VEC) {
+        if (cols > 8 * h) *reinterpret_cast<v4i*>(dst + 8 * h) = out;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (8 * h + i < cols) dst[8 * h + i] = (uint16_t)((uint32_t)out[i / 2] >> (16 * (i & 1)));
+      }
+    }
+  }
+}
+
+template <int TYPE, bool VEC, bool VECW>
+static hipError_t run_expand(const LoraExpand& p, hipStream_t s) {
+  // a tile of 16 positions while those leave the device unfilled, else 64: W is read once per tile
+  const int64_t cols = (p.C + 255) / 256;
+  const int rows = tiles_bound(p.rows.M, p.rows.L + 1, 16) * cols < 2048 ? 16 : 64;
+  const dim3 grid((uint32_t)tiles_bound(p.rows.M, p.rows.L + 1, rows), (uint32_t)cols);
+  if (p.R <= 16) hipLaunchKernelGGL((lora_expand_kernel<TYPE, VEC, VECW, 1>), grid, dim3(256), 0, s, p, rows);
+  else if (p.R <= 32) hipLaunchKernelGGL((lora_expand_kernel<TYPE, VEC, VECW, 2>), grid, dim3(256), 0, s, p, rows);
+  else if (p.R <= 64) hipLaunchKernelGGL((lora_expand_kernel<TYPE, VEC, VECW, 4>), grid, dim3(256), 0, s, p, rows);
+  else hipLaunchKernelGGL((lora_expand_kernel<TYPE, VEC, VECW, 8>), grid, dim3(256), 0, s, p, rows);
+  return hipGetLastError();
+}
+template <int TYPE>
+static hipError_t expand_vec(const LoraExpand& p, hipStream_t s) {
+  const bool v = (!p.base || vec16(p.base, p.ldbase, p.C)) && vec16(p.y, p.ldy, p.C);
+  const bool w = vec16(p.w, p.ldw, p.w_stride) && (p.R & 7) == 0;
+  if (v) return w ? run_expand<TYPE, true, true>(p, s) : run_expand<TYPE, true, false>(p, s);
+  return w ? run_expand<TYPE, false, true>(p, s) : run_expand<TYPE, false, false>(p, s);
+}
+hipError_t launch_lora_expand(const LoraExpand& p, hipStream_t s) {
+  return p.type == MM_BF16 ? expand_vec<MM_BF16>(p, s) : expand_vec<MM_FP16>(p, s);
+}
+
+// ----------------------------------------------------------------------------- outer
+// part[chunk][r][c] = sum over the chunk's positions of v[p, r] X[row p, c]: a chunk of positions of
+// one adapter by 256 columns, 64 positions a stage.  Both factors are contracted over positions, so
+// both are read from LDS by ds_read_b64_tr_b16 (as the ring kernel's transposed units).  The chunks
+// of an adapter are joined in order by lora_outer_sum.
+constexpr int OP = 64, OC = 256;
+
+template <int TYPE, bool VEC, int RT>
+__global__ __launch_bounds__(256) void lora_outer_kernel(LoraOuter p, int chunk_rows) {
+  using E = Elem<TYPE>;
+  constexpr int VW = RT * 16;                                     // ranks in LDS
+  __shared__ __align__(1024) uint16_t sx[OP * OC];
+  __shared__ __align__(1024) uint16_t sv[2][OP * VW];             // hi, lo
+  __shared__ float s_top[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const RowTile rt = find_row_tile(p.rows.count, p.rows.L, (uint32_t)p.rows.M, chunk_rows, 1, false, blockIdx.x, lane);
+  if (rt.g < 0) return;
+  const int64_t pos0 = (int64_t)rt.row0 + (int64_t)rt.t * chunk_rows;
+  const int valid = min((int)(rt.m - rt.t * chunk_rows), chunk_rows);
+  const int64_t c0 = (int64_t)blockIdx.y * OC;
+  auto factor = [&](int64_t pos, int r) {
+    float f = 0.0f;
+    for (int z = 0; z < p.parts; ++z) f += p.v[((int64_t)z * p.rows.M + pos) * p.R + r];
+    return f;
+  };
+  float scale = 1.0f;
+  if (TYPE == MM_FP16) {                                          // one power of two for the chunk
+    float top = 0.0f;
+    for (int i = tid; i < valid * p.R; i += 256) {
+      const float f = fabsf(factor(pos0 + i / p.R, i % p.R));
+      if (__builtin_isfinite(f)) top = fmaxf(top, f);
+    }
+    top = wave_max(top);
+    if (lane == 0) s_top[wave] = top;
+    __syncthreads();
+    scale = fp16_scale(fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3])));
+  }
+  v4f acc[RT][4];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int f = 0; f < 4; ++f) acc[t][f] = v4f{0, 0, 0, 0};
+
+  // a thread stages 8 columns of rows tid / 32 + 8 i
+  const int xr = tid >> 5, xc = (tid & 31) * 8;
+  const int xcols = (int)min(p.C - c0 - xc, (int64_t)8);
+  v4i xs[OP / 8];
+  auto fetch = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < OP / 8; ++i) {
+      const int r = b + xr + 8 * i;
+      xs[i] = r < valid ? load8<VEC>(static_cast<const uint16_t*>(p.x) + p.rows.order[pos0 + r] * p.ldx + c0 + xc, xcols)
+                        : v4i{0, 0, 0, 0};
+    }
+  };
+  fetch(0);
+  const int i16 = lane & 15, r4 = i16 >> 2, j = lane >> 4;
+  const uint32_t sx0 = (uint32_t)(uintptr_t)sx, sv0 = (uint32_t)(uintptr_t)sv;
+  typedef __attribute__((address_space(3))) v4s lds_v4s;
+  auto tr = [](uint32_t a, uint32_t step) {
+    const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)a));
+    const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)(a + step)));
+    return v4i{lo.x, lo.y, hi.x, hi.y};
+  };
+  for (int b = 0; b < valid; b += OP) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < OP / 8; ++i) {
+      const int r = xr + 8 * i;
+      *reinterpret_cast<v4i*>(sx + r * OC + (((xc >> 3) ^ ((r & 3) << 2)) << 3)) = xs[i];
+    }
+    for (int i = tid; i < OP * VW; i += 256) {
+      const int m = i / VW, r = i % VW;
+      const float f = (b + m < valid && r < p.R) ? scale * factor(pos0 + b + m, r) : 0.0f;
+      const uint16_t h = E::down(f);
+      const float hf = E::up(h);
+      sv[0][i] = h;
+      sv[1][i] = E::down(__builtin_isfinite(hf) ? f - hf : 0.0f);
+    }
+    if (b + OP < valid) fetch(b + OP);
+    __syncthreads();
+#pragma unroll
+    for (int ks = 0; ks < OP / 32; ++ks) {
+      const int row = 32 * ks + 8 * j + r4;
+      v4i xf[4];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int chunk = ((wave * 64 + 16 * f) / 8 + ((i16 & 3) >> 1)) ^ (r4 << 2);
+        xf[f] = tr(sx0 + row * (OC * 2) + chunk * 16 + (i16 & 1) * 8, 4 * OC * 2);
+      }
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const v4i vf = tr(sv0 + h * (OP * VW * 2) + row * (VW * 2) + t * 32 + (i16 & 3) * 8, 4 * VW * 2);
+#pragma unroll
+          for (int f = 0; f < 4; ++f) acc[t][f] = E::mma16(vf, xf[f], acc[t][f]);
+        }
+    }
+  }
+  // lane: ranks 16 t + 4 j + i, column 16 f + lane % 16
+  const float inv = inverse_pow2(scale);
+  float* out = p.part + (int64_t)blockIdx.x * p.R * p.C;
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 16 * t + 4 * j + i;
+        const int64_t c = c0 + wave * 64 + 16 * f + i16;
+        if (r < p.R && c < p.C) out[r * p.C + c] = inv * acc[t][f][i];
+      }
+}
+
+// Chunks of the adapters before l, and of l.
+struct ChunkSpan {
+  uint32_t first, n;
+};
+__device__ __forceinline__ ChunkSpan find_chunks(const int32_t* count, int L, uint32_t M, uint32_t h, int l, int lane) {
+  uint32_t done = 0, before = 0;
+  ChunkSpan s{0, 0};
+  for (int base = 0; base <= l; base += 64) {
+    const Span sp = wave_spans(count, L, M, base, lane, done);
+    const uint32_t mine = (sp.end - sp.start + h - 1) / h;
+    const uint32_t incl = wave_incl_add(mine, lane, 0x7FFFFFFFu);
+    const int at = min(l - base, 63);
+    s.n = (uint32_t)__builtin_amdgcn_readlane((int)mine, at);
+    s.first = before + (uint32_t)__builtin_amdgcn_readlane((int)incl, at) - s.n;
+    before += (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
+  }
+  return s;
+}
+
+// Eight ranks of 256 columns of one adapter.
+template <int TYPE, bool TRANSPOSED>
+__global__ __launch_bounds__(256) void lora_outer_sum_kernel(LoraOuter p, int chunk_rows) {
+  using E = Elem<TYPE>;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int l = blockIdx.z, r0 = blockIdx.y * 8;
+  const int64_t c = (int64_t)blockIdx.x * 256 + tid;
+  const ChunkSpan s = find_chunks(p.rows.count, p.rows.L, (uint32_t)p.rows.M, chunk_rows, l, lane);
+  if (c >= p.C) return;
+  float acc[8] = {};
+  for (uint32_t k = 0; k < s.n; ++k) {
+    const float* src = p.part + ((int64_t)(s.first + k) * p.R + r0) * p.C + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (r0 + i < p.R) acc[i] += src[i * p.C];
+  }
+  const float sc = p.scales ? p.scales[l] : 1.0f;
+  uint16_t* out = static_cast<uint16_t*>(p.out);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (r0 + i >= p.R) break;
+    const uint16_t v = s.n ? E::down(sc * acc[i]) : (uint16_t)0;
+    if (TRANSPOSED) out[((int64_t)l * p.C + c) * p.R + r0 + i] = v;
+    else out[((int64_t)l * p.R + r0 + i) * p.C + c] = v;
+  }
+}
+
+// Positions of a chunk: about 512 workgroups over the tensor, at least 256 (the chunks' results are
+// written and read once more) and at most 2048.
+static int outer_rows(int64_t M, int64_t C) {
+  const int64_t r = M * ((C + OC - 1) / OC) / 512;
+  return (int)(std::min<int64_t>(std::max<int64_t>(r, 256), 2048) + OP - 1) / OP * OP;
+}
+int64_t lora_outer_part_floats(int64_t M, int64_t C, int R, int L) {
+  return tiles_bound(M, L, outer_rows(M, C)) * R * C;
+}
+template <int TYPE, bool VEC>
+static hipError_t run_outer(const LoraOuter& p, hipStream_t s) {
+  const int rows = outer_rows(p.rows.M, p.C);
+  const dim3 grid((uint32_t)tiles_bound(p.rows.M, p.rows.L, rows), (uint32_t)((p.C + OC - 1) / OC));
+  if (p.R <= 16) hipLaunchKernelGGL((lora_outer_kernel<TYPE, VEC, 1>), grid, dim3(256), 0, s, p, rows);
+  else if (p.R <= 32) hipLaunchKernelGGL((lora_outer_kernel<TYPE, VEC, 2>), grid, dim3(256), 0, s, p, rows);
+  else if (p.R <= 64) hipLaunchKernelGGL((lora_outer_kernel<TYPE, VEC, 4>), grid, dim3(256), 0, s, p, rows);
+  else hipLaunchKernelGGL((lora_outer_kernel<TYPE, VEC, 8>), grid, dim3(256), 0, s, p, rows);
+  if (hipError_t e = hipGetLastError()) return e;
+  const dim3 sum((uint32_t)((p.C + 255) / 256), (uint32_t)((p.R + 7) / 8), (uint32_t)p.rows.L);
+  if (p.transposed) hipLaunchKernelGGL((lora_outer_sum_kernel<TYPE, true>), sum, dim3(256), 0, s, p, rows);
+  else hipLaunchKernelGGL((lora_outer_sum_kernel<TYPE, false>), sum, dim3(256), 0, s, p, rows);
+  return hipGetLastError();
+}
+hipError_t launch_lora_outer(const LoraOuter& p, hipStream_t s) {
+  const bool v = vec16(p.x, p.ldx, p.C);
+  if (p.type == MM_BF16) return v ? run_outer<MM_BF16, true>(p, s) : run_outer<MM_BF16, false>(p, s);
+  return v ? run_outer<MM_FP16, true>(p, s) : run_outer<MM_FP16, false>(p, s);
+}
+
+// ----------------------------------------------------------------------------- transposed weights
+// dst[l][c][r] = src[l][r][c] through a 64 x 64 tile; adapters without rows are left out.
+__global__ __launch_bounds__(256) void lora_transpose_kernel(const uint16_t* __restrict__ src, int64_t lds_, int64_t ss,
+                                                             int64_t R, int64_t C, uint16_t* __restrict__ dst,
+                                                             int64_t ldd, int64_t ds, const int32_t* __restrict__ count) {
+  __shared__ uint16_t t[64][66];
+  const int l = blockIdx.z;
+  if (count[l] <= 0) return;
+  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
+  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+  for (int i = y; i < 64; i += 4)
+    if (r0 + i < R && c0 + x < C) t[i][x] = src[l * ss + (r0 + i) * lds_ + c0 + x];
+  __syncthreads();
+  for (int i = y; i < 64; i += 4)
+    if (c0 + i < C && r0 + x < ldd) dst[l * ds + (c0 + i) * ldd + r0 + x] = r0 + x < R ? t[x][i] : (uint16_t)0;
+}
+hipError_t launch_lora_transpose(const void* src, int64_t lds_, int64_t src_stride, int64_t R, int64_t C, void* dst,
+                                 int64_t ldd, int64_t dst_stride, const int32_t* count, int L, hipStream_t s) {
+  const dim3 grid((uint32_t)((C + 63) / 64), (uint32_t)((R + 63) / 64), (uint32_t)L);
+  hipLaunchKernelGGL(lora_transpose_kernel, grid, dim3(256), 0, s, static_cast<const uint16_t*>(src), lds_, src_stride,
+                     R, C, static_cast<uint16_t*>(dst), ldd, dst_stride, count);
+  return hipGetLastError();
+}
+
+__global__ void zero16_kernel(uint16_t* p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) p[i] = 0;
+}
+hipError_t launch_zero16(void* p, int64_t n, hipStream_t s) {
+  const int64_t blocks = std::min<int64_t>((n + 255) / 256, 4096);
+  hipLaunchKernelGGL(zero16_kernel, dim3((uint32_t)blocks), dim3(256), 0, s, static_cast<uint16_t*>(p), n);
+  return hipGetLastError();
+}
+
+}  // namespace gmlp

@@ -176,7 +176,7 @@ extern "C" gmlp_status gmlp_dispatch_plan(const int32_t* experts, int64_t n, int
   const size_t need = order_ws(n, E);
   if (need && (!ws || ws_bytes < need || !aligned16(ws)))
     return set_error(GMLP_WORKSPACE, "workspace: %zu bytes, 16-byte aligned, are needed", need);
-  return launched(launch_group_order(experts, n, E, m_splits, rows, order, static_cast<int32_t*>(ws), stream),
+  return launched(launch_group_order(experts, n, E, false, m_splits, rows, order, static_cast<int32_t*>(ws), stream),
                   "dispatch plan");
 }
 
@@ -188,4 +188,175 @@ extern "C" gmlp_status gmlp_combine(const gmlp_move_args* args, hipStream_t stre
 }
 extern "C" gmlp_status gmlp_combine_dprobs(const gmlp_move_args* args, hipStream_t stream) {
   return move(args, MOVE_DPROBS, stream);
+}
+
+// ----------------------------------------------------------------------------- low-rank adapters
+namespace {
+struct Carve {      // sections of a caller buffer at 256-byte offsets
+  uint8_t* base;
+  size_t off = 0;
+  template <class T>
+  T* take(int64_t count) {
+    off = (off + 255) & ~size_t(255);
+    T* p = base ? reinterpret_cast<T*>(base + off) : nullptr;
+    off += (size_t)count * sizeof(T);
+    return p;
+  }
+};
+struct LoraCtx {
+  int32_t* count;
+  int32_t* order;
+  float* u;
+  int parts;
+};
+LoraCtx carve_lora_ctx(Carve& c, int64_t M, int64_t K, int R, int L) {
+  LoraCtx x;
+  x.parts = lora_shrink_parts(M, K, R, L);
+  x.count = c.take<int32_t>(L + 1);
+  x.order = c.take<int32_t>(M);
+  x.u = c.take<float>((int64_t)x.parts * M * R);
+  return x;
+}
+struct LoraWs {
+  uint16_t* at;      // [L, K, ldr]
+  uint16_t* bt;      // [L, R, ldn]
+  float* du;
+  float* part;
+  int64_t ldr, ldn;
+  int parts;
+};
+int64_t up8(int64_t v) { return (v + 7) & ~int64_t(7); }
+LoraWs carve_lora_ws(Carve& c, int64_t M, int64_t K, int64_t N, int R, int L) {
+  LoraWs w;
+  w.ldr = up8(R);
+  w.ldn = up8(N);
+  w.parts = lora_shrink_parts(M, N, R, L);
+  w.at = c.take<uint16_t>((int64_t)L * K * w.ldr);
+  w.bt = c.take<uint16_t>((int64_t)L * R * w.ldn);
+  w.du = c.take<float>((int64_t)w.parts * M * R);
+  w.part = c.take<float>(std::max(lora_outer_part_floats(M, K, R, L), lora_outer_part_floats(M, N, R, L)));
+  return w;
+}
+gmlp_status check_lora_sizes(int64_t M, int64_t K, int64_t N, int32_t R, int32_t L) {
+  if (M < 0 || M >= kMaxRows) return set_error(GMLP_UNSUPPORTED, "dims: M = %lld rows is out of range", (long long)M);
+  if (K < 1 || N < 1 || K >= kMaxLd || N >= kMaxLd)
+    return set_error(GMLP_UNSUPPORTED, "dims: K and N must be in [1, 2^20), got %lld and %lld", (long long)K, (long long)N);
+  if (R < 1 || R > kLoraMaxRank) return set_error(GMLP_UNSUPPORTED, "dims: ranks 1 to %d are supported, got %d", kLoraMaxRank, R);
+  if (L < 1 || L > kLoraMaxAdapters)
+    return set_error(GMLP_UNSUPPORTED, "dims: 1 to %d adapters are supported, got %d", kLoraMaxAdapters, L);
+  return GMLP_OK;
+}
+gmlp_status check_lora_weights(const gmlp_lora_weights& w, int64_t K, int64_t N, int R, int L) {
+  if (!w.a || !w.b) return set_error(GMLP_INVALID_ARG, "null pointer argument");
+  if (!aligned2(w.a) || !aligned2(w.b) || !aligned4(w.scales))
+    return set_error(GMLP_INVALID_ARG, "a tensor is not aligned to its elements");
+  if (w.lda < K || w.ldb < R || w.lda >= kMaxLd || w.ldb >= kMaxLd)
+    return set_error(GMLP_INVALID_ARG, "strides: row strides must be at least the row's length and below 2^20");
+  if (L > 1 && (w.a_stride < (R - 1) * w.lda + K || w.b_stride < (N - 1) * w.ldb + R))
+    return set_error(GMLP_INVALID_ARG, "strides: the adapters overlap");
+  return GMLP_OK;
+}
+bool bad_ld(int64_t ld, int64_t cols) { return ld < cols; }
+}  // namespace
+
+extern "C" gmlp_status gmlp_lora_query_sizes(int64_t M, int64_t K, int64_t N, int32_t R, int32_t L,
+                                             gmlp_lora_sizes* out) {
+  if (!out) return set_error(GMLP_INVALID_ARG, "null pointer argument");
+  const gmlp_status st = check_lora_sizes(M, K, N, R, L);
+  if (st != GMLP_OK) return st;
+  Carve c{nullptr}, w{nullptr};
+  carve_lora_ctx(c, M, K, R, L);
+  carve_lora_ws(w, M, K, N, R, L);
+  out->ctx_bytes = c.off + 256;
+  out->fwd_ws_bytes = order_ws(M, L + 1);
+  out->bwd_ws_bytes = w.off + 256;
+  return fine();
+}
+
+extern "C" gmlp_status gmlp_lora_forward(const gmlp_lora_fwd_args* p, hipStream_t stream) {
+  if (!p) return set_error(GMLP_INVALID_ARG, "null pointer argument");
+  gmlp_status st = check_dtype(p->dtype);
+  if (st != GMLP_OK) return st;
+  gmlp_lora_sizes sz;
+  if ((st = gmlp_lora_query_sizes(p->M, p->K, p->N, p->R, p->L, &sz)) != GMLP_OK) return st;
+  if ((st = check_lora_weights(p->w, p->K, p->N, p->R, p->L)) != GMLP_OK) return st;
+  if (p->M == 0) return fine();
+  if (!p->x || !p->ids || !p->y) return set_error(GMLP_INVALID_ARG, "null pointer argument");
+  if (!aligned2(p->x) || !aligned2(p->base) || !aligned2(p->y) || !aligned4(p->ids))
+    return set_error(GMLP_INVALID_ARG, "a tensor is not aligned to its elements");
+  if (bad_ld(p->ldx, p->K) || bad_ld(p->ldy, p->N) || (p->base && bad_ld(p->ldbase, p->N)))
+    return set_error(GMLP_INVALID_ARG, "strides: row strides must be at least the row's length");
+  if (p->base == p->y && p->ldbase != p->ldy)
+    return set_error(GMLP_INVALID_ARG, "strides: base and y are one tensor with two row strides");
+  if (!p->ctx || p->ctx_bytes < sz.ctx_bytes || !aligned16(p->ctx))
+    return set_error(GMLP_WORKSPACE, "ctx: %zu bytes, 16-byte aligned, are needed", sz.ctx_bytes);
+  if (sz.fwd_ws_bytes && (!p->ws || p->ws_bytes < sz.fwd_ws_bytes || !aligned16(p->ws)))
+    return set_error(GMLP_WORKSPACE, "workspace: %zu bytes, 16-byte aligned, are needed", sz.fwd_ws_bytes);
+  Carve c{static_cast<uint8_t*>(p->ctx)};
+  const LoraCtx x = carve_lora_ctx(c, p->M, p->K, p->R, p->L);
+  const LoraRows rows{x.count, x.order, p->M, p->L};
+  hipError_t e = launch_group_order(p->ids, p->M, p->L + 1, true, x.count, nullptr, x.order, static_cast<int32_t*>(p->ws), stream);
+  if (e != hipSuccess) return launched(e, "adapter order");
+  LoraShrink s{p->dtype, p->R, rows, p->x, p->ldx, p->w.a, p->w.lda, p->w.a_stride, p->K, nullptr, x.u, x.parts};
+  if ((e = launch_lora_shrink(s, stream)) != hipSuccess) return launched(e, "lora shrink");
+  LoraExpand ex{p->dtype, p->R, rows, x.u, x.parts, p->w.b, p->w.ldb, p->w.b_stride, p->N, p->w.scales,
+                p->base, p->ldbase, p->y, p->ldy};
+  return launched(launch_lora_expand(ex, stream), "lora expand");
+}
+
+extern "C" gmlp_status gmlp_lora_backward(const gmlp_lora_bwd_args* p, hipStream_t stream) {
+  if (!p) return set_error(GMLP_INVALID_ARG, "null pointer argument");
+  gmlp_status st = check_dtype(p->dtype);
+  if (st != GMLP_OK) return st;
+  gmlp_lora_sizes sz;
+  if ((st = gmlp_lora_query_sizes(p->M, p->K, p->N, p->R, p->L, &sz)) != GMLP_OK) return st;
+  if ((st = check_lora_weights(p->w, p->K, p->N, p->R, p->L)) != GMLP_OK) return st;
+  if (p->M > 0 && (!p->dy || (p->da && !p->x) || !p->ctx)) return set_error(GMLP_INVALID_ARG, "null pointer argument");
+  if (!aligned2(p->dy) || !aligned2(p->x) || !aligned2(p->dx) || !aligned2(p->dx_add) || !aligned2(p->da) || !aligned2(p->db))
+    return set_error(GMLP_INVALID_ARG, "a tensor is not aligned to its elements");
+  if (p->M > 0 && (bad_ld(p->lddy, p->N) || (p->x && bad_ld(p->ldx, p->K)) || (p->dx && bad_ld(p->lddx, p->K)) ||
+                   (p->dx_add && bad_ld(p->lddx_add, p->K))))
+    return set_error(GMLP_INVALID_ARG, "strides: row strides must be at least the row's length");
+  if (p->dx && p->dx == p->dx_add && p->lddx != p->lddx_add)
+    return set_error(GMLP_INVALID_ARG, "strides: dx and dx_add are one tensor with two row strides");
+  if (p->M > 0 && (p->ctx_bytes < sz.ctx_bytes || !aligned16(p->ctx)))
+    return set_error(GMLP_WORKSPACE, "ctx: %zu bytes, 16-byte aligned, are needed", sz.ctx_bytes);
+  if (!p->ws || p->ws_bytes < sz.bwd_ws_bytes || !aligned16(p->ws))
+    return set_error(GMLP_WORKSPACE, "workspace: %zu bytes, 16-byte aligned, are needed", sz.bwd_ws_bytes);
+  hipError_t e;
+  const int64_t K = p->K, N = p->N;
+  const int R = p->R, L = p->L;
+  if (p->M == 0) {
+    // no rows: zero gradients
+    for (int i = 0; i < 2; ++i) {
+      void* d = i ? p->db : p->da;
+      if (d && (e = launch_zero16(d, (int64_t)L * R * (i ? N : K), stream)) != hipSuccess) return launched(e, "zero");
+    }
+    return fine();
+  }
+  Carve c{const_cast<uint8_t*>(static_cast<const uint8_t*>(p->ctx))}, cw{static_cast<uint8_t*>(p->ws)};
+  const LoraCtx x = carve_lora_ctx(c, p->M, K, R, L);
+  const LoraWs w = carve_lora_ws(cw, p->M, K, N, R, L);
+  const LoraRows rows{x.count, x.order, p->M, L};
+  if (p->db) {
+    LoraOuter o{p->dtype, R, rows, x.u, x.parts, p->dy, p->lddy, N, p->w.scales, p->db, true, w.part};
+    if ((e = launch_lora_outer(o, stream)) != hipSuccess) return launched(e, "lora db");
+  }
+  if (!p->dx && !p->da) return fine();
+  // du = scale dy b: the shrink over N with b transposed
+  if ((e = launch_lora_transpose(p->w.b, p->w.ldb, p->w.b_stride, N, R, w.bt, w.ldn, R * w.ldn, x.count, L, stream)) != hipSuccess)
+    return launched(e, "lora transpose");
+  LoraShrink s{p->dtype, R, rows, p->dy, p->lddy, w.bt, w.ldn, R * w.ldn, N, p->w.scales, w.du, w.parts};
+  if ((e = launch_lora_shrink(s, stream)) != hipSuccess) return launched(e, "lora shrink");
+  if (p->dx) {
+    if ((e = launch_lora_transpose(p->w.a, p->w.lda, p->w.a_stride, R, K, w.at, w.ldr, K * w.ldr, x.count, L, stream)) != hipSuccess)
+      return launched(e, "lora transpose");
+    LoraExpand ex{p->dtype, R, rows, w.du, w.parts, w.at, w.ldr, K * w.ldr, K, nullptr, p->dx_add, p->lddx_add, p->dx, p->lddx};
+    if ((e = launch_lora_expand(ex, stream)) != hipSuccess) return launched(e, "lora dx");
+  }
+  if (p->da) {
+    LoraOuter o{p->dtype, R, rows, w.du, w.parts, p->x, p->ldx, K, nullptr, p->da, false, w.part};
+    if ((e = launch_lora_outer(o, stream)) != hipSuccess) return launched(e, "lora da");
+  }
+  return fine();
 }

@@ -136,3 +136,86 @@ def test_plan_abi_refusals():
     assert L.gmlp_dispatch_plan(p, 8, 3, None, p, None, None, 0, None) == 1
     assert L.gmlp_dispatch_plan(None, 8, 3, p, p, None, None, 0, None) == 1
     assert L.gmlp_dispatch_plan(ctypes.c_void_p(255), 8, 3, p, p, None, None, 0, None) == 1
+
+
+def _lora_args():
+    return dict(base=_t(4, 8), x=_t(4, 16), a=_t(2, 4, 16), b=_t(2, 8, 4), ids=torch.zeros(4, dtype=torch.int32),
+                scales=torch.ones(2))
+
+
+@pytest.mark.parametrize("kw,exc,why", [
+    (dict(), ValueError, "GPU tensor"), (dict(x=torch.zeros(4, 16)), TypeError, "bf16 or fp16"),
+    (dict(a=_t(2, 4, 16, dtype=torch.float16)), TypeError, "a:"), (dict(x=_t(4, 15)), ValueError, "16 elements"),
+    (dict(b=_t(2, 8, 5)), ValueError, "b:"), (dict(b=_t(3, 8, 4)), ValueError, "b:"),
+    (dict(ids=torch.zeros(4, dtype=torch.int64)), TypeError, "ids"), (dict(ids=torch.zeros(5, dtype=torch.int32)), TypeError, "ids"),
+    (dict(scales=torch.ones(3)), TypeError, "scales"), (dict(scales=torch.ones(2).half()), TypeError, "scales"),
+    (dict(base=_t(4, 9)), ValueError, "base"), (dict(out=_t(4, 9)), ValueError, "out"),
+    (dict(a=_t(2, 129, 16), b=_t(2, 8, 129)), ValueError, "GPU tensor"),
+])
+def test_lora_binding_refusals(kw, exc, why):
+    args = _lora_args()
+    args.update(kw)
+    with pytest.raises(exc, match=why):
+        g.lora_forward(**args)
+
+
+def test_lora_sizes_and_scale_gradient_refused():
+    with pytest.raises(g.GmlpError, match="ranks 1 to 128"):
+        g.lora_query_sizes(4, 16, 8, 129, 2)
+    with pytest.raises(g.GmlpError, match="1 to 1023 adapters"):
+        g.lora_query_sizes(4, 16, 8, 4, 1024)
+    with pytest.raises(g.GmlpError, match="K and N"):
+        g.lora_query_sizes(4, 0, 8, 4, 2)
+    a = _lora_args()
+    a["scales"].requires_grad_()
+    with pytest.raises(ValueError, match="scales"):
+        g.lora(**a)
+    with pytest.raises(TypeError, match="ctx"):
+        g.lora_backward(_t(4, 8), _t(4, 16), _t(2, 4, 16), _t(2, 8, 4), None)
+
+
+def _lf(**kw):
+    a = g.LoraFwdArgs()
+    w = dict(a=256, lda=16, a_stride=64, b=256, ldb=4, b_stride=32, scales=256)
+    vals = dict(dtype=0, R=4, L=2, M=4, K=16, N=8, base=256, ldbase=8, x=256, ldx=16, ids=256, y=256, ldy=8, ctx=256,
+                ctx_bytes=1 << 20, ws=256, ws_bytes=1 << 20)
+    for k, v in kw.items():
+        (w if k in w else vals)[k] = v
+    for k, v in vals.items():
+        setattr(a, k, v)
+    a.w = g.LoraWeights(*[w[k] for k in ("a", "lda", "a_stride", "b", "ldb", "b_stride", "scales")])
+    return g.lib().gmlp_lora_forward(ctypes.byref(a), None)
+
+
+@pytest.mark.parametrize("kw,status,why", [
+    (dict(dtype=3), 2, "dtype"), (dict(R=0), 2, "ranks"), (dict(L=0), 2, "adapters"), (dict(M=-1), 2, "rows"),
+    (dict(x=None), 1, "null"), (dict(ids=None), 1, "null"), (dict(y=None), 1, "null"), (dict(a=None), 1, "null"),
+    (dict(b=None), 1, "null"), (dict(x=257), 1, "aligned"), (dict(scales=258), 1, "aligned"), (dict(lda=15), 1, "strides"),
+    (dict(ldb=3), 1, "strides"), (dict(a_stride=63), 1, "overlap"), (dict(ldx=15), 1, "strides"), (dict(ldy=7), 1, "strides"),
+    (dict(ldbase=16), 1, "two row strides"), (dict(ctx=None), 3, "ctx"), (dict(ctx_bytes=16), 3, "ctx"), (dict(ctx=264), 3, "ctx"),
+    (dict(M=5000, ws=None), 3, "workspace"), (dict(M=0, x=None, y=None, ids=None, ctx=None), 0, ""),
+])
+def test_lora_abi_refusals(kw, status, why):
+    assert _lf(**kw) == status and why in g.last_error(), g.last_error()
+
+
+def _lb(**kw):
+    a = g.LoraBwdArgs()
+    w = dict(a=256, lda=16, a_stride=64, b=256, ldb=4, b_stride=32, scales=256)
+    vals = dict(dtype=0, R=4, L=2, M=4, K=16, N=8, dy=256, lddy=8, x=256, ldx=16, dx_add=None, lddx_add=0, dx=256, lddx=16,
+                da=256, db=256, ctx=256, ctx_bytes=1 << 20, ws=256, ws_bytes=1 << 24)
+    for k, v in kw.items():
+        (w if k in w else vals)[k] = v
+    for k, v in vals.items():
+        setattr(a, k, v)
+    a.w = g.LoraWeights(*[w[k] for k in ("a", "lda", "a_stride", "b", "ldb", "b_stride", "scales")])
+    return g.lib().gmlp_lora_backward(ctypes.byref(a), None)
+
+
+@pytest.mark.parametrize("kw,status,why", [
+    (dict(dy=None), 1, "null"), (dict(x=None), 1, "null"), (dict(ctx=None), 1, "null"), (dict(da=257), 1, "aligned"),
+    (dict(lddx=15), 1, "strides"), (dict(lddy=7), 1, "strides"), (dict(dx_add=256, lddx_add=24), 1, "two row strides"),
+    (dict(ctx_bytes=8), 3, "ctx"), (dict(ws=None), 3, "workspace"), (dict(ws_bytes=64), 3, "workspace"),
+])
+def test_lora_backward_abi_refusals(kw, status, why):
+    assert _lb(**kw) == status and why in g.last_error(), g.last_error()
