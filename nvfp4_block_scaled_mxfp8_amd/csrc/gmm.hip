@@ -154,6 +154,8 @@ struct Feed {
   uint32_t step;                // bytes between a wave's DMAs of one unit
   uint32_t row_bytes;           // 2 ld
   uint32_t cols_bytes;          // TR: bytes from the tile's first column to the end of a row
+  v4i rsrc;                     // the unit being issued
+  uint32_t v;
 
   __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int valid, int64_t kn, int tid) {
     base = sgpr64((uint64_t)(uintptr_t)p);
@@ -175,7 +177,7 @@ struct Feed {
     }
   }
   // The unit's descriptor, then on to the next stage.
-  __device__ __forceinline__ void next(v4i& rsrc, uint32_t& v) {
+  __device__ __forceinline__ void next() {
     int32_t n;
     if (!TR) n = left > 0 ? (int32_t)rest + 2 * left : 0;
     else n = left > 0 ? (int32_t)min((uint64_t)(uint32_t)(left - 1) * row_bytes + cols_bytes, (uint64_t)0x7FFFFFFF) : 0;
@@ -184,12 +186,14 @@ struct Feed {
     base += TR ? 64ull * row_bytes : 128ull;
     left -= 64;
   }
-  __device__ __forceinline__ void issue(uint32_t slot, int wave) {
-    v4i rsrc;
-    uint32_t v;
-    next(rsrc, v);
+  // DMA number i of the unit (after next()).
+  __device__ __forceinline__ void issue(int i, uint32_t slot, int wave) {
+    dma16(rsrc, v, (uint32_t)sgpr(i * step), (uint32_t)sgpr(slot + i * NT * 16 + wave * 1024));
+  }
+  __device__ __forceinline__ void issue_all(uint32_t slot, int wave) {
+    next();
 #pragma unroll
-    for (int i = 0; i < kDma; ++i) dma16(rsrc, v, (uint32_t)sgpr(i * step), (uint32_t)sgpr(slot + i * NT * 16 + wave * 1024));
+    for (int i = 0; i < kDma; ++i) issue(i, slot, wave);
   }
 };
 
@@ -197,6 +201,7 @@ struct Feed {
 template <bool TR, int T, int N>
 struct Frags {
   uint32_t off[4];              // lane offsets: !TR by step, TR by tile
+  uint32_t at[4];               // the same in the current unit
   __device__ __forceinline__ void init(int first, int lane) {
     if (!TR) {
       const int r = lane & 31, j = lane >> 5;
@@ -211,21 +216,24 @@ struct Frags {
       }
     }
   }
-  __device__ __forceinline__ void read(uint32_t unit, int s, v4i* f) const {
+  // The bases stay opaque, so that the steps and tiles are instruction offsets.
+  __device__ __forceinline__ void enter(uint32_t unit) {
 #pragma unroll
-    for (int t = 0; t < N; ++t) {
-      if (!TR) {
-        f[t] = *(const __attribute__((address_space(3))) v4i*)(uintptr_t)(unit + off[s] + t * 32 * 128);
-      } else {
-        const uint32_t a = unit + off[t] + s * 16 * (T * 2);
-        const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)a);
-        const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)(a + 4 * (T * 2)));
-        const v2i l2 = __builtin_bit_cast(v2i, lo), h2 = __builtin_bit_cast(v2i, hi);
-        f[t] = v4i{l2.x, l2.y, h2.x, h2.y};
-      }
+    for (int i = 0; i < (TR ? N : 4); ++i) {
+      at[i] = unit + off[i];
+      asm volatile("" : "+v"(at[i]));
     }
   }
+  __device__ __forceinline__ v4i read(int s, int t) const {
+    if (!TR) return *(const __attribute__((address_space(3))) v4i*)(uintptr_t)(at[s] + t * 32 * 128);
+    const uint32_t a = at[t] + s * 16 * (T * 2);
+    const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)a));
+    const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)(a + 4 * (T * 2))));
+    return v4i{lo.x, lo.y, hi.x, hi.y};
+  }
 };
+
+#define MM_FENCE() __builtin_amdgcn_sched_barrier(0)
 
 template <int TYPE, int LAYOUT, int OUT, int T, int NWM, int NWN>
 __global__ __launch_bounds__(64 * NWM * NWN, 2) void gmm_ring_kernel(MmArgs p) {
@@ -311,40 +319,59 @@ __global__ __launch_bounds__(64 * NWM * NWN, 2) void gmm_ring_kernel(MmArgs p) {
     ra.init(wm * WM, lane);
     rb.init(wn * WN, lane);
     constexpr int P = Feed<AT, T, NT>::kDma;
-    fa.issue(lds0 + 0 * SLOT, wave);
-    fb.issue(lds0 + 1 * SLOT, wave);
-    fa.issue(lds0 + 2 * SLOT, wave);
-    fb.issue(lds0 + 3 * SLOT, wave);
-    fa.issue(lds0 + 4 * SLOT, wave);
+    fa.issue_all(lds0 + 0 * SLOT, wave);
+    fb.issue_all(lds0 + 1 * SLOT, wave);
+    fa.issue_all(lds0 + 2 * SLOT, wave);
+    fb.issue_all(lds0 + 3 * SLOT, wave);
+    fa.issue_all(lds0 + 4 * SLOT, wave);
     uint32_t ua = lds0, ub = lds0 + SLOT;       // the stage's units
     const uint32_t end = lds0 + 5 * SLOT;
     v4i a[2][NA], b[2][NB];
+    constexpr int NR = NA + NB, NM = NA * NB;
+    // fragment reads in the order the MFMAs want them: b0 a0 b1 a1 a2 ...
+    auto read_one = [&](int step, int n, v4i* xa, v4i* xb) {
+      if (n < 2 * NB && !(n & 1)) xb[n / 2] = rb.read(step, n / 2);
+      else if (n < 2 * NB) xa[n / 2] = ra.read(step, n / 2);
+      else xa[n - NB] = ra.read(step, n - NB);
+    };
     wait_stage<3 * P>();
-    ra.read(ua, 0, a[0]);
-    rb.read(ub, 0, b[0]);
+    ra.enter(ua);
+    rb.enter(ub);
+#pragma unroll
+    for (int n = 0; n < NR; ++n) read_one(0, n, a[0], b[0]);
     for (int s = 0; s < nst; ++s) {
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
         const int cur = ks & 1, nxt = cur ^ 1;
-        if (ks < 3) {
-          ra.read(ua, ks + 1, a[nxt]);
-          rb.read(ub, ks + 1, b[nxt]);
-        } else {
+        uint32_t da = 0, db = 0;
+        if (ks == 3) {
           wait_stage<P>();
-          fb.issue(ua, wave);                     // B of stage s + 2 into A's slot, A of s + 3 into B's
-          fa.issue(ub, wave);
+          da = ub;                                // A of stage s + 3 goes into B's slot,
+          db = ua;                                // B of s + 2 into A's
           ua += 2 * SLOT;
           ub += 2 * SLOT;
           if (ua >= end) ua -= 5 * SLOT;
           if (ub >= end) ub -= 5 * SLOT;
-          ra.read(ua, 0, a[nxt]);
-          rb.read(ub, 0, b[nxt]);
+          ra.enter(ua);
+          rb.enter(ub);
+          fb.next();
+          fa.next();
         }
-        // the transposed product: a lane then holds consecutive columns of one row
+        MM_FENCE();
+        // the transposed product: a lane then holds consecutive columns of one row.  One read of the
+        // next step behind each MFMA, and at the stage's end one DMA.
 #pragma unroll
-        for (int i = 0; i < NA; ++i)
-#pragma unroll
-          for (int j = 0; j < NB; ++j) acc[i][j] = E::mma32(b[cur][j], a[cur][i], acc[i][j]);
+        for (int m = 0; m < NM; ++m) {
+          const int i = m / NB, j = m % NB;
+          acc[i][j] = E::mma32(b[cur][j], a[cur][i], acc[i][j]);
+          MM_FENCE();
+          if (m < NR) read_one(ks < 3 ? ks + 1 : 0, m, a[nxt], b[nxt]);
+          if (ks == 3 && m < 2 * P) {
+            if (m < P) fb.issue(m, db, wave);
+            else fa.issue(m - P, da, wave);
+          }
+          MM_FENCE();
+        }
       }
     }
     wait_stage<0>();
