@@ -5,13 +5,12 @@
 #include "mm_common.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace gmlp {
 
-#ifndef GMM_T
-#define GMM_T 256
-#define GMM_WM 2
-#define GMM_WN 4
+#ifndef GMM_STREAM
+#define GMM_STREAM true
 #endif
 
 // ----------------------------------------------------------------------------- any alignment
@@ -129,9 +128,11 @@ __device__ __forceinline__ uint64_t sgpr64(uint64_t v) {
   return (uint64_t)(uint32_t)sgpr((int)(uint32_t)v) | ((uint64_t)(uint32_t)sgpr((int)(uint32_t)(v >> 32)) << 32);
 }
 // 16 bytes per lane from a buffer into LDS at m0 + 16 lane.  Inline asm, as the compiler would wait
-// for every outstanding DMA before each LDS read; the kernel counts them itself.
+// for every outstanding DMA before each LDS read; the kernel counts them itself.  The compiler may
+// have written the scalar operands by a vector instruction just before (a lane read), which a
+// vector-memory instruction must not read for five wait states: the move and the s_nop are those.
 __device__ __forceinline__ void dma16(v4i rsrc, uint32_t voff, uint32_t soff, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                :: "v"(voff), "s"(rsrc), "s"(soff), "s"(m0) : "memory");
 }
 template <int VM>
@@ -359,16 +360,20 @@ __global__ __launch_bounds__(64 * NWM * NWN, 2) void gmm_ring_kernel(MmArgs p) {
         }
         MM_FENCE();
         // the transposed product: a lane then holds consecutive columns of one row.  One read of the
-        // next step behind each MFMA, and at the stage's end one DMA.
+        // next step behind each MFMA, and at the stage's end its DMAs.
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
           const int i = m / NB, j = m % NB;
           acc[i][j] = E::mma32(b[cur][j], a[cur][i], acc[i][j]);
           MM_FENCE();
           if (m < NR) read_one(ks < 3 ? ks + 1 : 0, m, a[nxt], b[nxt]);
-          if (ks == 3 && m < 2 * P) {
-            if (m < P) fb.issue(m, db, wave);
-            else fa.issue(m - P, da, wave);
+          if (ks == 3) {
+            constexpr int D = (2 * P + NM - 1) / NM;
+#pragma unroll
+            for (int d = m * D; d < (m + 1) * D && d < 2 * P; ++d) {
+              if (d < P) fb.issue(d, db, wave);
+              else fa.issue(d - P, da, wave);
+            }
           }
           MM_FENCE();
         }
@@ -428,6 +433,369 @@ __global__ __launch_bounds__(64 * NWM * NWN, 2) void gmm_ring_kernel(MmArgs p) {
   }
 }
 
+// ----------------------------------------------------------------------------- stream kernel
+// The ring kernel made persistent: one workgroup per CU walks a list of 256 x 256 tiles and the
+// units of all its tiles form one sequence through the ring, so that a tile's first units are on
+// their way while the one before it ends, and its stores drain under the next one's products.
+//
+// At a tile's last stage the slot that held B is not refilled: it takes the tile's results (4 KB per
+// wave, 32 rows of 128 bytes at a time), which are read back as whole rows, and is refilled then; the
+// stores are issued behind those DMAs, so that the next tile's first stage need not wait for them.  Every wave issues the same count of DMAs and stores for every tile (the buffer
+// range check drops what lies outside), which is what the vmcnt bounds count on.
+//
+// A tile has three stages at least (empty ones read and multiply nothing): the units issued while
+// one tile is computed then belong to it or to its successor.  A wave multiplies only the 32-row
+// blocks of its half that hold a row, and the last stage only the 16-deep steps that hold an
+// element, so that a group's last tile costs what it holds.
+//
+// Row tiles of the groups come from a table that gmm_table_kernel writes first: eight words
+// {group, the group's first tile, its tiles, its first row, its rows}; WGRAD reads each group's
+// {first row, rows}.
+constexpr int kTableWords = 8;
+
+__global__ __launch_bounds__(1024) void gmm_table_kernel(MmArgs p, int h, uint32_t* table, bool rows) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t done = 0, tiles = 0;
+  for (int base = 0; base <= p.G; base += 64) {
+    const int g = base + lane;
+    Span s = wave_spans(p.m_splits, p.G, (uint32_t)p.M, base, lane, done);
+    if (g == p.G) s.end = p.zero_rest ? (uint32_t)p.M : s.start;       // the rows behind the last group
+    if (g > p.G) s.end = s.start;
+    const uint32_t m = s.end - s.start, n = (m + h - 1) / h;
+    const uint32_t incl = wave_incl_add(n, lane, 0x7FFFFFFFu);
+    if (!rows) {
+      if (wave == 0 && g < p.G) {
+        table[8 + 2 * g] = s.start;
+        table[8 + 2 * g + 1] = m;
+      }
+    } else if (g <= p.G) {
+      const uint32_t first = tiles + incl - n;
+      for (uint32_t t = wave; t < n; t += 16) {
+        uint32_t* e = table + 8 + (uint64_t)(first + t) * kTableWords;
+        e[0] = (uint32_t)g;
+        e[1] = first;
+        e[2] = n;
+        e[3] = s.start;
+        e[4] = m;
+      }
+    }
+    tiles += (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
+  }
+  if (wave == 0) {
+    const uint32_t f = wave_split_flags(p.m_splits, p.G, p.M, lane);
+    if (lane == 0) {
+      *p.flags = f;
+      table[0] = tiles;
+    }
+  }
+}
+
+// One output tile (uniform values).
+struct StreamTile {
+  const uint16_t* a;
+  const uint16_t* b;
+  uint8_t* c;              // its first element
+  int arows, bcols;        // valid rows and columns, at most T; 0 rows: no tile
+  int kn, nst;
+};
+
+template <int LAYOUT, int OUT, int T>
+struct TileWalk {
+  uint32_t at, step, end;  // positions in this workgroup's list
+  uint32_t x;              // XCD
+  // The next tile of the list.
+  __device__ __forceinline__ void init(const MmArgs& p, const uint32_t* __restrict__ table) {
+    const uint32_t workers = gridDim.x >> 3;
+    x = blockIdx.x & 7;
+    if (LAYOUT == MM_WGRAD) {
+      const uint32_t tpg = ((p.n + T - 1) / T) * ((p.k + T - 1) / T);
+      if (tpg >= 64) {                   // XCD x takes the x-th eighth of every group's tiles
+        at = blockIdx.x >> 3;
+        step = workers;
+        end = (tpg + 7) / 8 * p.G;
+      } else {
+        at = blockIdx.x;
+        step = gridDim.x;
+        end = tpg * p.G;
+      }
+    } else {                             // XCD x takes the x-th eighth of all tiles
+      const uint32_t total = table[0] * ((p.n + T - 1) / T), per = (total + 7) / 8;
+      at = x * per + (blockIdx.x >> 3);
+      step = workers;
+      end = min((x + 1) * per, total);
+    }
+  }
+  __device__ __forceinline__ StreamTile next(const MmArgs& p, const uint32_t* __restrict__ table) {
+    constexpr uint32_t GR = 4;           // four row tiles to a column sweep
+    StreamTile t{};
+    while (at < end) {
+      const uint32_t l = at;
+      at += step;
+      if (LAYOUT == MM_WGRAD) {
+        const uint32_t ntm = (p.n + T - 1) / T, ntn = (p.k + T - 1) / T, tpg = ntm * ntn;
+        uint32_t g, i;
+        if (tpg >= 64) {
+          const uint32_t per = (tpg + 7) / 8;
+          g = l / per;
+          i = x * per + l % per;
+          if (i >= tpg) continue;
+        } else {
+          g = l / tpg;
+          i = l % tpg;
+        }
+        const uint32_t row0 = table[8 + 2 * g], m = table[8 + 2 * g + 1];
+        if (OUT == MM_OUT_ACC32 && m == 0) continue;
+        const uint32_t grp = i / (GR * ntn), rem = i % (GR * ntn), rh = min(GR, ntm - grp * GR);
+        const int tm = (int)((grp * GR + rem % rh) * T), col0 = (int)(rem / rh * T);
+        t.a = static_cast<const uint16_t*>(p.a) + (int64_t)row0 * p.lda + tm;
+        t.b = static_cast<const uint16_t*>(p.b) + (int64_t)row0 * p.ldb + col0;
+        t.c = static_cast<uint8_t*>(p.c) + ((int64_t)g * p.c_stride + (int64_t)tm * p.ldc + col0) * (OUT == MM_OUT_SAME ? 2 : 4);
+        t.arows = min(p.n - tm, T);
+        t.bcols = min(p.k - col0, T);
+        t.kn = (int)m;
+      } else {
+        const uint32_t ntn = (p.n + T - 1) / T;
+        const uint32_t* e = table + 8 + (uint64_t)(l / ntn) * kTableWords;
+        const uint32_t g = e[0], ntm = e[2], row0 = e[3], m = e[4];
+        const uint32_t i = l - e[1] * ntn;
+        const uint32_t grp = i / (GR * ntn), rem = i % (GR * ntn), rh = min(GR, ntm - grp * GR);
+        const uint32_t tm = (grp * GR + rem % rh) * T;
+        const int col0 = (int)(rem / rh * T);
+        const int64_t row = (int64_t)row0 + tm;
+        t.a = static_cast<const uint16_t*>(p.a) + row * p.lda;
+        t.b = static_cast<const uint16_t*>(p.b);
+        if ((int)g < p.G) t.b += (int64_t)g * p.b_stride + (LAYOUT == MM_FPROP ? (int64_t)col0 * p.ldb : (int64_t)col0);
+        t.c = static_cast<uint8_t*>(p.c) + (row * p.ldc + col0) * 2;
+        t.arows = (int)min(m - tm, (uint32_t)T);
+        t.bcols = min(p.n - col0, T);
+        t.kn = (int)g < p.G ? p.k : 0;
+      }
+      t.nst = max(3, (t.kn + 63) / 64);
+      return t;
+    }
+    t.nst = 1 << 30;                     // behind the last tile: empty units
+    return t;
+  }
+};
+
+// A Feed that moves on to the next tile by itself.
+template <bool TR, int T, int NT>
+struct StreamFeed : Feed<TR, T, NT> {
+  int todo;
+  __device__ __forceinline__ void set(const uint16_t* ptr, int64_t ld, int valid, const StreamTile& t, int tid) {
+    this->init(ptr, ld, valid, t.kn, tid);
+    todo = t.nst;
+  }
+  __device__ __forceinline__ void advance(const uint16_t* ptr, int64_t ld, int valid, const StreamTile& nt, int tid) {
+    if (todo == 0) set(ptr, ld, valid, nt, tid);
+    --todo;
+    this->next();
+  }
+};
+
+template <int TYPE, int LAYOUT, int OUT>
+__global__ __launch_bounds__(512, 2) void gmm_stream_kernel(MmArgs p, const uint32_t* __restrict__ table) {
+  using E = Elem<TYPE>;
+  constexpr int T = 256, NWN = 4, NT = 512, SLOT = T * 128;
+  constexpr bool AT = LAYOUT == MM_WGRAD, BT = LAYOUT != MM_FPROP;
+  constexpr int WM = 128, NA = 4, NB = 2, NR = NA + NB;
+  constexpr int NST = 16;                          // a wave's stores per tile (16-bit results)
+  typedef __attribute__((address_space(3))) v4i lds_v4i;
+  typedef __attribute__((address_space(3))) v2i lds_v2i;
+  __shared__ __align__(1024) uint8_t lds[5 * SLOT];
+  const int tid = threadIdx.x, lane = tid & 63, wave = sgpr(tid >> 6);
+  const int wm = wave / NWN, wn = wave % NWN;
+
+  TileWalk<LAYOUT, OUT, T> walk;
+  walk.init(p, table);
+  StreamTile cur = walk.next(p, table);
+  if (cur.arows == 0) return;
+  StreamTile nt = walk.next(p, table);
+
+  StreamFeed<AT, T, NT> fa;
+  StreamFeed<BT, T, NT> fb;
+  fa.set(cur.a, p.lda, cur.arows, cur, tid);
+  fb.set(cur.b, p.ldb, cur.bcols, cur, tid);
+  auto next_a = [&]() { fa.advance(nt.a, p.lda, nt.arows, nt, tid); };
+  auto next_b = [&]() { fb.advance(nt.b, p.ldb, nt.bcols, nt, tid); };
+  constexpr int P = Feed<AT, T, NT>::kDma;
+  auto issue_a = [&](uint32_t slot) {
+    next_a();
+#pragma unroll
+    for (int i = 0; i < P; ++i) fa.issue(i, slot, wave);
+  };
+  auto issue_b = [&](uint32_t slot) {
+    next_b();
+#pragma unroll
+    for (int i = 0; i < P; ++i) fb.issue(i, slot, wave);
+  };
+  Frags<AT, T, NA> ra;
+  Frags<BT, T, NB> rb;
+  ra.init(wm * WM, lane);
+  rb.init(wn * 64, lane);
+
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds, end = lds0 + 5 * SLOT;
+  issue_a(lds0);
+  issue_b(lds0 + SLOT);
+  issue_a(lds0 + 2 * SLOT);
+  issue_b(lds0 + 3 * SLOT);
+  issue_a(lds0 + 4 * SLOT);
+  uint32_t ua = lds0, ub = lds0 + SLOT;            // the stage's units
+  uint32_t sa = 0, sb = 0;                         // the units read before them
+  v4i a[2][NA], b[2][NB];
+  auto read_one = [&](int step, int n, v4i* xa, v4i* xb) {
+    if (n < 2 * NB && !(n & 1)) xb[n / 2] = rb.read(step, n / 2);
+    else if (n < 2 * NB) xa[n / 2] = ra.read(step, n / 2);
+    else xa[n - NB] = ra.read(step, n - NB);
+  };
+  v16f acc[NA][NB];
+  auto turn = [&]() {                              // on to the next stage's units
+    sa = ua;
+    sb = ub;
+    ua += 2 * SLOT;
+    ub += 2 * SLOT;
+    if (ua >= end) ua -= 5 * SLOT;
+    if (ub >= end) ub -= 5 * SLOT;
+    ra.enter(ua);
+    rb.enter(ub);
+  };
+  int nal = 0;                                     // 32-row blocks of this wave's half that hold a row
+  // One 16-deep step: behind each pair of MFMAs the reads of the step after it and, in a stage's last
+  // step, DMAs into the units just left.  A tile's last step reads nothing and leaves B's slot free.
+  // Row blocks without a row
+  // and steps without an element are not multiplied.
+  auto step = [&](auto more_, int ks, int left) {
+    constexpr bool MORE = decltype(more_)::value;
+    const int cu = ks & 1, nx = cu ^ 1;
+    const int live = sgpr(16 * ks < left ? nal : 0);
+    MM_FENCE();
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      if (i == 0) E::template mma32_pair<0>(live, b[cu][0], b[cu][1], a[cu][0], acc[0][0], acc[0][1]);
+      if (i == 1) E::template mma32_pair<1>(live, b[cu][0], b[cu][1], a[cu][1], acc[1][0], acc[1][1]);
+      if (i == 2) E::template mma32_pair<2>(live, b[cu][0], b[cu][1], a[cu][2], acc[2][0], acc[2][1]);
+      if (i == 3) E::template mma32_pair<3>(live, b[cu][0], b[cu][1], a[cu][3], acc[3][0], acc[3][1]);
+      MM_FENCE();
+      if (MORE) {
+#pragma unroll
+        for (int r = 2 * i; r < 2 * i + 2 && r < NR; ++r) read_one((ks + 1) & 3, r, a[nx], b[nx]);
+      }
+      if (ks == 3) {
+#pragma unroll
+        for (int d = 2 * i; d < 2 * i + 2; ++d) {
+          if (d < P) fb.issue(d, sa, wave);
+          else if (MORE) fa.issue(d - P, sb, wave);
+        }
+      }
+      MM_FENCE();
+    }
+  };
+  static_assert(P == NA && NB == 2, "two DMAs behind each pair of MFMAs of a stage's last step");
+  using No = std::integral_constant<bool, false>;
+  using Yes = std::integral_constant<bool, true>;
+  bool stores = false;                             // the tile before left stores behind its DMAs
+  auto stage = [&](auto more_, int s) {
+    constexpr bool MORE = decltype(more_)::value;
+    const int left = cur.kn - 64 * s;
+    step(Yes{}, 0, left);
+    step(Yes{}, 1, left);
+    step(Yes{}, 2, left);
+    if (OUT == MM_OUT_SAME && s == 0 && stores) wait_stage<P + NST>();
+    else wait_stage<P>();
+    turn();
+    next_b();
+    if (MORE) next_a();
+    step(more_, 3, left);
+  };
+
+  wait_stage<3 * P>();
+  ra.enter(ua);
+  rb.enter(ub);
+  while (true) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = v16f{};
+    nal = sgpr(min(max((cur.arows - wm * WM + 31) / 32, 0), 4));
+    // first fragments of the tile (its first two units have landed)
+#pragma unroll
+    for (int n = 0; n < NR; ++n) read_one(0, n, a[0], b[0]);
+    for (int s = 0; s + 1 < cur.nst; ++s) stage(Yes{}, s);
+    stage(No{}, cur.nst - 1);
+    mma32_settle();
+    // acc[i][j][e]: row 32 i + lane % 32, column 32 j + 8 (e / 4) + 4 (lane / 32) + e % 4 of the wave's
+    // 128 x 64; staged by 32 rows of 128 bytes in the wave's 4 KB of the slot B left
+    const uint32_t reg = sb + wave * 4096;
+    const int m = lane & 31, h = lane >> 5, msw = (m >> 1) & 7;
+    const int sr = lane >> 3, sc = lane & 7;
+    constexpr int EB = OUT == MM_OUT_SAME ? 2 : 4;
+    const uint32_t ldb = (uint32_t)(p.ldc * EB);
+    const uint64_t cb = sgpr64((uint64_t)(uintptr_t)cur.c);
+    const v4i rc{(int)(uint32_t)cb, (int)((uint32_t)(cb >> 32) & 0xFFFFu),
+                 sgpr((int)((uint32_t)(cur.arows - 1) * ldb + (uint32_t)(cur.bcols * EB))), 0x00020000};
+    auto staged = [&](int r) {                     // 16 bytes of row 8 r + sr
+      return *(lds_v4i*)(uintptr_t)(reg + (8 * r + sr) * 128 + ((sc ^ (((8 * r + sr) >> 1) & 7)) << 4));
+    };
+    auto store = [&](v4i v, uint32_t vo, uint32_t so) {
+      asm volatile("s_nop 4\n\tbuffer_store_dwordx4 %0, %1, %2, %3 offen\n\ts_nop 1" :: "v"(v), "v"(vo), "s"(rc), "s"((uint32_t)sgpr((int)so)) : "memory");
+    };
+    if constexpr (OUT == MM_OUT_SAME) {
+      v4i out[NA][4];
+#pragma unroll
+      for (int i = 0; i < NA; ++i) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const v16f& c = acc[i][j];
+            const v2i v{(int)E::down2(c[4 * q], c[4 * q + 1]), (int)E::down2(c[4 * q + 2], c[4 * q + 3])};
+            *(lds_v2i*)(uintptr_t)(reg + m * 128 + (((4 * j + q) ^ msw) << 4) + h * 8) = v;
+          }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) out[i][r] = staged(r);
+      }
+      wait_stage<63>();                            // every wave's rows are out of the slot
+      issue_a(sb);
+      const int c = wn * 64 + sc * 8;
+      const uint32_t vo = c < cur.bcols ? (uint32_t)(wm * WM + sr) * ldb + (uint32_t)(c * EB) : kNoLane;
+#pragma unroll
+      for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) store(out[i][r], vo, (32 * i + 8 * r) * ldb);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const v16f& c = acc[i][j];
+            const v4f v{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+            *(lds_v4i*)(uintptr_t)(reg + m * 128 + (((2 * q + h) ^ msw) << 4)) = __builtin_bit_cast(v4i, v);
+          }
+          const int c = wn * 64 + j * 32 + sc * 4;
+          const uint32_t vo = c < cur.bcols ? (uint32_t)(wm * WM + sr) * ldb + (uint32_t)(c * EB) : kNoLane;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            v4f f = __builtin_bit_cast(v4f, staged(r));
+            if (OUT == MM_OUT_ACC32) {
+              const int row = wm * WM + 32 * i + 8 * r + sr;
+              if (row < cur.arows && c < cur.bcols) f = *reinterpret_cast<const v4f*>(cur.c + (int64_t)row * ldb + c * EB) + f;
+            }
+            store(__builtin_bit_cast(v4i, f), vo, (32 * i + 8 * r) * ldb);
+          }
+        }
+      wait_stage<63>();
+      issue_a(sb);
+    }
+    stores = OUT == MM_OUT_SAME;
+    if (nt.arows == 0) break;
+    cur = nt;
+    nt = walk.next(p, table);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no DMA may land after the LDS is given away
+}
+
 // The most row tiles of height h that any splits of M rows give: at most min(G + 1, M) runs of rows
 // (the groups and the rows behind them), each with less than one tile of padding.
 static int64_t row_tiles_bound(const MmArgs& p, int h) {
@@ -466,10 +834,35 @@ static bool vec_ok(const MmArgs& p) {
   return (addr & 15) == 0 && ((p.n | p.k | p.lda | p.ldb | p.ldc | p.b_stride | p.c_stride) & 7) == 0;
 }
 
+static int cu_count() {
+  int dev = 0, n = 0;
+  if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 8)
+    return 256;
+  return n;
+}
+
+template <int TYPE, int LAYOUT, int OUT>
+static hipError_t run_stream(const MmArgs& p, hipStream_t s) {
+  uint32_t* table = static_cast<uint32_t*>(p.table);
+  hipLaunchKernelGGL(gmm_table_kernel, dim3(1), dim3(1024), 0, s, p, 256, table, LAYOUT != MM_WGRAD);
+  if (hipError_t e = hipGetLastError()) return e;
+  auto* k = gmm_stream_kernel<TYPE, LAYOUT, OUT>;
+  hipLaunchKernelGGL(k, dim3((uint32_t)(cu_count() / 8 * 8)), dim3(512), 0, s, p, static_cast<const uint32_t*>(table));
+  return hipGetLastError();
+}
+static bool use_stream(const MmArgs& p) {
+  return GMM_STREAM;
+}
+size_t grouped_matmul_table_bytes(int G, int64_t M) {
+  const int64_t rows = (M + 255 * std::min<int64_t>((int64_t)G + 1, M)) / 256;
+  return 4 * (8 + (size_t)std::max<int64_t>(rows * kTableWords, 2 * (int64_t)G));
+}
+
 template <int TYPE, int LAYOUT, int OUT>
 static hipError_t run_sized(const MmArgs& p, hipStream_t s) {
   if (!vec_ok(p)) return run_any<TYPE, LAYOUT, OUT>(p, s);
-  return run_ring<TYPE, LAYOUT, OUT, GMM_T, GMM_WM, GMM_WN>(p, s);
+  if (use_stream(p)) return run_stream<TYPE, LAYOUT, OUT>(p, s);
+  return run_ring<TYPE, LAYOUT, OUT, 128, 2, 2>(p, s);
 }
 
 template <int TYPE>

@@ -186,7 +186,9 @@ struct MmArgs {
   int n, k;
   int zero_rest;          // FPROP, DGRAD: rows of C behind the last group are written as zeros
   uint32_t* flags;        // bits as SplitTables::flags
+  void* table;            // grouped_matmul_table_bytes of scratch
 };
+size_t grouped_matmul_table_bytes(int G, int64_t M);
 hipError_t launch_grouped_matmul(const MmArgs& a, hipStream_t s);
 
 // ----------------------------------------------------------------------------- group order

@@ -10,7 +10,11 @@ typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef int v2i __attribute__((ext_vector_type(2)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 
-// The two 16-bit operand types: conversions round to nearest even.
+// The two 16-bit operand types: conversions round to nearest even.  mma32_pair is c0 += a0 b, c1 += a1 b
+// where I < live (uniform), accumulators in place and the branch inside the asm: written
+// as a branch around the builtins, the two paths leave the accumulators in different registers and
+// the compiler copies and spills all of them.  The wait states it would put between a product and
+// a read of its result are then the caller's: mma32_settle before the first such read.
 template <int TYPE>
 struct Elem;
 template <>
@@ -20,6 +24,12 @@ struct Elem<MM_BF16> {
   static __device__ __forceinline__ uint32_t down2(float lo, float hi) { return pack_bf16x2(lo, hi); }
   static __device__ __forceinline__ v16f mma32(v4i a, v4i b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+  }
+  template <int I>
+  static __device__ __forceinline__ void mma32_pair(int live, v4i a0, v4i a1, v4i b, v16f& c0, v16f& c1) {
+    asm volatile("s_cmp_le_i32 %5, %6\n\ts_cbranch_scc1 L_mma_%=\n\t"
+                 "v_mfma_f32_32x32x16_bf16 %0, %2, %4, %0\n\tv_mfma_f32_32x32x16_bf16 %1, %3, %4, %1\n\t"
+                 "L_mma_%=:" : "+v"(c0), "+v"(c1) : "v"(a0), "v"(a1), "v"(b), "s"(live), "n"(I) : "scc");
   }
   static __device__ __forceinline__ v4f mma16(v4i a, v4i b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
@@ -35,10 +45,18 @@ struct Elem<MM_FP16> {
   static __device__ __forceinline__ v16f mma32(v4i a, v4i b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
   }
+  template <int I>
+  static __device__ __forceinline__ void mma32_pair(int live, v4i a0, v4i a1, v4i b, v16f& c0, v16f& c1) {
+    asm volatile("s_cmp_le_i32 %5, %6\n\ts_cbranch_scc1 L_mma_%=\n\t"
+                 "v_mfma_f32_32x32x16_f16 %0, %2, %4, %0\n\tv_mfma_f32_32x32x16_f16 %1, %3, %4, %1\n\t"
+                 "L_mma_%=:" : "+v"(c0), "+v"(c1) : "v"(a0), "v"(a1), "v"(b), "s"(live), "n"(I) : "scc");
+  }
   static __device__ __forceinline__ v4f mma16(v4i a, v4i b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
   }
 };
+
+__device__ __forceinline__ void mma32_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 // ----------------------------------------------------------------------------- split sizes
 // Every wave walks m_splits by itself, 64 groups at a time (no table, no launch before the
