@@ -448,46 +448,106 @@ __global__ __launch_bounds__(64 * NWM * NWN, 2) void gmm_ring_kernel(MmArgs p) {
 // blocks of its half that hold a row, and the last stage only the 16-deep steps that hold an
 // element, so that a group's last tile costs what it holds.
 //
-// Row tiles of the groups come from a table that gmm_table_kernel writes first: eight words
-// {group, the group's first tile, its tiles, its first row, its rows}; WGRAD reads each group's
-// {first row, rows}.
+// The groups come from a table that gmm_table_kernel writes first, largest first (with static shares the
+// small tiles then even out the workgroups' ends), rows cut into ceil(m / 256) tiles of equal height,
+// a multiple of 32: eight words {group, its first row tile in the table's order, its row tiles, first
+// row, rows, tile height} per row tile; WGRAD reads one such entry per group.
+//
+// A workgroup's share: rounds of one tile per workgroup; within a round an XCD takes consecutive
+// tiles, so that those resident together share A rows and B columns in its L2, and from round to
+// round a workgroup moves on by one within its XCD, as tiles of one group's full and last row
+// blocks alternate.
 constexpr int kTableWords = 8;
+constexpr int kTableSort = 1024;       // groups that one workgroup sorts; more keep their order
 
-__global__ __launch_bounds__(1024) void gmm_table_kernel(MmArgs p, int h, uint32_t* table, bool rows) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t done = 0, tiles = 0;
-  for (int base = 0; base <= p.G; base += 64) {
-    const int g = base + lane;
+// n / d for any n < 2^32: the product with floor((2^32 - 1) / d) is at most two below.
+struct UDiv {
+  uint32_t d, m;
+  UDiv() = default;
+  explicit UDiv(uint32_t v) : d(v), m(0xFFFFFFFFu / v) {}
+  __device__ __forceinline__ uint32_t div(uint32_t n, uint32_t& r) const {
+    uint32_t q = (uint32_t)(((uint64_t)n * m) >> 32);
+    r = n - q * d;
+    if (r >= d) { ++q; r -= d; }
+    if (r >= d) { ++q; r -= d; }
+    return q;
+  }
+};
+struct StreamArgs {
+  MmArgs p;
+  uint32_t* table;
+  UDiv ntn, sweep, per;  // column tiles; tiles of a four-row sweep; WGRAD: an XCD's tiles of a group
+  uint32_t ntm, tpg;     // WGRAD: row tiles and tiles of a group
+};
+
+__global__ __launch_bounds__(1024) void gmm_table_kernel(StreamArgs args, bool by_rows) {
+  const MmArgs& p = args.p;
+  __shared__ uint32_t s_rows[kTableSort], s_row0[kTableSort];
+  __shared__ uint16_t s_group[kTableSort];
+  uint32_t* table = args.table;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = p.G + (by_rows && p.zero_rest ? 1 : 0);      // the rows behind the last group are group G
+  const bool sort = n <= kTableSort;
+  if (wave == 15) {
+    const uint32_t f = wave_split_flags(p.m_splits, p.G, p.M, lane);
+    if (lane == 0) *p.flags = f;
+  }
+  auto spans = [&](int base, uint32_t& done) {
     Span s = wave_spans(p.m_splits, p.G, (uint32_t)p.M, base, lane, done);
-    if (g == p.G) s.end = p.zero_rest ? (uint32_t)p.M : s.start;       // the rows behind the last group
-    if (g > p.G) s.end = s.start;
-    const uint32_t m = s.end - s.start, n = (m + h - 1) / h;
-    const uint32_t incl = wave_incl_add(n, lane, 0x7FFFFFFFu);
-    if (!rows) {
-      if (wave == 0 && g < p.G) {
-        table[8 + 2 * g] = s.start;
-        table[8 + 2 * g + 1] = m;
+    if (base + lane == p.G && n > p.G) s.end = (uint32_t)p.M;
+    if (base + lane >= n) s.end = s.start;
+    return s;
+  };
+  if (sort) {
+    uint32_t done = 0;
+    for (int base = 0; base < n; base += 64) {
+      const Span s = spans(base, done);
+      if (wave == 0 && base + lane < n) {
+        s_row0[base + lane] = s.start;
+        s_rows[base + lane] = s.end - s.start;
       }
-    } else if (g <= p.G) {
-      const uint32_t first = tiles + incl - n;
-      for (uint32_t t = wave; t < n; t += 16) {
-        uint32_t* e = table + 8 + (uint64_t)(first + t) * kTableWords;
-        e[0] = (uint32_t)g;
-        e[1] = first;
-        e[2] = n;
-        e[3] = s.start;
-        e[4] = m;
+    }
+    __syncthreads();
+    if (tid < n) {
+      const uint32_t mine = s_rows[tid];
+      int rank = 0;
+      for (int i = 0; i < n; ++i) rank += s_rows[i] > mine || (s_rows[i] == mine && i < tid);
+      s_group[rank] = (uint16_t)tid;
+    }
+    __syncthreads();
+  }
+  uint32_t done = 0, tiles = 0;
+  for (int base = 0; base < n; base += 64) {
+    const int at = base + lane;
+    uint32_t g = at, row0 = 0, m = 0;
+    if (sort) {
+      if (at < n) {
+        g = s_group[at];
+        row0 = s_row0[g];
+        m = s_rows[g];
       }
+    } else {
+      const Span s = spans(base, done);
+      row0 = s.start;
+      m = s.end - s.start;
+    }
+    const uint32_t nt = by_rows ? (m + 255) / 256 : 1;
+    const uint32_t count = at < n ? nt : 0;
+    const uint32_t incl = wave_incl_add(count, lane, 0x7FFFFFFFu);
+    const uint32_t first = tiles + incl - count;
+    const uint32_t h = by_rows && nt ? ((m + nt - 1) / nt + 31) / 32 * 32 : 0;
+    for (uint32_t t = wave; t < count; t += 16) {
+      uint32_t* e = table + 8 + (uint64_t)(first + t) * kTableWords;
+      e[0] = g;
+      e[1] = first;
+      e[2] = nt;
+      e[3] = row0;
+      e[4] = m;
+      e[5] = h;
     }
     tiles += (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
   }
-  if (wave == 0) {
-    const uint32_t f = wave_split_flags(p.m_splits, p.G, p.M, lane);
-    if (lane == 0) {
-      *p.flags = f;
-      table[0] = tiles;
-    }
-  }
+  if (tid == 0) table[0] = tiles;
 }
 
 // One output tile (uniform values).
@@ -501,72 +561,62 @@ struct StreamTile {
 
 template <int LAYOUT, int OUT, int T>
 struct TileWalk {
-  uint32_t at, step, end;  // positions in this workgroup's list
-  uint32_t x;              // XCD
-  // The next tile of the list.
-  __device__ __forceinline__ void init(const MmArgs& p, const uint32_t* __restrict__ table) {
-    const uint32_t workers = gridDim.x >> 3;
+  uint32_t round, rounds, x, w, nw, total;
+  __device__ __forceinline__ void init(const StreamArgs& s) {
+    nw = gridDim.x >> 3;
     x = blockIdx.x & 7;
-    if (LAYOUT == MM_WGRAD) {
-      const uint32_t tpg = ((p.n + T - 1) / T) * ((p.k + T - 1) / T);
-      if (tpg >= 64) {                   // XCD x takes the x-th eighth of every group's tiles
-        at = blockIdx.x >> 3;
-        step = workers;
-        end = (tpg + 7) / 8 * p.G;
-      } else {
-        at = blockIdx.x;
-        step = gridDim.x;
-        end = tpg * p.G;
-      }
-    } else {                             // XCD x takes the x-th eighth of all tiles
-      const uint32_t total = table[0] * ((p.n + T - 1) / T), per = (total + 7) / 8;
-      at = x * per + (blockIdx.x >> 3);
-      step = workers;
-      end = min((x + 1) * per, total);
-    }
+    w = blockIdx.x >> 3;
+    round = 0;
+    total = LAYOUT == MM_WGRAD ? (s.tpg >= 64 ? s.per.d : s.tpg) * (uint32_t)s.p.G : s.table[0] * s.ntn.d;
+    // WGRAD with many tiles a group: every XCD has the same count of tiles of its own
+    const uint32_t each = LAYOUT == MM_WGRAD && s.tpg >= 64 ? nw : nw * 8;
+    rounds = (total + each - 1) / each;
   }
-  __device__ __forceinline__ StreamTile next(const MmArgs& p, const uint32_t* __restrict__ table) {
+  // The next tile of this workgroup.
+  __device__ __forceinline__ StreamTile next(const StreamArgs& s) {
     constexpr uint32_t GR = 4;           // four row tiles to a column sweep
+    const MmArgs& p = s.p;
     StreamTile t{};
-    while (at < end) {
-      const uint32_t l = at;
-      at += step;
+    while (round < rounds) {
+      const bool own = LAYOUT == MM_WGRAD && s.tpg >= 64;
+      const uint32_t l = (own ? round : round * 8 + x) * nw + w;
+      ++round;
+      w = w + 1 == nw ? 0 : w + 1;
+      if (l >= total) continue;
+      uint32_t i, rem;
+      const uint32_t* e;
       if (LAYOUT == MM_WGRAD) {
-        const uint32_t ntm = (p.n + T - 1) / T, ntn = (p.k + T - 1) / T, tpg = ntm * ntn;
-        uint32_t g, i;
-        if (tpg >= 64) {
-          const uint32_t per = (tpg + 7) / 8;
-          g = l / per;
-          i = x * per + l % per;
-          if (i >= tpg) continue;
-        } else {
-          g = l / tpg;
-          i = l % tpg;
-        }
-        const uint32_t row0 = table[8 + 2 * g], m = table[8 + 2 * g + 1];
-        if (OUT == MM_OUT_ACC32 && m == 0) continue;
-        const uint32_t grp = i / (GR * ntn), rem = i % (GR * ntn), rh = min(GR, ntm - grp * GR);
-        const int tm = (int)((grp * GR + rem % rh) * T), col0 = (int)(rem / rh * T);
-        t.a = static_cast<const uint16_t*>(p.a) + (int64_t)row0 * p.lda + tm;
+        uint32_t q = s.per.div(l, i);
+        if (own) i += x * s.per.d;
+        if (i >= s.tpg) continue;
+        e = s.table + 8 + q * kTableWords;
+      } else {
+        e = s.table + 8 + (uint64_t)s.ntn.div(l, i) * kTableWords;
+        i = l - e[1] * s.ntn.d;
+      }
+      const uint32_t g = e[0], row0 = e[3], m = e[4];
+      const uint32_t ntm = LAYOUT == MM_WGRAD ? s.ntm : e[2];
+      if (OUT == MM_OUT_ACC32 && m == 0) continue;
+      const uint32_t grp = s.sweep.div(i, rem), rh = min(GR, ntm - grp * GR);
+      const uint32_t col = rh == 4 ? rem >> 2 : rh == 3 ? (uint32_t)(((uint64_t)rem * 0xAAAAAAABu) >> 33) : rh == 2 ? rem >> 1 : rem;
+      const uint32_t tm = grp * GR + rem - col * rh;
+      const int col0 = (int)(col * T);
+      if (LAYOUT == MM_WGRAD) {
+        const int r = (int)(tm * T);
+        t.a = static_cast<const uint16_t*>(p.a) + (int64_t)row0 * p.lda + r;
         t.b = static_cast<const uint16_t*>(p.b) + (int64_t)row0 * p.ldb + col0;
-        t.c = static_cast<uint8_t*>(p.c) + ((int64_t)g * p.c_stride + (int64_t)tm * p.ldc + col0) * (OUT == MM_OUT_SAME ? 2 : 4);
-        t.arows = min(p.n - tm, T);
+        t.c = static_cast<uint8_t*>(p.c) + ((int64_t)g * p.c_stride + (int64_t)r * p.ldc + col0) * (OUT == MM_OUT_SAME ? 2 : 4);
+        t.arows = min(p.n - r, T);
         t.bcols = min(p.k - col0, T);
         t.kn = (int)m;
       } else {
-        const uint32_t ntn = (p.n + T - 1) / T;
-        const uint32_t* e = table + 8 + (uint64_t)(l / ntn) * kTableWords;
-        const uint32_t g = e[0], ntm = e[2], row0 = e[3], m = e[4];
-        const uint32_t i = l - e[1] * ntn;
-        const uint32_t grp = i / (GR * ntn), rem = i % (GR * ntn), rh = min(GR, ntm - grp * GR);
-        const uint32_t tm = (grp * GR + rem % rh) * T;
-        const int col0 = (int)(rem / rh * T);
-        const int64_t row = (int64_t)row0 + tm;
+        const uint32_t h = e[5];
+        const int64_t row = (int64_t)row0 + tm * h;
         t.a = static_cast<const uint16_t*>(p.a) + row * p.lda;
         t.b = static_cast<const uint16_t*>(p.b);
         if ((int)g < p.G) t.b += (int64_t)g * p.b_stride + (LAYOUT == MM_FPROP ? (int64_t)col0 * p.ldb : (int64_t)col0);
         t.c = static_cast<uint8_t*>(p.c) + (row * p.ldc + col0) * 2;
-        t.arows = (int)min(m - tm, (uint32_t)T);
+        t.arows = (int)min(m - tm * h, h);
         t.bcols = min(p.n - col0, T);
         t.kn = (int)g < p.G ? p.k : 0;
       }
@@ -594,7 +644,8 @@ struct StreamFeed : Feed<TR, T, NT> {
 };
 
 template <int TYPE, int LAYOUT, int OUT>
-__global__ __launch_bounds__(512, 2) void gmm_stream_kernel(MmArgs p, const uint32_t* __restrict__ table) {
+__global__ __launch_bounds__(512, 2) void gmm_stream_kernel(StreamArgs args) {
+  const MmArgs& p = args.p;
   using E = Elem<TYPE>;
   constexpr int T = 256, NWN = 4, NT = 512, SLOT = T * 128;
   constexpr bool AT = LAYOUT == MM_WGRAD, BT = LAYOUT != MM_FPROP;
@@ -607,10 +658,10 @@ __global__ __launch_bounds__(512, 2) void gmm_stream_kernel(MmArgs p, const uint
   const int wm = wave / NWN, wn = wave % NWN;
 
   TileWalk<LAYOUT, OUT, T> walk;
-  walk.init(p, table);
-  StreamTile cur = walk.next(p, table);
+  walk.init(args);
+  StreamTile cur = walk.next(args);
   if (cur.arows == 0) return;
-  StreamTile nt = walk.next(p, table);
+  StreamTile nt = walk.next(args);
 
   StreamFeed<AT, T, NT> fa;
   StreamFeed<BT, T, NT> fb;
@@ -791,7 +842,7 @@ __global__ __launch_bounds__(512, 2) void gmm_stream_kernel(MmArgs p, const uint
     stores = OUT == MM_OUT_SAME;
     if (nt.arows == 0) break;
     cur = nt;
-    nt = walk.next(p, table);
+    nt = walk.next(args);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no DMA may land after the LDS is given away
 }
@@ -843,11 +894,19 @@ static int cu_count() {
 
 template <int TYPE, int LAYOUT, int OUT>
 static hipError_t run_stream(const MmArgs& p, hipStream_t s) {
-  uint32_t* table = static_cast<uint32_t*>(p.table);
-  hipLaunchKernelGGL(gmm_table_kernel, dim3(1), dim3(1024), 0, s, p, 256, table, LAYOUT != MM_WGRAD);
+  constexpr bool W = LAYOUT == MM_WGRAD;
+  StreamArgs a;
+  a.p = p;
+  a.table = static_cast<uint32_t*>(p.table);
+  a.ntn = UDiv((uint32_t)(((W ? p.k : p.n) + 255) / 256));
+  a.sweep = UDiv(4 * a.ntn.d);
+  a.ntm = W ? (uint32_t)((p.n + 255) / 256) : 0;
+  a.tpg = a.ntm * a.ntn.d;
+  a.per = UDiv(W ? (a.tpg >= 64 ? (a.tpg + 7) / 8 : a.tpg) : 1);
+  hipLaunchKernelGGL(gmm_table_kernel, dim3(1), dim3(1024), 0, s, a, !W);
   if (hipError_t e = hipGetLastError()) return e;
   auto* k = gmm_stream_kernel<TYPE, LAYOUT, OUT>;
-  hipLaunchKernelGGL(k, dim3((uint32_t)(cu_count() / 8 * 8)), dim3(512), 0, s, p, static_cast<const uint32_t*>(table));
+  hipLaunchKernelGGL(k, dim3((uint32_t)(cu_count() / 8 * 8)), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 static bool use_stream(const MmArgs& p) {
@@ -855,7 +914,7 @@ static bool use_stream(const MmArgs& p) {
 }
 size_t grouped_matmul_table_bytes(int G, int64_t M) {
   const int64_t rows = (M + 255 * std::min<int64_t>((int64_t)G + 1, M)) / 256;
-  return 4 * (8 + (size_t)std::max<int64_t>(rows * kTableWords, 2 * (int64_t)G));
+  return 4 * (8 + (size_t)std::max<int64_t>(rows, G) * kTableWords);
 }
 
 template <int TYPE, int LAYOUT, int OUT>
