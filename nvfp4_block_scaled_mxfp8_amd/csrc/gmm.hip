@@ -1,7 +1,7 @@
 // Grouped products on bf16 / fp16 operands, rows grouped by expert with ragged sizes:
 //   FPROP  y[r, :] = x[r, :] w[g]^T      DGRAD  dx[r, :] = dy[r, :] w[g]      WGRAD  dw[g] = dy_g^T x_g
 // accumulated in fp32 on the matrix cores and rounded once.  The split sizes are read on the
-// device by every workgroup (mm_common.h).
+// device (mm_common.h).
 #include "mm_common.h"
 
 #include <algorithm>
@@ -9,118 +9,35 @@
 
 namespace gmlp {
 
-#ifndef GMM_STREAM
-#define GMM_STREAM true
-#endif
-
-// ----------------------------------------------------------------------------- any alignment
-// 64 x 64 tile, 4 waves of 32 x 32, 32-deep stages through registers into LDS, every element
-// checked.  Takes every stride, size and alignment; what the 16-byte loads of the other kernels
-// cannot read runs here.
-constexpr int ST = 64, SK = 32, SLD = SK + 8;
-
-template <int TYPE, int LAYOUT, int OUT>
-__global__ __launch_bounds__(256) void gmm_any_kernel(MmArgs p) {
-  using E = Elem<TYPE>;
-  __shared__ uint16_t sa[ST * SLD], sb[ST * SLD];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if (blockIdx.x == 0 && wave == 0) {
-    const uint32_t f = wave_split_flags(p.m_splits, p.G, p.M, lane);
-    if (lane == 0) *p.flags = f;
-  }
-  const uint16_t* A = static_cast<const uint16_t*>(p.a);
-  const uint16_t* B = static_cast<const uint16_t*>(p.b);
-  int64_t crow0, kn;                 // first C row of the tile, contraction length
-  int arows, bcols, col0;            // valid rows and columns of the tile, first column
-  if (LAYOUT == MM_WGRAD) {
-    const uint32_t ntm = (p.n + ST - 1) / ST, ntn = (p.k + ST - 1) / ST;
-    const int g = (int)(blockIdx.x / (ntm * ntn));
-    const uint32_t t = blockIdx.x % (ntm * ntn);
-    const RowTile rt = find_group_rows(p.m_splits, p.G, (uint32_t)p.M, g, lane);
-    const int tm = t % ntm * ST;
-    col0 = t / ntm * ST;
-    arows = min(ST, p.n - tm);
-    bcols = min(ST, p.k - col0);
-    kn = rt.m;
-    A += (int64_t)rt.row0 * p.lda + tm;
-    B += (int64_t)rt.row0 * p.ldb + col0;
-    crow0 = tm;
-    p.c = static_cast<uint8_t*>(p.c) + (int64_t)g * p.c_stride * (OUT == MM_OUT_SAME ? 2 : 4);
-    if (OUT == MM_OUT_ACC32 && kn == 0) return;
-  } else {
-    const uint32_t ntn = (p.n + ST - 1) / ST;
-    const RowTile rt = find_row_tile(p.m_splits, p.G, (uint32_t)p.M, ST, ntn, p.zero_rest, blockIdx.x, lane);
-    if (rt.g < 0) return;
-    const uint32_t tm = rt.t / ntn * ST;
-    col0 = rt.t % ntn * ST;
-    arows = min((uint32_t)ST, rt.m - tm);
-    bcols = min(ST, p.n - col0);
-    kn = rt.g < p.G ? p.k : 0;
-    crow0 = (int64_t)rt.row0 + tm;
-    A += crow0 * p.lda;
-    if (rt.g < p.G) B += (int64_t)rt.g * p.b_stride + (LAYOUT == MM_FPROP ? (int64_t)col0 * p.ldb : (int64_t)col0);
-  }
-  constexpr bool AT = LAYOUT == MM_WGRAD, BT = LAYOUT != MM_FPROP;     // contraction along the rows in memory
-  auto load = [&](const uint16_t* src, int64_t ld, bool tr, int valid, int64_t k0, uint16_t* dst) {
-    if (!tr) {
-      const int r = tid >> 2, c = (tid & 3) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        dst[r * SLD + c + i] = (r < valid && k0 + c + i < kn) ? src[r * ld + k0 + c + i] : (uint16_t)0;
-    } else {
-      const int r = tid >> 3, c = (tid & 7) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        dst[(c + i) * SLD + r] = (c + i < valid && k0 + r < kn) ? src[(k0 + r) * ld + c + i] : (uint16_t)0;
-    }
-  };
-  v16f acc = {};
-  const int wm = wave >> 1, wn = wave & 1;
-  for (int64_t k0 = 0; k0 < kn; k0 += SK) {
-    load(A, p.lda, AT, arows, k0, sa);
-    load(B, p.ldb, BT, bcols, k0, sb);
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < SK; s += 16) {
-      const int o = (lane & 31) * SLD + s + 8 * (lane >> 5);
-      const v4i fa = *reinterpret_cast<const v4i*>(sa + wm * 32 * SLD + o);
-      const v4i fb = *reinterpret_cast<const v4i*>(sb + wn * 32 * SLD + o);
-      acc = E::mma32(fa, fb, acc);
-    }
-    __syncthreads();
-  }
-  // lane l, element i: row 8 (i / 4) + 4 (l / 32) + i % 4, column l % 32
-  const int c = wn * 32 + (lane & 31);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = wm * 32 + 8 * (i / 4) + 4 * (lane >> 5) + (i & 3);
-    if (r >= arows || c >= bcols) continue;
-    const int64_t o = (crow0 + r) * p.ldc + col0 + c;
-    if (OUT == MM_OUT_SAME) static_cast<uint16_t*>(p.c)[o] = E::down(acc[i]);
-    else if (OUT == MM_OUT_FP32) static_cast<float*>(p.c)[o] = acc[i];
-    else static_cast<float*>(p.c)[o] += acc[i];
-  }
-}
 
 // ----------------------------------------------------------------------------- ring kernel
-// Tiles of TM x TN (TM == TN), NWM x NWN waves, contraction in stages of 64.  A stage is two units,
-// A's and B's 64-deep slabs of the tile (TM x 128 bytes each), and the units of all stages run
-// through a ring of five LDS slots filled by buffer-to-LDS DMA: while stage s is read, both units
-// of stage s + 1 and A of s + 2 are on their way.  One barrier a stage: at it every wave has the
-// stage's last fragments in registers and its share of the next stage's units has landed, so the
-// two slots read last are refilled and the next stage's first fragments read while the last
-// sixteen-deep step's MFMAs run.
+// 128 x 128 tiles, 2 x 2 waves of 64 x 64, contraction in stages of 64.  A stage is two units, A's
+// and B's 64-deep slabs of the tile (128 x 128 bytes each), and the units of all stages run through a
+// ring of five LDS slots filled by buffer-to-LDS DMA: while stage s is read, both units of stage
+// s + 1 and A of s + 2 are on their way.  One barrier a stage: at it every wave has the stage's last
+// fragments in registers and its share of the next stage's units has landed, so the two slots read
+// last are refilled and the next stage's first fragments read while the last sixteen-deep step's
+// MFMAs run.  80 KB: two workgroups per CU, whose ends and beginnings overlap.
 //
 // A unit whose operand is contiguous along the contraction (x, dy and FPROP's w) holds rows of 128
 // bytes, 16-byte chunks XOR-swizzled by row so that 16 consecutive rows meet all 16 bank groups;
 // fragments are ds_read_b128.  A unit whose operand has the contraction along its rows in memory
-// (DGRAD's w, both of WGRAD's) holds 64 rows of TM elements as they are in memory; its fragments
+// (DGRAD's w, both of WGRAD's) holds 64 rows of T elements as they are in memory; its fragments
 // are transposed on the way out by ds_read_b64_tr_b16 (16 lanes read four rows of 16 elements and
 // get one column of four each), chunks XORed by (row % 4) so that the four rows fall into four
-// different 64-byte windows of the banks.
+// different 64-byte windows of the banks.  Conflicts: 1% of the LDS cycles (counter).
 //
 // Rows, columns and contraction past the operand's end read as zero by the buffer range check;
 // a contraction tail inside a row (k % 64) is cut per lane in the last stage.
+//
+// Where rows are not multiples of 16 bytes the DMA cannot read them: the units then come through
+// registers into two pairs of slots, 16 bytes per lane from any address, the ragged chunk at a
+// row's end by element.
+//
+// Few tiles with a long contraction (PART): the contraction is cut over blockIdx.y, each part's
+// fp32 tile goes to scratch, and gmm_sum_kernel adds the parts in order.
+constexpr int MM_OUT_PART = 3;
+
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 
 __device__ __forceinline__ int sgpr(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -236,23 +153,78 @@ struct Frags {
 
 #define MM_FENCE() __builtin_amdgcn_sched_barrier(0)
 
-template <int TYPE, int LAYOUT, int OUT, int T, int NWM, int NWN>
-__global__ __launch_bounds__(64 * NWM * NWN, 2) void gmm_ring_kernel(MmArgs p) {
+// Eight elements from any even address, `valid` of which exist.
+__device__ __forceinline__ v4i load8_any(const uint16_t* p, int valid) {
+  v4i v{0, 0, 0, 0};
+  if (valid >= 8) {
+    __builtin_memcpy(&v, p, 16);
+  } else {
+    uint32_t w[4] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+    v = v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+  }
+  return v;
+}
+
+// The same units as a Feed's, through registers.
+template <bool TR, int T, int NT>
+struct Staged {
+  static constexpr int N = T * 128 / (NT * 16);
+  const uint16_t* ptr;          // this thread's chunk of the next unit
+  int64_t ld;
+  int left, valid, row, chunk;
+  v4i v[N];
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld_, int valid_, int64_t kn, int tid) {
+    ld = ld_;
+    valid = valid_;
+    left = (int)min(kn, (int64_t)0x40000000);
+    if (!TR) {
+      row = tid >> 3;
+      chunk = (tid & 7) ^ ((row >> 1) & 7);
+    } else {
+      row = tid / (T / 8);
+      chunk = (tid % (T / 8)) ^ ((row & 3) << 2);
+    }
+    ptr = p + row * ld + chunk * 8;
+  }
+  __device__ __forceinline__ void load() {
+    constexpr int ROWS = TR ? NT / (T / 8) : NT / 8;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = row + i * ROWS;
+      const int n = TR ? (r < left ? valid - 8 * chunk : 0) : (r < valid ? left - 8 * chunk : 0);
+      v[i] = load8_any(ptr + i * ROWS * ld, n);
+    }
+    ptr += TR ? 64 * ld : 64;
+    left -= 64;
+  }
+  __device__ __forceinline__ void store(uint32_t slot, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) *(__attribute__((address_space(3))) v4i*)(uintptr_t)(slot + (i * NT + tid) * 16) = v[i];
+  }
+};
+
+template <int TYPE, int LAYOUT, int OUT, bool VEC>
+__global__ __launch_bounds__(256, 2) void gmm_ring_kernel(MmArgs p) {
   using E = Elem<TYPE>;
-  constexpr int NT = 64 * NWM * NWN, SLOT = T * 128;
+  constexpr int T = 128, NWN = 2, NT = 256, SLOT = T * 128;
   constexpr bool AT = LAYOUT == MM_WGRAD, BT = LAYOUT != MM_FPROP;
-  constexpr int WM = T / NWM, WN = T / NWN, NA = WM / 32, NB = WN / 32;
-  static_assert(WN == 64, "the epilogue stages rows of 64 columns");
-  __shared__ __align__(1024) uint8_t lds[5 * SLOT];
+  constexpr int WM = 64, WN = 64, NA = WM / 32, NB = WN / 32;
+  __shared__ __align__(1024) uint8_t lds[(VEC ? 5 : 4) * SLOT];
   const int tid = threadIdx.x, lane = tid & 63, wave = sgpr(tid >> 6);
-  if (blockIdx.x == 0 && wave == 0) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) {
     const uint32_t f = wave_split_flags(p.m_splits, p.G, p.M, lane);
     if (lane == 0) *p.flags = f;
   }
   const uint16_t* A = static_cast<const uint16_t*>(p.a);
   const uint16_t* B = static_cast<const uint16_t*>(p.b);
-  int64_t crow0, kn;
+  constexpr int EB = OUT == MM_OUT_SAME ? 2 : 4;
+  uint8_t* C = static_cast<uint8_t*>(p.c);
+  int64_t crow0, kn, ldc = p.ldc;
   int arows, bcols, col0, ncols;
+  constexpr uint32_t GR = 4;             // four row tiles to a column sweep
   if (LAYOUT == MM_WGRAD) {
     const uint32_t ntm = (p.n + T - 1) / T, ntn = (p.k + T - 1) / T, tpg = ntm * ntn;
     uint32_t g, t;
@@ -267,7 +239,6 @@ __global__ __launch_bounds__(64 * NWM * NWN, 2) void gmm_ring_kernel(MmArgs p) {
       if ((int)g >= p.G) return;
     }
     const RowTile rt = find_group_rows(p.m_splits, p.G, (uint32_t)p.M, (int)g, lane);
-    constexpr uint32_t GR = 4;           // four row tiles to a column sweep
     const uint32_t grp = t / (GR * ntn), rem = t % (GR * ntn), rh = min(GR, ntm - grp * GR);
     const int tm = (int)((grp * GR + rem % rh) * T);
     col0 = (int)(rem / rh * T);
@@ -278,7 +249,7 @@ __global__ __launch_bounds__(64 * NWM * NWN, 2) void gmm_ring_kernel(MmArgs p) {
     A += (int64_t)rt.row0 * p.lda + tm;
     B += (int64_t)rt.row0 * p.ldb + col0;
     crow0 = tm;
-    p.c = static_cast<uint8_t*>(p.c) + (int64_t)g * p.c_stride * (OUT == MM_OUT_SAME ? 2 : 4);
+    C += (int64_t)g * (OUT == MM_OUT_PART ? (int64_t)p.n * p.k : p.c_stride) * EB;
   } else {
     const uint32_t ntn = (p.n + T - 1) / T;
     const uint32_t total = row_tiles_total(p.m_splits, p.G, (uint32_t)p.M, T, ntn, p.zero_rest, lane);
@@ -286,7 +257,6 @@ __global__ __launch_bounds__(64 * NWM * NWN, 2) void gmm_ring_kernel(MmArgs p) {
     if (l >= per) return;
     const RowTile rt = find_row_tile(p.m_splits, p.G, (uint32_t)p.M, T, ntn, p.zero_rest, (blockIdx.x & 7) * per + l, lane);
     if (rt.g < 0) return;
-    constexpr uint32_t GR = 4;
     const uint32_t ntm = (rt.m + T - 1) / T;
     const uint32_t grp = rt.t / (GR * ntn), rem = rt.t % (GR * ntn), rh = min(GR, ntm - grp * GR);
     const uint32_t tm = (grp * GR + rem % rh) * T;
@@ -297,6 +267,15 @@ __global__ __launch_bounds__(64 * NWM * NWN, 2) void gmm_ring_kernel(MmArgs p) {
     crow0 = (int64_t)rt.row0 + tm;
     A += crow0 * p.lda;
     if (rt.g < p.G) B += (int64_t)rt.g * p.b_stride + (LAYOUT == MM_FPROP ? (int64_t)col0 * p.ldb : (int64_t)col0);
+  }
+  if (OUT == MM_OUT_PART) {              // this part's stages
+    const int64_t nst = (kn + 63) / 64, z = blockIdx.y;
+    const int64_t k0 = 64 * (nst * z / p.parts), k1 = min(kn, 64 * (nst * (z + 1) / p.parts));
+    A += AT ? k0 * p.lda : k0;
+    B += BT ? k0 * p.ldb : k0;
+    kn = max(k1 - k0, (int64_t)0);
+    ldc = ncols;
+    C = reinterpret_cast<uint8_t*>(p.part + z * p.part_stride) + (LAYOUT == MM_WGRAD ? C - static_cast<uint8_t*>(p.c) : 0);
   }
   arows = sgpr(min(arows, T));
   bcols = sgpr(min(ncols - col0, T));
@@ -311,75 +290,108 @@ __global__ __launch_bounds__(64 * NWM * NWN, 2) void gmm_ring_kernel(MmArgs p) {
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
   const int nst = sgpr((int)((kn + 63) / 64));
   if (nst > 0) {
-    Feed<AT, T, NT> fa;
-    Feed<BT, T, NT> fb;
-    fa.init(A, p.lda, arows, kn, tid);
-    fb.init(B, p.ldb, bcols, kn, tid);
     Frags<AT, T, NA> ra;
     Frags<BT, T, NB> rb;
     ra.init(wm * WM, lane);
     rb.init(wn * WN, lane);
-    constexpr int P = Feed<AT, T, NT>::kDma;
-    fa.issue_all(lds0 + 0 * SLOT, wave);
-    fb.issue_all(lds0 + 1 * SLOT, wave);
-    fa.issue_all(lds0 + 2 * SLOT, wave);
-    fb.issue_all(lds0 + 3 * SLOT, wave);
-    fa.issue_all(lds0 + 4 * SLOT, wave);
-    uint32_t ua = lds0, ub = lds0 + SLOT;       // the stage's units
-    const uint32_t end = lds0 + 5 * SLOT;
     v4i a[2][NA], b[2][NB];
     constexpr int NR = NA + NB, NM = NA * NB;
-    // fragment reads in the order the MFMAs want them: b0 a0 b1 a1 a2 ...
+    // fragment reads in the order the MFMAs want them: b0 a0 b1 a1
     auto read_one = [&](int step, int n, v4i* xa, v4i* xb) {
-      if (n < 2 * NB && !(n & 1)) xb[n / 2] = rb.read(step, n / 2);
-      else if (n < 2 * NB) xa[n / 2] = ra.read(step, n / 2);
-      else xa[n - NB] = ra.read(step, n - NB);
+      if (!(n & 1)) xb[n / 2] = rb.read(step, n / 2);
+      else xa[n / 2] = ra.read(step, n / 2);
     };
-    wait_stage<3 * P>();
-    ra.enter(ua);
-    rb.enter(ub);
+    static_assert(NA == 2 && NB == 2, "reads alternate between the operands");
+    if constexpr (VEC) {
+      Feed<AT, T, NT> fa;
+      Feed<BT, T, NT> fb;
+      fa.init(A, p.lda, arows, kn, tid);
+      fb.init(B, p.ldb, bcols, kn, tid);
+      constexpr int P = Feed<AT, T, NT>::kDma;
+      fa.issue_all(lds0 + 0 * SLOT, wave);
+      fb.issue_all(lds0 + 1 * SLOT, wave);
+      fa.issue_all(lds0 + 2 * SLOT, wave);
+      fb.issue_all(lds0 + 3 * SLOT, wave);
+      fa.issue_all(lds0 + 4 * SLOT, wave);
+      uint32_t ua = lds0, ub = lds0 + SLOT;       // the stage's units
+      const uint32_t end = lds0 + 5 * SLOT;
+      wait_stage<3 * P>();
+      ra.enter(ua);
+      rb.enter(ub);
 #pragma unroll
-    for (int n = 0; n < NR; ++n) read_one(0, n, a[0], b[0]);
-    for (int s = 0; s < nst; ++s) {
+      for (int n = 0; n < NR; ++n) read_one(0, n, a[0], b[0]);
+      for (int s = 0; s < nst; ++s) {
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const int cur = ks & 1, nxt = cur ^ 1;
-        uint32_t da = 0, db = 0;
-        if (ks == 3) {
-          wait_stage<P>();
-          da = ub;                                // A of stage s + 3 goes into B's slot,
-          db = ua;                                // B of s + 2 into A's
-          ua += 2 * SLOT;
-          ub += 2 * SLOT;
-          if (ua >= end) ua -= 5 * SLOT;
-          if (ub >= end) ub -= 5 * SLOT;
-          ra.enter(ua);
-          rb.enter(ub);
-          fb.next();
-          fa.next();
-        }
-        MM_FENCE();
-        // the transposed product: a lane then holds consecutive columns of one row.  One read of the
-        // next step behind each MFMA, and at the stage's end its DMAs.
-#pragma unroll
-        for (int m = 0; m < NM; ++m) {
-          const int i = m / NB, j = m % NB;
-          acc[i][j] = E::mma32(b[cur][j], a[cur][i], acc[i][j]);
-          MM_FENCE();
-          if (m < NR) read_one(ks < 3 ? ks + 1 : 0, m, a[nxt], b[nxt]);
+        for (int ks = 0; ks < 4; ++ks) {
+          const int cur = ks & 1, nxt = cur ^ 1;
+          uint32_t da = 0, db = 0;
           if (ks == 3) {
-            constexpr int D = (2 * P + NM - 1) / NM;
-#pragma unroll
-            for (int d = m * D; d < (m + 1) * D && d < 2 * P; ++d) {
-              if (d < P) fb.issue(d, db, wave);
-              else fa.issue(d - P, da, wave);
-            }
+            wait_stage<P>();
+            da = ub;                                // A of stage s + 3 goes into B's slot,
+            db = ua;                                // B of s + 2 into A's
+            ua += 2 * SLOT;
+            ub += 2 * SLOT;
+            if (ua >= end) ua -= 5 * SLOT;
+            if (ub >= end) ub -= 5 * SLOT;
+            ra.enter(ua);
+            rb.enter(ub);
+            fb.next();
+            fa.next();
           }
           MM_FENCE();
+          // the transposed product: a lane then holds consecutive columns of one row.  One read of the
+          // next step behind each MFMA, and at the stage's end its DMAs.
+#pragma unroll
+          for (int m = 0; m < NM; ++m) {
+            const int i = m / NB, j = m % NB;
+            acc[i][j] = E::mma32(b[cur][j], a[cur][i], acc[i][j]);
+            MM_FENCE();
+            if (m < NR) read_one(ks < 3 ? ks + 1 : 0, m, a[nxt], b[nxt]);
+            if (ks == 3) {
+              constexpr int D = (2 * P + NM - 1) / NM;
+#pragma unroll
+              for (int d = m * D; d < (m + 1) * D && d < 2 * P; ++d) {
+                if (d < P) fb.issue(d, db, wave);
+                else fa.issue(d - P, da, wave);
+              }
+            }
+            MM_FENCE();
+          }
         }
       }
+      wait_stage<0>();
+    } else {
+      Staged<AT, T, NT> fa;
+      Staged<BT, T, NT> fb;
+      fa.init(A, p.lda, arows, kn, tid);
+      fb.init(B, p.ldb, bcols, kn, tid);
+      fa.load();
+      fb.load();
+      for (int s = 0; s < nst; ++s) {
+        const uint32_t u = lds0 + (s & 1) * 2 * SLOT;
+        fa.store(u, tid);
+        fb.store(u + SLOT, tid);
+        __syncthreads();                          // the other pair's readers are past the barrier before
+        if (s + 1 < nst) {
+          fa.load();
+          fb.load();
+        }
+        ra.enter(u);
+        rb.enter(u + SLOT);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) read_one(0, n, a[0], b[0]);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+#pragma unroll
+          for (int m = 0; m < NM; ++m) {
+            const int i = m / NB, j = m % NB;
+            if (ks < 3) read_one(ks + 1, m, a[(ks & 1) ^ 1], b[(ks & 1) ^ 1]);
+            acc[i][j] = E::mma32(b[ks & 1][j], a[ks & 1][i], acc[i][j]);
+          }
+        }
+      }
+      __syncthreads();
     }
-    wait_stage<0>();
   }
 
   // acc[i][j][e]: row 32 i + lane % 32, column 32 j + 8 (e / 4) + 4 (lane / 32) + e % 4 of the wave's
@@ -390,6 +402,7 @@ __global__ __launch_bounds__(64 * NWM * NWN, 2) void gmm_ring_kernel(MmArgs p) {
   typedef __attribute__((address_space(3))) v4i lds_v4i;
   typedef __attribute__((address_space(3))) v2i lds_v2i;
   constexpr int PASSES = OUT == MM_OUT_SAME ? 1 : NB;
+  constexpr int CE = 16 / EB;                       // elements of a 16-byte chunk
 #pragma unroll
   for (int ps = 0; ps < PASSES; ++ps) {
 #pragma unroll
@@ -416,21 +429,64 @@ __global__ __launch_bounds__(64 * NWM * NWN, 2) void gmm_ring_kernel(MmArgs p) {
     for (int r0 = 0; r0 < WM; r0 += 8) {
       const int r = r0 + sr, tr = wm * WM + r;
       const v4i v = *(lds_v4i*)(uintptr_t)(reg + r * 128 + ((sc ^ ((r >> 1) & 7)) << 4));
-      if constexpr (OUT == MM_OUT_SAME) {
-        const int c = wn * WN + sc * 8;
-        if (tr < arows && c < bcols)
-          *reinterpret_cast<v4i*>(static_cast<uint16_t*>(p.c) + (crow0 + tr) * p.ldc + col0 + c) = v;
+      const int c = wn * WN + (OUT == MM_OUT_SAME ? 0 : ps * 32) + sc * CE;
+      if (tr >= arows || c >= bcols) continue;
+      uint8_t* dst = C + ((crow0 + tr) * ldc + col0 + c) * EB;
+      if (VEC || c + CE <= bcols) {
+        v4i out = v;
+        if (OUT == MM_OUT_ACC32) {
+          v4f old;
+          __builtin_memcpy(&old, dst, 16);
+          out = __builtin_bit_cast(v4i, old + __builtin_bit_cast(v4f, v));
+        }
+        if constexpr (VEC) *reinterpret_cast<v4i*>(dst) = out;
+        else __builtin_memcpy(dst, &out, 16);
       } else {
-        const int c = wn * WN + ps * 32 + sc * 4;
-        if (tr < arows && c < bcols) {
-          v4f* dst = reinterpret_cast<v4f*>(static_cast<float*>(p.c) + (crow0 + tr) * p.ldc + col0 + c);
-          const v4f f = __builtin_bit_cast(v4f, v);
-          if (OUT == MM_OUT_FP32) *dst = f;
-          else *dst = *dst + f;
+#pragma unroll
+        for (int e = 0; e < CE; ++e) {
+          if (c + e >= bcols) break;
+          if constexpr (OUT == MM_OUT_SAME) {
+            reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
+          } else {
+            float* f = reinterpret_cast<float*>(dst) + e;
+            const float x = __builtin_bit_cast(v4f, v)[e];
+            *f = OUT == MM_OUT_ACC32 ? *f + x : x;
+          }
         }
       }
     }
   }
+}
+
+// c = the parts' sum in order, one element per thread.  FPROP, DGRAD: rows behind the last group are
+// zeroed or left; adding to c, a zero sum (an empty group's) leaves it as it is.
+template <int TYPE, int LAYOUT, int OUT>
+__global__ __launch_bounds__(256) void gmm_sum_kernel(MmArgs p) {
+  const int64_t cols = LAYOUT == MM_WGRAD ? p.k : p.n;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  long long used = 0;                    // rows of all groups
+  if (LAYOUT != MM_WGRAD) {
+    for (int g = threadIdx.x & 63; g < p.G; g += 64) used += max(p.m_splits[g], 0);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) used += __shfl_xor(used, o, 64);
+  }
+  if (i >= p.part_stride) return;
+  const int64_t row = i / cols, col = i - row * cols;
+  int64_t o = row * p.ldc + col;
+  bool live = true;
+  if (LAYOUT == MM_WGRAD) {
+    const int64_t g = row / p.n;
+    o = g * p.c_stride + (row - g * p.n) * p.ldc + col;
+  } else {
+    live = row < used;
+    if (!live && !p.zero_rest) return;
+  }
+  float f = 0.0f;
+  if (live)
+    for (int z = 0; z < p.parts; ++z) f += p.part[z * p.part_stride + i];
+  if (OUT == MM_OUT_SAME) static_cast<uint16_t*>(p.c)[o] = Elem<TYPE>::down(f);
+  else if (OUT == MM_OUT_FP32) static_cast<float*>(p.c)[o] = f;
+  else if (f != 0.0f) static_cast<float*>(p.c)[o] += f;
 }
 
 // ----------------------------------------------------------------------------- stream kernel
@@ -788,7 +844,7 @@ __global__ __launch_bounds__(512, 2) void gmm_stream_kernel(StreamArgs args) {
       return *(lds_v4i*)(uintptr_t)(reg + (8 * r + sr) * 128 + ((sc ^ (((8 * r + sr) >> 1) & 7)) << 4));
     };
     auto store = [&](v4i v, uint32_t vo, uint32_t so) {
-      asm volatile("s_nop 4\n\tbuffer_store_dwordx4 %0, %1, %2, %3 offen\n\ts_nop 1" :: "v"(v), "v"(vo), "s"(rc), "s"((uint32_t)sgpr((int)so)) : "memory");
+      asm volatile("s_nop 4\n\tbuffer_store_dwordx4 %0, %1, %2, %3 offen nt\n\ts_nop 1" :: "v"(v), "v"(vo), "s"(rc), "s"((uint32_t)sgpr((int)so)) : "memory");
     };
     if constexpr (OUT == MM_OUT_SAME) {
       v4i out[NA][4];
@@ -852,20 +908,35 @@ __global__ __launch_bounds__(512, 2) void gmm_stream_kernel(StreamArgs args) {
 static int64_t row_tiles_bound(const MmArgs& p, int h) {
   return (p.M + (h - 1) * std::min<int64_t>((int64_t)p.G + 1, p.M)) / h;
 }
-
-template <int TYPE, int LAYOUT, int OUT>
-static hipError_t run_any(const MmArgs& p, hipStream_t s) {
-  int64_t grid;
-  if (LAYOUT == MM_WGRAD) grid = (int64_t)p.G * ((p.n + ST - 1) / ST) * ((p.k + ST - 1) / ST);
-  else grid = row_tiles_bound(p, ST) * ((p.n + ST - 1) / ST);
-  grid = std::max<int64_t>(grid, 1);
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gmm_any_kernel<TYPE, LAYOUT, OUT>), dim3((uint32_t)grid), dim3(256), 0, s, p);
-  return hipGetLastError();
+// Row tiles of height h when the M rows are spread evenly.
+static int64_t row_tiles_even(int64_t M, int G, int h) {
+  const int64_t used = std::min<int64_t>(G, std::max<int64_t>(M, 1));
+  return used * ((M / used + h - 1) / h);
+}
+static int cu_count() {
+  int dev = 0, n = 0;
+  if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 8)
+    return 256;
+  return n;
 }
 
-template <int TYPE, int LAYOUT, int OUT, int T, int NWM, int NWN>
+// Parts of the contraction: with fewer tiles than CUs and eight stages or more, as many as fill the
+// device twice, none shorter than four stages.
+int grouped_matmul_parts(int layout, int G, int64_t M, int64_t n, int64_t k) {
+  const int64_t tn = (n + 127) / 128, tk = (k + 127) / 128;
+  const int64_t tiles = layout == MM_WGRAD ? G * tn * tk : row_tiles_even(M, G, 128) * tn;
+  const int64_t stages = ((layout == MM_WGRAD ? M / std::min<int64_t>(G, std::max<int64_t>(M, 1)) : k) + 63) / 64;
+  if (tiles >= 256 || stages < 8) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(tiles, 1), stages / 4, 16}));
+}
+int64_t grouped_matmul_part_floats(int layout, int G, int64_t M, int64_t n, int64_t k) {
+  const int parts = grouped_matmul_parts(layout, G, M, n, k);
+  return parts > 1 ? parts * (layout == MM_WGRAD ? G * n * k : M * n) : 0;
+}
+
+template <int TYPE, int LAYOUT, int OUT, bool VEC>
 static hipError_t run_ring(const MmArgs& p, hipStream_t s) {
+  constexpr int T = 128;
   int64_t grid;
   if (LAYOUT == MM_WGRAD) {
     const int64_t tpg = (int64_t)((p.n + T - 1) / T) * ((p.k + T - 1) / T);
@@ -874,22 +945,20 @@ static hipError_t run_ring(const MmArgs& p, hipStream_t s) {
     grid = 8 * ((row_tiles_bound(p, T) * ((p.n + T - 1) / T) + 7) / 8);
   }
   grid = std::max<int64_t>(grid, 8);
-  auto* k = gmm_ring_kernel<TYPE, LAYOUT, OUT, T, NWM, NWN>;
-  hipLaunchKernelGGL(k, dim3((uint32_t)grid), dim3(64 * NWM * NWN), 0, s, p);
+  auto* k = gmm_ring_kernel<TYPE, LAYOUT, OUT, VEC>;
+  hipLaunchKernelGGL(k, dim3((uint32_t)grid, OUT == MM_OUT_PART ? p.parts : 1), dim3(256), 0, s, p);
   return hipGetLastError();
 }
-
-// 16-byte loads and stores throughout.
-static bool vec_ok(const MmArgs& p) {
-  const uintptr_t addr = reinterpret_cast<uintptr_t>(p.a) | reinterpret_cast<uintptr_t>(p.b) | reinterpret_cast<uintptr_t>(p.c);
-  return (addr & 15) == 0 && ((p.n | p.k | p.lda | p.ldb | p.ldc | p.b_stride | p.c_stride) & 7) == 0;
-}
-
-static int cu_count() {
-  int dev = 0, n = 0;
-  if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 8)
-    return 256;
-  return n;
+template <int TYPE, int LAYOUT, int OUT, bool VEC>
+static hipError_t run_tiles(const MmArgs& p, hipStream_t s) {
+  if (p.parts <= 1) return run_ring<TYPE, LAYOUT, OUT, VEC>(p, s);
+  MmArgs q = p;
+  q.part_stride = (LAYOUT == MM_WGRAD ? (int64_t)p.G * p.n : p.M) * (LAYOUT == MM_WGRAD ? p.k : p.n);
+  q.zero_rest = 0;
+  if (hipError_t e = run_ring<TYPE, LAYOUT, MM_OUT_PART, VEC>(q, s)) return e;
+  q.zero_rest = p.zero_rest;
+  hipLaunchKernelGGL((gmm_sum_kernel<TYPE, LAYOUT, OUT>), dim3((uint32_t)((q.part_stride + 255) / 256)), dim3(256), 0, s, q);
+  return hipGetLastError();
 }
 
 template <int TYPE, int LAYOUT, int OUT>
@@ -909,19 +978,33 @@ static hipError_t run_stream(const MmArgs& p, hipStream_t s) {
   hipLaunchKernelGGL(k, dim3((uint32_t)(cu_count() / 8 * 8)), dim3(512), 0, s, a);
   return hipGetLastError();
 }
+// The 256 x 256 tiles where they fill the device and hold rows enough.  Measured (bf16, us, 128-tile
+// ring / stream): 8 x 512 rows, 4096 x 2048: forward 71.7 / 64.7, at 256 rows a group 38.6 / 64.6;
+// 64 x 256 rows, 1024 x 2048: 104 / 78; 64 x 128 rows, 2816 x 2048: 206 / 200 and dgrad 157 / 159;
+// 32 x 64 rows, 4096 x 2048: 133 / 138.  WGRAD by its tiles alone: 8 x 128 rows, 4096 x 2048 (1024
+// tiles) 49.1 / 44.1, one group 2048 rows 4096 x 4096 (256 tiles) 71.0 / 67.0, 16384 rows 1024 x
+// 1024 (16 tiles) 134 / 335.
 static bool use_stream(const MmArgs& p) {
-  return GMM_STREAM;
+  const int64_t tn = (p.n + 255) / 256, tk = (p.k + 255) / 256;
+  if (p.layout == MM_WGRAD) return p.G * tn * tk >= 256;
+  return p.M >= (int64_t)160 * p.G && row_tiles_even(p.M, p.G, 256) * tn >= 256;
 }
 size_t grouped_matmul_table_bytes(int G, int64_t M) {
   const int64_t rows = (M + 255 * std::min<int64_t>((int64_t)G + 1, M)) / 256;
   return 4 * (8 + (size_t)std::max<int64_t>(rows, G) * kTableWords);
 }
 
+// 16-byte loads and stores throughout.
+static bool vec_ok(const MmArgs& p) {
+  const uintptr_t addr = reinterpret_cast<uintptr_t>(p.a) | reinterpret_cast<uintptr_t>(p.b) | reinterpret_cast<uintptr_t>(p.c);
+  return (addr & 15) == 0 && ((p.n | p.k | p.lda | p.ldb | p.ldc | p.b_stride | p.c_stride) & 7) == 0;
+}
+
 template <int TYPE, int LAYOUT, int OUT>
 static hipError_t run_sized(const MmArgs& p, hipStream_t s) {
-  if (!vec_ok(p)) return run_any<TYPE, LAYOUT, OUT>(p, s);
+  if (!vec_ok(p)) return run_tiles<TYPE, LAYOUT, OUT, false>(p, s);
   if (use_stream(p)) return run_stream<TYPE, LAYOUT, OUT>(p, s);
-  return run_ring<TYPE, LAYOUT, OUT, 128, 2, 2>(p, s);
+  return run_tiles<TYPE, LAYOUT, OUT, true>(p, s);
 }
 
 template <int TYPE>

@@ -187,8 +187,13 @@ struct MmArgs {
   int zero_rest;          // FPROP, DGRAD: rows of C behind the last group are written as zeros
   uint32_t* flags;        // bits as SplitTables::flags
   void* table;            // grouped_matmul_table_bytes of scratch
+  int parts;              // grouped_matmul_parts, and its scratch of grouped_matmul_part_floats
+  float* part;
+  int64_t part_stride;    // set by the launcher
 };
 size_t grouped_matmul_table_bytes(int G, int64_t M);
+int grouped_matmul_parts(int layout, int G, int64_t M, int64_t n, int64_t k);
+int64_t grouped_matmul_part_floats(int layout, int G, int64_t M, int64_t n, int64_t k);
 hipError_t launch_grouped_matmul(const MmArgs& a, hipStream_t s);
 
 // ----------------------------------------------------------------------------- group order

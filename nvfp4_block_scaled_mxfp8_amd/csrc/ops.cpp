@@ -26,7 +26,9 @@ gmlp_status check_dtype(int32_t t) {
   return GMLP_OK;
 }
 
-constexpr size_t kMmWsBytes = 256;      // the flag word; the tile table follows
+// Workspace of a grouped product: the flag word, the tile table, the parts of a cut contraction.
+constexpr size_t kMmFlagBytes = 256;
+size_t mm_table_bytes(int32_t G, int64_t M) { return (grouped_matmul_table_bytes(G, M) + 255) & ~size_t(255); }
 
 gmlp_status check_mm_sizes(int32_t layout, int32_t G, int64_t M, int64_t n, int64_t k) {
   if (layout != GMLP_GEMM_FPROP && layout != GMLP_GEMM_WGRAD && layout != GMLP_GEMM_DGRAD)
@@ -50,7 +52,7 @@ extern "C" gmlp_status gmlp_grouped_matmul_ws_bytes(int32_t layout, int32_t G, i
   if (!bytes) return set_error(GMLP_INVALID_ARG, "null pointer argument");
   const gmlp_status st = check_mm_sizes(layout, G, M, n, k);
   if (st != GMLP_OK) return st;
-  *bytes = kMmWsBytes + grouped_matmul_table_bytes(G, M);
+  *bytes = kMmFlagBytes + mm_table_bytes(G, M) + sizeof(float) * (size_t)grouped_matmul_part_floats(layout, G, M, n, k);
   return fine();
 }
 
@@ -100,7 +102,9 @@ extern "C" gmlp_status gmlp_grouped_matmul(const gmlp_grouped_matmul_args* p, hi
   a.k = (int)p->k;
   a.zero_rest = p->zero_rest != 0;
   a.flags = static_cast<uint32_t*>(p->ws);
-  a.table = static_cast<uint8_t*>(p->ws) + kMmWsBytes;
+  a.table = static_cast<uint8_t*>(p->ws) + kMmFlagBytes;
+  a.parts = grouped_matmul_parts(p->layout, p->G, p->M, p->n, p->k);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(p->ws) + kMmFlagBytes + mm_table_bytes(p->G, p->M));
   return launched(launch_grouped_matmul(a, stream), "grouped matmul");
 }
 
