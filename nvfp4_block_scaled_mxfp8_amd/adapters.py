@@ -8,12 +8,13 @@ any other), a [L, R, K] and b [L, N, R] the adapters, ids int32 [M] each row's a
 lora_forward and lora_backward are the same calls without autograd.  Argument marshalling only.
 """
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
 
-from . import _SIGS, _check, _dev_ptr, _stream, lib
-from .matmul import _DTYPES, _check_rows_out, _dtype16, _gs, _ld, _on, _row_major, _same
+from . import _SIGS, _check, _dev_ptr, lib
+from .matmul import _DTYPES, _check_rows_out, _dtype16, _gs, _ld, _packer, _row_major, _run, _same
 
 
 class LoraWeights(ctypes.Structure):
@@ -45,15 +46,21 @@ class LoraBwdArgs(ctypes.Structure):
 _SIGS.update({
     "gmlp_lora_query_sizes": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
                                              ctypes.c_int32, ctypes.POINTER(LoraSizes)]),
-    "gmlp_lora_forward": (ctypes.c_int, [ctypes.POINTER(LoraFwdArgs), ctypes.c_void_p]),
-    "gmlp_lora_backward": (ctypes.c_int, [ctypes.POINTER(LoraBwdArgs), ctypes.c_void_p]),
+    "gmlp_lora_forward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),          # LoraFwdArgs*
+    "gmlp_lora_backward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),         # LoraBwdArgs*
 })
+_pack_fwd, _pack_bwd = _packer(LoraFwdArgs), _packer(LoraBwdArgs)
+
+
+@functools.lru_cache(maxsize=4096)
+def _sizes(M, K, N, R, L):
+    s = LoraSizes()
+    _check(lib().gmlp_lora_query_sizes(M, K, N, R, L, ctypes.byref(s)))
+    return s.ctx_bytes, s.fwd_ws_bytes, s.bwd_ws_bytes
 
 
 def lora_query_sizes(M, K, N, R, L):
-    s = LoraSizes()
-    _check(lib().gmlp_lora_query_sizes(M, K, N, R, L, ctypes.byref(s)))
-    return {"ctx_bytes": s.ctx_bytes, "fwd_ws_bytes": s.fwd_ws_bytes, "bwd_ws_bytes": s.bwd_ws_bytes}
+    return dict(zip(("ctx_bytes", "fwd_ws_bytes", "bwd_ws_bytes"), _sizes(M, K, N, R, L)))
 
 
 @dataclass
@@ -86,8 +93,12 @@ def _check_weights(x, a, b, scales, what):
     return L, R, K, N
 
 
+def _ptr(t):
+    return t.data_ptr() if t is not None else 0
+
+
 def _weights(a, b, scales):
-    return LoraWeights(_dev_ptr(a, "a"), _ld(a), _gs(a), _dev_ptr(b, "b"), _ld(b), _gs(b), _dev_ptr(scales, "scales"))
+    return a.data_ptr(), _ld(a), _gs(a), b.data_ptr(), _ld(b), _gs(b), _ptr(scales)
 
 
 def lora_forward(base, x, a, b, ids, scales=None, out=None):
@@ -111,17 +122,15 @@ def lora_forward(base, x, a, b, ids, scales=None, out=None):
     _dev_ptr(x, "x")
     x, a, b, ids = _row_major(x), _row_major(a), _row_major(b), ids.contiguous()
     scales = scales.contiguous() if scales is not None else None
-    sz = lora_query_sizes(M, K, N, R, L)
+    ctx_bytes, ws_bytes, _ = _sizes(M, K, N, R, L)
     y = out if out is not None else torch.empty((M, N), dtype=x.dtype, device=dev)
     # one allocation: the workspace lies behind the context
-    buf = torch.empty(sz["ctx_bytes"] + sz["fwd_ws_bytes"] + 256, dtype=torch.uint8, device=dev)
-    at = (sz["ctx_bytes"] + 255) // 256 * 256
-    p = _dev_ptr(buf, "ctx")
-    args = LoraFwdArgs(_DTYPES[x.dtype], R, L, M, K, N, _dev_ptr(base, "base"), _ld(base) if base is not None else 0,
-                       _dev_ptr(x, "x"), _ld(x), _weights(a, b, scales), _dev_ptr(ids, "ids"), _dev_ptr(y, "y"), _ld(y),
-                       p, sz["ctx_bytes"], p + at, buf.numel() - at)
-    with _on(dev):
-        _check(lib().gmlp_lora_forward(ctypes.byref(args), _stream(dev)))
+    at = (ctx_bytes + 255) // 256 * 256
+    buf = torch.empty(at + ws_bytes, dtype=torch.uint8, device=dev)
+    p = buf.data_ptr()
+    args = _pack_fwd(_DTYPES[x.dtype], R, L, M, K, N, _ptr(base), _ld(base) if base is not None else 0, x.data_ptr(), _ld(x),
+                     *_weights(a, b, scales), ids.data_ptr(), y.data_ptr(), _ld(y), p, ctx_bytes, p + at, ws_bytes)
+    _run(lib().gmlp_lora_forward, args, dev)
     return y, LoraContext(buf, M, K, N, R, L, x.dtype, scales)
 
 
@@ -149,17 +158,15 @@ def lora_backward(dy, x, a, b, ctx, dx_add=None, need_dx=True, need_da=True, nee
         dx_add = _row_major(dx_add)
     _dev_ptr(dy, "dy")
     dy, x, a, b = _row_major(dy), _row_major(x), _row_major(a), _row_major(b)
-    sz = lora_query_sizes(M, K, N, R, L)
-    ws = torch.empty(sz["bwd_ws_bytes"], dtype=torch.uint8, device=dev)
+    ctx_bytes, _, ws_bytes = _sizes(M, K, N, R, L)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     dx = torch.empty((M, K), dtype=dy.dtype, device=dev) if need_dx else None
     da = torch.empty((L, R, K), dtype=dy.dtype, device=dev) if need_da else None
     db = torch.empty((L, N, R), dtype=dy.dtype, device=dev) if need_db else None
-    args = LoraBwdArgs(_DTYPES[dy.dtype], R, L, M, K, N, _dev_ptr(dy, "dy"), _ld(dy), _dev_ptr(x, "x"), _ld(x),
-                       _weights(a, b, ctx.scales), _dev_ptr(dx_add, "dx_add"), _ld(dx_add) if dx_add is not None else 0,
-                       _dev_ptr(dx, "dx"), K, _dev_ptr(da, "da"), _dev_ptr(db, "db"), _dev_ptr(ctx.buf, "ctx"),
-                       sz["ctx_bytes"], _dev_ptr(ws, "ws"), ws.numel())
-    with _on(dev):
-        _check(lib().gmlp_lora_backward(ctypes.byref(args), _stream(dev)))
+    args = _pack_bwd(_DTYPES[dy.dtype], R, L, M, K, N, dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x),
+                     *_weights(a, b, ctx.scales), _ptr(dx_add), _ld(dx_add) if dx_add is not None else 0, _ptr(dx), K,
+                     _ptr(da), _ptr(db), ctx.buf.data_ptr(), ctx_bytes, ws.data_ptr(), ws_bytes)
+    _run(lib().gmlp_lora_backward, args, dev)
     return {"dx": dx, "da": da, "db": db}
 
 

@@ -8,12 +8,13 @@ dispatch and combine are differentiable (x; expert_output and probs); the *_forw
 functions are the same calls without autograd.  Argument marshalling only.
 """
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
 
-from . import _SIGS, _check, _dev_ptr, _p, _stream, lib
-from .matmul import _DTYPES, _check_rows_out, _dtype16, _ld, _on, _row_major
+from . import _SIGS, _check, _dev_ptr, lib
+from .matmul import _DTYPES, _check_rows_out, _dtype16, _ld, _packer, _row_major, _run
 
 
 class MoveArgs(ctypes.Structure):
@@ -29,10 +30,11 @@ _SIGS.update({
     "gmlp_dispatch_plan": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p,
                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                           ctypes.c_void_p]),
-    "gmlp_dispatch": (ctypes.c_int, [ctypes.POINTER(MoveArgs), ctypes.c_void_p]),
-    "gmlp_combine": (ctypes.c_int, [ctypes.POINTER(MoveArgs), ctypes.c_void_p]),
-    "gmlp_combine_dprobs": (ctypes.c_int, [ctypes.POINTER(MoveArgs), ctypes.c_void_p]),
+    "gmlp_dispatch": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),              # MoveArgs*
+    "gmlp_combine": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
+    "gmlp_combine_dprobs": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
 })
+_pack_move = _packer(MoveArgs)
 
 
 @dataclass
@@ -51,20 +53,26 @@ class DispatchPlan:
         return self.rows.shape[1]
 
 
+@functools.lru_cache(maxsize=4096)
+def _plan_ws_bytes(n, E):
+    need = ctypes.c_size_t(0)
+    _check(lib().gmlp_dispatch_plan_ws_bytes(n, E, ctypes.byref(need)))
+    return need.value
+
+
 def dispatch_plan(experts, E):
     """The stable order by expert of the slots of `experts` (int32 [T, k] on the device)."""
     if not isinstance(experts, torch.Tensor) or experts.dtype != torch.int32 or experts.dim() != 2 or experts.shape[1] < 1:
         raise TypeError("experts: an int32 tensor [T, k] is required")
     experts = experts.contiguous()
     dev, n = experts.device, experts.numel()
-    need = ctypes.c_size_t(0)
-    _check(lib().gmlp_dispatch_plan_ws_bytes(n, E, ctypes.byref(need)))
+    need = _plan_ws_bytes(n, E)
     _dev_ptr(experts, "experts")
-    ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     plan = DispatchPlan(torch.empty(E, dtype=torch.int32, device=dev), torch.empty_like(experts))
-    with _on(dev):
-        _check(lib().gmlp_dispatch_plan(_p(experts), n, E, _p(plan.m_splits), _p(plan.rows), None, _p(ws), need.value,
-                                        _stream(dev)))
+    L = lib()
+    _run(lambda _, stream: L.gmlp_dispatch_plan(experts.data_ptr(), n, E, plan.m_splits.data_ptr(), plan.rows.data_ptr(),
+                                                None, ws.data_ptr() if need else None, need, stream), None, dev)
     return plan
 
 
@@ -89,15 +97,20 @@ def _check_probs(probs, plan):
     return probs.contiguous()
 
 
+def _ptr(t):
+    return t.data_ptr() if t is not None else 0
+
+
 def _move(fn, plan, src, dst, probs=None, zero_rest=False, src2=None, dprobs=None):
+    _dev_ptr(src, "src")                                             # refuses host tensors
     src = _row_major(src)
-    src2 = _row_major(src2) if src2 is not None else None
-    a = MoveArgs(_DTYPES[src.dtype], int(zero_rest), _dev_ptr(src, "src"), _ld(src), _dev_ptr(src2, "src2"),
-                 _ld(src2) if src2 is not None else 0, _dev_ptr(dst, "dst"), _ld(dst) if dst is not None else 0,
-                 plan.tokens, src.shape[1], plan.k, plan.m_splits.numel(), _dev_ptr(plan.rows, "rows"),
-                 _dev_ptr(plan.m_splits, "m_splits"), _dev_ptr(probs, "probs"), _dev_ptr(dprobs, "dprobs"))
-    with _on(src.device):
-        _check(getattr(lib(), fn)(ctypes.byref(a), _stream(src.device)))
+    if src2 is not None:
+        src2 = _row_major(src2)
+    T, k = plan.rows.shape
+    args = _pack_move(_DTYPES[src.dtype], zero_rest, src.data_ptr(), _ld(src), _ptr(src2),
+                      _ld(src2) if src2 is not None else 0, _ptr(dst), _ld(dst) if dst is not None else 0, T, src.shape[1],
+                      k, plan.m_splits.numel(), plan.rows.data_ptr(), plan.m_splits.data_ptr(), _ptr(probs), _ptr(dprobs))
+    _run(getattr(lib(), fn), args, src.device)
     return dst
 
 

@@ -8,12 +8,13 @@
 g is the group of row r by m_splits (int32 [G] on the device), products are accumulated in fp32
 and rounded once.  Argument marshalling only; the kernels are the library's.
 """
-import contextlib
 import ctypes
+import functools
+import struct
 
 import torch
 
-from . import (_SIGS, _check, _check_out, _dev_ptr, _splits, _stream, GEMM_DGRAD, GEMM_FPROP, GEMM_WGRAD, OUT_FP32,
+from . import (_SIGS, _check, _check_out, _dev_ptr, _splits, GEMM_DGRAD, GEMM_FPROP, GEMM_WGRAD, OUT_FP32,
                OUT_FP32_ACCUMULATE, lib)
 
 OUT_SAME = 0                   # the operands' type
@@ -29,11 +30,35 @@ class GroupedMatmulArgs(ctypes.Structure):
                 ("k", ctypes.c_int64), ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
 
 
+_CODES = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_void_p: "P", ctypes.c_size_t: "N"}
+
+
+def _packer(cls):
+    """pack(field values in order) -> the bytes of a ctypes structure (nested ones flattened): a
+    decode step's calls spend most of their host time in filling ctypes fields one by one."""
+    def codes(c):
+        return "".join(codes(t) if issubclass(t, ctypes.Structure) else _CODES[t] for _, t in c._fields_)
+    pk = struct.Struct("@" + codes(cls) + "0P")
+    assert pk.size == ctypes.sizeof(cls), cls
+    return pk.pack
+
+
 _SIGS.update({
     "gmlp_grouped_matmul_ws_bytes": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
                                                     ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]),
-    "gmlp_grouped_matmul": (ctypes.c_int, [ctypes.POINTER(GroupedMatmulArgs), ctypes.c_void_p]),
+    "gmlp_grouped_matmul": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),       # GroupedMatmulArgs*
 })
+_pack_mm = _packer(GroupedMatmulArgs)
+
+
+def _run(fn, args, device):
+    """One library call with packed arguments on the device's current stream."""
+    i = device.index
+    if i == torch._C._cuda_getDevice():
+        _check(fn(args, torch._C._cuda_getCurrentRawStream(i)))
+    else:
+        with torch.cuda.device(i):
+            _check(fn(args, torch._C._cuda_getCurrentRawStream(i)))
 
 
 def _dtype16(t, name):
@@ -54,6 +79,8 @@ def _same(t, ref, dim, name):
 
 def _row_major(t):
     """t with its last dimension contiguous and rows that do not overlap (a copy if it is not so)."""
+    if t.is_contiguous():
+        return t
     ok = t.shape[-1] <= 1 or t.stride(-1) == 1
     need = t.shape[-1]
     for d in range(t.dim() - 2, -1, -1):
@@ -75,13 +102,6 @@ def _gs(t):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1] * _ld(t)
 
 
-def _on(device):
-    """The device made current for a call (nothing to do where it already is)."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
 def _check_rows_out(t, shape, like, name):
     """A given output: like's dtype and device, the shape, last dimension contiguous, rows apart."""
     if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != like.dtype or t.device != like.device:
@@ -90,6 +110,7 @@ def _check_rows_out(t, shape, like, name):
         raise ValueError(f"{name}: the last dimension must be contiguous and rows must not overlap")
 
 
+@functools.lru_cache(maxsize=4096)
 def grouped_matmul_ws_bytes(layout, G, M, n, k):
     v = ctypes.c_size_t(0)
     _check(lib().gmlp_grouped_matmul_ws_bytes(layout, G, M, n, k, ctypes.byref(v)))
@@ -102,17 +123,16 @@ def _call(layout, a, b, c, m_splits, M, n, k, out_dtype, zero_rest, ws):
     if m_splits.device != dev:
         raise ValueError(f"m_splits: on {m_splits.device}, the other tensors are on {dev}")
     if dev.type != "cuda":
-        _dev_ptr(a, "x" if layout == GEMM_FPROP else "dy")          # refuses host tensors
+        _dev_ptr(a, "dy" if layout != GEMM_FPROP else "x")          # refuses host tensors
     if ws is None:
         ws = torch.empty(grouped_matmul_ws_bytes(layout, G, M, n, k), dtype=torch.uint8, device=dev)
-    elif ws.device != dev:
-        raise ValueError(f"ws: on {ws.device}, the other tensors are on {dev}")
-    args = GroupedMatmulArgs(layout, _DTYPES[a.dtype], out_dtype, int(zero_rest), _dev_ptr(a, "a"), _ld(a),
-                             _dev_ptr(b, "b"), _ld(b), 0 if layout == GEMM_WGRAD else _gs(b), _dev_ptr(c, "c"), _ld(c),
-                             _gs(c) if layout == GEMM_WGRAD else 0, _dev_ptr(m_splits, "m_splits"), G, M, n, k,
-                             _dev_ptr(ws, "ws"), ws.numel() * ws.element_size())
-    with _on(dev):
-        _check(lib().gmlp_grouped_matmul(ctypes.byref(args), _stream(dev)))
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: a contiguous tensor on {dev} is required")
+    wgrad = layout == GEMM_WGRAD
+    args = _pack_mm(layout, _DTYPES[a.dtype], out_dtype, zero_rest, a.data_ptr(), _ld(a), b.data_ptr(), _ld(b),
+                    0 if wgrad else _gs(b), c.data_ptr(), _ld(c), _gs(c) if wgrad else 0, m_splits.data_ptr(), G, M, n, k,
+                    ws.data_ptr(), ws.numel() * ws.element_size())
+    _run(lib().gmlp_grouped_matmul, args, dev)
     return c
 
 

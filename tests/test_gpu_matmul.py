@@ -22,6 +22,15 @@ CASES = {
     "empty": ([0, 0, 0], 5, 64, 64),
     "no_rows": ([0, 0], 0, 64, 64),
     "tall": ([1000], 1000, 8, 2048),
+    # the 256 x 256 stream: column tiles enough, groups of several row tiles and a ragged one, rows behind
+    # the last group; as forward, as dgrad (and the other as a contraction cut into parts)
+    "stream_n": ([700, 0, 1200, 49], 2048, 8200, 72),
+    "stream_k": ([700, 0, 1200, 49], 2048, 72, 8200),
+    "stream_one": ([2400], 2400, 6656, 200),
+    # weight gradients by the stream: with few and with many tiles a group, and more groups than are sorted
+    "stream_w": ([0, 65, 1, 300, 64, 0, 17, 128, 5], 600, 1032, 1544),
+    "stream_x": ([3, 0, 150, 140], 300, 2056, 2056),
+    "stream_g": ([i % 2 for i in range(1100)] + [77], 700, 64, 72),
 }
 
 
