@@ -219,7 +219,16 @@ struct LoraRows {
   int64_t M;
   int L;
 };
-// v[z][p][r] = scale sum over the z-th part of c of X[row p, c] W_l[r, c]; W [L, R, C] (z < parts)
+// A rank-sized factor v [M, R] by position, as the products take it: hi [M][2][rp] of the operands'
+// type with rp = lora_rp(R), v = inv (hi + lo) per position, zero behind rank R; inv null: 1 (bf16).
+// v itself (fp32) only where a common scale has to be found again (fp16 outer products).
+struct LoraFactor {
+  uint16_t* hi;
+  float* inv;
+  float* v;
+};
+inline int lora_rp(int R) { return (R + 15) & ~15; }
+// v[p][r] = scale sum_c X[row p, c] W_l[r, c]; W [L, R, C]
 struct LoraShrink {
   int type, R;
   LoraRows rows;
@@ -227,17 +236,14 @@ struct LoraShrink {
   const void* w; int64_t ldw, w_stride;
   int64_t C;
   const float* scales;      // [L] or null (1)
-  float* v;
-  int parts;
+  LoraFactor out;
 };
 hipError_t launch_lora_shrink(const LoraShrink& a, hipStream_t s);
-int lora_shrink_parts(int64_t M, int64_t C, int R, int L);
-// Y[row p, c] = base[row p, c] + scale sum_r (sum_z v[z][p][r]) W_l[c, r]; W [L, C, R]; base null: 0
+// Y[row p, c] = base[row p, c] + scale sum_r v[p][r] W_l[c, r]; W [L, C, R]; base null: 0
 struct LoraExpand {
   int type, R;
   LoraRows rows;
-  const float* v;
-  int parts;
+  LoraFactor v;
   const void* w; int64_t ldw, w_stride;
   int64_t C;
   const float* scales;
@@ -250,8 +256,7 @@ hipError_t launch_lora_expand(const LoraExpand& a, hipStream_t s);
 struct LoraOuter {
   int type, R;
   LoraRows rows;
-  const float* v;
-  int parts;
+  LoraFactor v;
   const void* x; int64_t ldx;
   int64_t C;
   const float* scales;
@@ -261,10 +266,15 @@ struct LoraOuter {
 };
 hipError_t launch_lora_outer(const LoraOuter& a, hipStream_t s);
 int64_t lora_outer_part_floats(int64_t M, int64_t C, int R, int L);
+// dst[l][c][r] = src[l][r][c] for adapters with rows, of two stacks in one launch (n = 1: the first
+// only); src [L, R, C], dst rows of ldd elements, zero behind R
+struct LoraTranspose {
+  const void* src; int64_t lds, src_stride;
+  int64_t R, C;
+  void* dst; int64_t ldd, dst_stride;
+};
+hipError_t launch_lora_transpose(const LoraTranspose* t, int n, const int32_t* count, int L, hipStream_t s);
 hipError_t launch_zero16(void* p, int64_t n, hipStream_t s);
-// dst[l][c][r] = src[l][r][c] for adapters with rows; src [L, R, C], dst rows of ldd elements
-hipError_t launch_lora_transpose(const void* src, int64_t lds, int64_t src_stride, int64_t R, int64_t C, void* dst,
-                                 int64_t ldd, int64_t dst_stride, const int32_t* count, int L, hipStream_t s);
 
 // ----------------------------------------------------------------------------- expert dispatch
 // x, y, dy are by token [T, H], xg, v, dv by row in expert order [T k, H]; rows [T, k] the row of each

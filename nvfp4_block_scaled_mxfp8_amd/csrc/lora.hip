@@ -4,10 +4,10 @@
 // All three are bound by the read (and write) of the [M, C] tensors: 2 R flops per element read.
 // Rows of one adapter are consecutive positions; a workgroup takes a tile of positions of one
 // adapter and gathers their rows through `order`, so requests need not be sorted or equal in
-// length.  The rank-sized factor v stays in fp32 in memory and enters the 16-bit matrix products
-// as hi + lo, two values of the operands' type (at least 16 of its bits): one
-// V_MFMA_F32_16X16X32 takes 16 ranks, hi in its lower and lo in its upper sixteen contraction
-// steps, so the second half costs no further instruction where a rank tile is 16 wide.
+// length.  The rank-sized factor v is summed in fp32 and enters the 16-bit matrix products as
+// hi + lo, two values of the operands' type (at least 16 of its bits), split once where v is made:
+// one V_MFMA_F32_16X16X32 takes 16 ranks, hi in its lower and lo in its upper sixteen contraction
+// steps.  fp16 scales each position's v by a power of two first, so that neither half leaves the range.
 #include "mm_common.h"
 
 #include <algorithm>
@@ -33,20 +33,11 @@ __device__ __forceinline__ v4i load8(const uint16_t* p, int valid) {
 
 // v as a factor of the 16-bit products: hi = T(v), lo = T(v - hi).
 template <int TYPE>
-__device__ __forceinline__ v4i split8(const float* v, bool lo) {
+__device__ __forceinline__ void split(float v, uint16_t& hi, uint16_t& lo) {
   using E = Elem<TYPE>;
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float f[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float x = v[2 * i + e], h = E::up(E::down(x));
-      f[e] = !lo ? x : (__builtin_isfinite(h) ? x - h : 0.0f);
-    }
-    w[i] = E::down2(f[0], f[1]);
-  }
-  return v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+  hi = E::down(v);
+  const float h = E::up(hi);
+  lo = E::down(__builtin_isfinite(h) ? v - h : 0.0f);
 }
 // A power of two that brings a largest magnitude m to [2^14, 2^15) (fp16 operands: hi then never
 // overflows and lo resolves 2^-39 of m), 1 where m is zero or not finite.  Exponents are kept where
@@ -59,15 +50,18 @@ __device__ __forceinline__ float fp16_scale(float m) {
 __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u - (__float_as_uint(s) >> 23)) << 23); }
 
 // ----------------------------------------------------------------------------- shrink
-// RB x 16 positions by RT x 16 ranks per workgroup, the contraction in blocks of 32 SPB split over
-// the four waves (and over gridDim.y parts), fragments straight from memory with the next block's
-// loads in flight.  Waves are joined through LDS in order.
-template <int TYPE, bool VEC, int RB, int RT>
-__global__ __launch_bounds__(256) void lora_shrink_kernel(LoraShrink p) {
+// RB x 16 positions by RT x 16 ranks per workgroup, the contraction in blocks of 32 SPB dealt to its
+// NW waves, fragments straight from memory with the next block's loads in flight.  The waves are
+// joined through LDS, in order.  A workgroup for the whole contraction keeps v out of memory until
+// it is whole; the waves of a workgroup give the loads in flight that few positions cannot.
+template <int TYPE, bool VEC, int RB, int RT, int NW>
+__global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraShrink p) {
   using E = Elem<TYPE>;
-  constexpr int SPB = RB + RT <= 3 ? 4 : RB + RT <= 6 ? 2 : 1;
+  // registers: 256 a lane with 8 waves, 128 with 16
+  constexpr int SPB = NW > 8 ? (RB + RT <= 2 ? 4 : RB + RT <= 3 ? 2 : 1) : RB + RT <= 3 ? 4 : RB + RT <= 6 ? 2 : 1;
   constexpr int LD = RT * 16 + 4;
-  __shared__ __align__(16) float red[RB * 16 * LD];
+  __shared__ __align__(16) float red[NW * RB * 16 * LD];
+  __shared__ float s_mul[RB * 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const RowTile rt = find_row_tile(p.rows.count, p.rows.L, (uint32_t)p.rows.M, RB * 16, 1, false, blockIdx.x, lane);
   if (rt.g < 0) return;
@@ -87,7 +81,7 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraShrink p) {
   for (int b = 0; b < RB; ++b)
 #pragma unroll
     for (int t = 0; t < RT; ++t) acc[b][t] = v4f{0, 0, 0, 0};
-  const int64_t step = (int64_t)32 * SPB;
+  constexpr int64_t step = 32 * SPB;
   const int64_t nblk = (p.C + step - 1) / step;
   v4i xf[2][SPB][RB], wf[2][SPB][RT];
   auto fetch = [&](int64_t blk, int s) {
@@ -110,72 +104,94 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraShrink p) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) acc[b][t] = E::mma16(wf[s][k][t], xf[s][k][b], acc[b][t]);
   };
-  const int64_t stride = 4 * (int64_t)gridDim.y;
-  int64_t blk = (int64_t)blockIdx.y * 4 + wave;
+  int64_t blk = wave;
   if (blk < nblk) {
     fetch(blk, 0);
     while (true) {
-      if (blk + stride < nblk) fetch(blk + stride, 1);
+      if (blk + NW < nblk) fetch(blk + NW, 1);
       mul(0);
-      blk += stride;
+      blk += NW;
       if (blk >= nblk) break;
-      if (blk + stride < nblk) fetch(blk + stride, 0);
+      if (blk + NW < nblk) fetch(blk + NW, 0);
       mul(1);
-      blk += stride;
+      blk += NW;
       if (blk >= nblk) break;
     }
   }
   // lane: position 16 b + q, ranks 16 t + 4 j + i
-  for (int w = 0; w < 4; ++w) {
-    if (wave == w) {
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
+  for (int b = 0; b < RB; ++b)
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          v4f* d = reinterpret_cast<v4f*>(red + (16 * b + q) * LD + 16 * t + 4 * j);
-          *d = w == 0 ? acc[b][t] : *d + acc[b][t];
-        }
+    for (int t = 0; t < RT; ++t)
+      *reinterpret_cast<v4f*>(red + ((wave * RB + b) * 16 + q) * LD + 16 * t + 4 * j) = acc[b][t];
+  __syncthreads();
+  const float sc = p.scales ? p.scales[rt.g] : 1.0f;
+  const int rp = (p.R + 15) & ~15;
+  constexpr int N = RB * 16 * RT * 16, PER = (N + 64 * NW - 1) / (64 * NW);
+  float v[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid + i * 64 * NW, row = e / (RT * 16), r = e % (RT * 16);
+    v[i] = 0.0f;
+    if (e < N && row < valid && r < p.R) {
+      for (int w = 0; w < NW; ++w) v[i] += red[(w * RB * 16 + row) * LD + r];
+      v[i] *= sc;
+    }
+  }
+  if (TYPE == MM_FP16) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = tid + i * 64 * NW;
+      if (e < N) red[e / (RT * 16) * LD + e % (RT * 16)] = v[i];
+    }
+    __syncthreads();
+    if (tid < RB * 16) {
+      float top = 0.0f;
+      for (int r = 0; r < p.R; ++r) top = fmaxf(top, fabsf(red[tid * LD + r]));
+      const float s = fp16_scale(top);
+      s_mul[tid] = s;
+      if (tid < valid) p.out.inv[pos0 + tid] = inverse_pow2(s);
     }
     __syncthreads();
   }
-  const float sc = p.scales ? p.scales[rt.g] : 1.0f;
-  float* out = p.v + ((int64_t)blockIdx.y * p.rows.M + pos0) * p.R;
-  for (int i = tid; i < valid * p.R; i += 256) out[i] = sc * red[i / p.R * LD + i % p.R];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid + i * 64 * NW, row = e / (RT * 16), r = e % (RT * 16);
+    if (e >= N || row >= valid || r >= rp) continue;
+    uint16_t hi, lo;
+    split<TYPE>(TYPE == MM_FP16 ? v[i] * s_mul[row] : v[i], hi, lo);
+    uint16_t* d = p.out.hi + (pos0 + row) * 2 * rp + r;
+    d[0] = hi;
+    d[rp] = lo;
+    if (p.out.v && r < p.R) p.out.v[(pos0 + row) * p.R + r] = v[i];
+  }
 }
 
 static int64_t tiles_bound(int64_t M, int groups, int64_t h) { return (M + (h - 1) * std::min<int64_t>(groups, M)) / h; }
 
-// Rows of a shrink tile: 16 while that leaves the device unfilled, else 32 (64 above 32 ranks, where
-// W would be read as often as X).
-static int shrink_rb(int64_t M, int R, int L) {
-  if (tiles_bound(M, L, 16) < 512) return 1;
-  return R > 32 ? 4 : 2;
-}
-// Parts of the contraction: enough workgroups for the device, none shorter than one block per wave.
-int lora_shrink_parts(int64_t M, int64_t C, int R, int L) {
-  const int64_t tiles = std::max<int64_t>(tiles_bound(M, L, 16 * shrink_rb(M, R, L)), 1);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, (C + 511) / 512, 16}));
-}
-
-template <int TYPE, bool VEC, int RB, int RT>
+template <int TYPE, bool VEC, int RB, int RT, int NW>
 static hipError_t run_shrink(const LoraShrink& p, hipStream_t s) {
   const int64_t tiles = tiles_bound(p.rows.M, p.rows.L, 16 * RB);
-  hipLaunchKernelGGL((lora_shrink_kernel<TYPE, VEC, RB, RT>), dim3((uint32_t)tiles, p.parts), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((lora_shrink_kernel<TYPE, VEC, RB, RT, NW>), dim3((uint32_t)tiles), dim3(64 * NW), 0, s, p);
   return hipGetLastError();
 }
-template <int TYPE, bool VEC, int RB>
+// 32 positions a tile where those fill the device, with as many waves as four a SIMD take; 16
+// positions and 16 waves below.  (Above 64 ranks a wave's registers allow half as many.)
+template <int TYPE, bool VEC, int RT>
 static hipError_t shrink_rank(const LoraShrink& p, hipStream_t s) {
-  if (p.R <= 16) return run_shrink<TYPE, VEC, RB, 1>(p, s);
-  if (p.R <= 32) return run_shrink<TYPE, VEC, RB, 2>(p, s);
-  if (p.R <= 64) return run_shrink<TYPE, VEC, RB, 4>(p, s);
-  return run_shrink<TYPE, VEC, RB, 8>(p, s);
+  constexpr int NW = RT > 4 ? 8 : 16;
+  const int64_t tiles = tiles_bound(p.rows.M, p.rows.L, 32);
+  if (tiles >= 512) return run_shrink<TYPE, VEC, 2, RT, 8>(p, s);
+  if (tiles >= 128) return run_shrink<TYPE, VEC, 2, RT, NW>(p, s);
+  return run_shrink<TYPE, VEC, 1, RT, NW>(p, s);
 }
 template <int TYPE, bool VEC>
 static hipError_t shrink_rows(const LoraShrink& p, hipStream_t s) {
-  const int rb = shrink_rb(p.rows.M, p.R, p.rows.L);
-  if (rb == 1) return shrink_rank<TYPE, VEC, 1>(p, s);
-  if (rb == 2) return shrink_rank<TYPE, VEC, 2>(p, s);
-  return p.R <= 64 ? run_shrink<TYPE, VEC, 4, 4>(p, s) : run_shrink<TYPE, VEC, 4, 8>(p, s);
+  if (p.R <= 16) return shrink_rank<TYPE, VEC, 1>(p, s);
+  if (p.R <= 32) return shrink_rank<TYPE, VEC, 2>(p, s);
+  if (p.R <= 64) return shrink_rank<TYPE, VEC, 4>(p, s);
+  return shrink_rank<TYPE, VEC, 8>(p, s);
 }
 static bool vec16(const void* p, int64_t ld, int64_t cols) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ((ld | cols) & 7) == 0;
@@ -217,6 +233,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraExpand p, int tile
     }
   }
   const float sc = !rest && p.scales ? p.scales[rt.g] : 1.0f;
+  const int rp = (p.R + 15) & ~15;
   const int64_t c = n0 + 16 * j;
   const int cols = (int)min(p.C - c, (int64_t)16);       // of this lane
   for (int b = 0; b < valid; b += 16) {
@@ -234,46 +251,15 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraExpand p, int tile
     for (int f = 0; f < 4; ++f) acc[f] = v4f{0, 0, 0, 0};
     float mul = sc;
     if (!rest) {
-      float v[RT][8];
-      float top = 0.0f;
+      const uint16_t* src = p.v.hi + (pos0 + at) * 2 * rp + (j >= 2 ? rp : 0) + 8 * (j & 1);
+      v4i u[RT];
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const int r = 16 * t + 8 * (j & 1);
+      for (int t = 0; t < RT; ++t) u[t] = 16 * t < rp ? *reinterpret_cast<const v4i*>(src + 16 * t) : v4i{0, 0, 0, 0};
+      if (p.v.inv) mul *= p.v.inv[pos0 + at];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[t][i] = 0.0f;
-        for (int z = 0; z < p.parts; ++z) {
-          const float* src = p.v + ((int64_t)z * p.rows.M + pos0 + at) * p.R + r;
-          if ((p.R & 3) == 0) {
+      for (int t = 0; t < RT; ++t)
 #pragma unroll
-            for (int i = 0; i < 8; i += 4)
-              if (r + i < p.R) {
-                const v4f x = *reinterpret_cast<const v4f*>(src + i);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[t][i + e] += x[e];
-              }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (r + i < p.R) v[t][i] += src[i];
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[t][i]));
-      }
-      if (TYPE == MM_FP16) {
-        const float s = fp16_scale(fmaxf(top, __shfl_xor(top, 16, 64)));
-        mul *= inverse_pow2(s);
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[t][i] *= s;
-      }
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const v4i u = split8<TYPE>(v[t], j >= 2);
-#pragma unroll
-        for (int f = 0; f < 4; ++f) acc[f] = E::mma16(wf[f][t], u, acc[f]);
-      }
+        for (int f = 0; f < 4; ++f) acc[f] = E::mma16(wf[f][t], u[t], acc[f]);
     }
     // mul is its row's: the accumulator's column is the lane's own position q
     if (!live) continue;
@@ -318,7 +304,7 @@ static hipError_t run_expand(const LoraExpand& p, hipStream_t s) {
 template <int TYPE>
 static hipError_t expand_vec(const LoraExpand& p, hipStream_t s) {
   const bool v = (!p.base || vec16(p.base, p.ldbase, p.C)) && vec16(p.y, p.ldy, p.C);
-  const bool w = vec16(p.w, p.ldw, p.w_stride) && (p.R & 7) == 0;
+  const bool w = vec16(p.w, p.ldw, p.w_stride) && (p.R & 7) == 0;     // rows of whole 16-byte chunks
   if (v) return w ? run_expand<TYPE, true, true>(p, s) : run_expand<TYPE, true, false>(p, s);
   return w ? run_expand<TYPE, false, true>(p, s) : run_expand<TYPE, false, false>(p, s);
 }
@@ -346,16 +332,12 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(LoraOuter p, int chunk_
   const int64_t pos0 = (int64_t)rt.row0 + (int64_t)rt.t * chunk_rows;
   const int valid = min((int)(rt.m - rt.t * chunk_rows), chunk_rows);
   const int64_t c0 = (int64_t)blockIdx.y * OC;
-  auto factor = [&](int64_t pos, int r) {
-    float f = 0.0f;
-    for (int z = 0; z < p.parts; ++z) f += p.v[((int64_t)z * p.rows.M + pos) * p.R + r];
-    return f;
-  };
+  const int rp = (p.R + 15) & ~15;
   float scale = 1.0f;
   if (TYPE == MM_FP16) {                                          // one power of two for the chunk
     float top = 0.0f;
     for (int i = tid; i < valid * p.R; i += 256) {
-      const float f = fabsf(factor(pos0 + i / p.R, i % p.R));
+      const float f = fabsf(p.v.v[pos0 * p.R + i]);
       if (__builtin_isfinite(f)) top = fmaxf(top, f);
     }
     top = wave_max(top);
@@ -397,13 +379,17 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(LoraOuter p, int chunk_
       const int r = xr + 8 * i;
       *reinterpret_cast<v4i*>(sx + r * OC + (((xc >> 3) ^ ((r & 3) << 2)) << 3)) = xs[i];
     }
-    for (int i = tid; i < OP * VW; i += 256) {
-      const int m = i / VW, r = i % VW;
-      const float f = (b + m < valid && r < p.R) ? scale * factor(pos0 + b + m, r) : 0.0f;
-      const uint16_t h = E::down(f);
-      const float hf = E::up(h);
-      sv[0][i] = h;
-      sv[1][i] = E::down(__builtin_isfinite(hf) ? f - hf : 0.0f);
+    if (TYPE == MM_FP16) {
+      for (int i = tid; i < OP * VW; i += 256) {
+        const int m = i / VW, r = i % VW;
+        split<TYPE>((b + m < valid && r < p.R) ? scale * p.v.v[(pos0 + b + m) * p.R + r] : 0.0f, sv[0][i], sv[1][i]);
+      }
+    } else {
+      for (int i = tid; i < OP * RT * 4; i += 256) {              // 8 ranks of hi or lo
+        const int m = i / (RT * 4), h = i / (RT * 2) & 1, r = i % (RT * 2) * 8;
+        *reinterpret_cast<v4i*>(sv[h] + m * VW + r) =
+            b + m < valid && r < rp ? *reinterpret_cast<const v4i*>(p.v.hi + (pos0 + b + m) * 2 * rp + h * rp + r) : v4i{0, 0, 0, 0};
+      }
     }
     if (b + OP < valid) fetch(b + OP);
     __syncthreads();
@@ -460,27 +446,34 @@ __device__ __forceinline__ ChunkSpan find_chunks(const int32_t* count, int L, ui
   return s;
 }
 
-// Eight ranks of 256 columns of one adapter.
+// Four ranks of 256 columns of one adapter, four chunks' loads in flight.
 template <int TYPE, bool TRANSPOSED>
 __global__ __launch_bounds__(256) void lora_outer_sum_kernel(LoraOuter p, int chunk_rows) {
   using E = Elem<TYPE>;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int l = blockIdx.z, r0 = blockIdx.y * 8;
+  const int l = blockIdx.z, r0 = blockIdx.y * 4;
   const int64_t c = (int64_t)blockIdx.x * 256 + tid;
   const ChunkSpan s = find_chunks(p.rows.count, p.rows.L, (uint32_t)p.rows.M, chunk_rows, l, lane);
   if (c >= p.C) return;
-  float acc[8] = {};
-  for (uint32_t k = 0; k < s.n; ++k) {
-    const float* src = p.part + ((int64_t)(s.first + k) * p.R + r0) * p.C + c;
+  const int live = min(p.R - r0, 4);
+  float acc[4] = {};
+  for (uint32_t k = 0; k < s.n; k += 4) {
+    float v[4][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (r0 + i < p.R) acc[i] += src[i * p.C];
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[u][i] = k + u < s.n && i < live ? p.part[((int64_t)(s.first + k + u) * p.R + r0 + i) * p.C + c] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] += v[u][i];
   }
   const float sc = p.scales ? p.scales[l] : 1.0f;
   uint16_t* out = static_cast<uint16_t*>(p.out);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (r0 + i >= p.R) break;
+  for (int i = 0; i < 4; ++i) {
+    if (i >= live) break;
     const uint16_t v = s.n ? E::down(sc * acc[i]) : (uint16_t)0;
     if (TRANSPOSED) out[((int64_t)l * p.C + c) * p.R + r0 + i] = v;
     else out[((int64_t)l * p.R + r0 + i) * p.C + c] = v;
@@ -505,7 +498,7 @@ static hipError_t run_outer(const LoraOuter& p, hipStream_t s) {
   else if (p.R <= 64) hipLaunchKernelGGL((lora_outer_kernel<TYPE, VEC, 4>), grid, dim3(256), 0, s, p, rows);
   else hipLaunchKernelGGL((lora_outer_kernel<TYPE, VEC, 8>), grid, dim3(256), 0, s, p, rows);
   if (hipError_t e = hipGetLastError()) return e;
-  const dim3 sum((uint32_t)((p.C + 255) / 256), (uint32_t)((p.R + 7) / 8), (uint32_t)p.rows.L);
+  const dim3 sum((uint32_t)((p.C + 255) / 256), (uint32_t)((p.R + 3) / 4), (uint32_t)p.rows.L);
   if (p.transposed) hipLaunchKernelGGL((lora_outer_sum_kernel<TYPE, true>), sum, dim3(256), 0, s, p, rows);
   else hipLaunchKernelGGL((lora_outer_sum_kernel<TYPE, false>), sum, dim3(256), 0, s, p, rows);
   return hipGetLastError();
@@ -517,26 +510,39 @@ hipError_t launch_lora_outer(const LoraOuter& p, hipStream_t s) {
 }
 
 // ----------------------------------------------------------------------------- transposed weights
-// dst[l][c][r] = src[l][r][c] through a 64 x 64 tile; adapters without rows are left out.
-__global__ __launch_bounds__(256) void lora_transpose_kernel(const uint16_t* __restrict__ src, int64_t lds_, int64_t ss,
-                                                             int64_t R, int64_t C, uint16_t* __restrict__ dst,
-                                                             int64_t ldd, int64_t ds, const int32_t* __restrict__ count) {
-  __shared__ uint16_t t[64][66];
-  const int l = blockIdx.z;
-  if (count[l] <= 0) return;
-  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
+// dst[l][c][r] = src[l][r][c] through 64 x 64 tiles, two stacks in one launch; adapters without rows are
+// left out.
+struct TransposeArgs {
+  LoraTranspose t[2];
+  int64_t tiles[2], cols[2];      // tiles of one adapter, and along C
+  const int32_t* count;
+};
+__global__ __launch_bounds__(256) void lora_transpose_kernel(TransposeArgs a) {
+  __shared__ uint16_t s[64][66];
+  const int l = blockIdx.y;
+  if (a.count[l] <= 0) return;
+  const int w = blockIdx.x < a.tiles[0] ? 0 : 1;
+  const int64_t i = blockIdx.x - (w ? a.tiles[0] : 0);
+  const LoraTranspose t = a.t[w];
+  const int64_t r0 = i / a.cols[w] * 64, c0 = i % a.cols[w] * 64;
+  const uint16_t* src = static_cast<const uint16_t*>(t.src) + l * t.src_stride;
+  uint16_t* dst = static_cast<uint16_t*>(t.dst) + l * t.dst_stride;
   const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  for (int i = y; i < 64; i += 4)
-    if (r0 + i < R && c0 + x < C) t[i][x] = src[l * ss + (r0 + i) * lds_ + c0 + x];
+  for (int k = y; k < 64; k += 4)
+    if (r0 + k < t.R && c0 + x < t.C) s[k][x] = src[(r0 + k) * t.lds + c0 + x];
   __syncthreads();
-  for (int i = y; i < 64; i += 4)
-    if (c0 + i < C && r0 + x < ldd) dst[l * ds + (c0 + i) * ldd + r0 + x] = r0 + x < R ? t[x][i] : (uint16_t)0;
+  for (int k = y; k < 64; k += 4)
+    if (c0 + k < t.C && r0 + x < t.ldd) dst[(c0 + k) * t.ldd + r0 + x] = r0 + x < t.R ? s[x][k] : (uint16_t)0;
 }
-hipError_t launch_lora_transpose(const void* src, int64_t lds_, int64_t src_stride, int64_t R, int64_t C, void* dst,
-                                 int64_t ldd, int64_t dst_stride, const int32_t* count, int L, hipStream_t s) {
-  const dim3 grid((uint32_t)((C + 63) / 64), (uint32_t)((R + 63) / 64), (uint32_t)L);
-  hipLaunchKernelGGL(lora_transpose_kernel, grid, dim3(256), 0, s, static_cast<const uint16_t*>(src), lds_, src_stride,
-                     R, C, static_cast<uint16_t*>(dst), ldd, dst_stride, count);
+hipError_t launch_lora_transpose(const LoraTranspose* t, int n, const int32_t* count, int L, hipStream_t s) {
+  TransposeArgs a{};
+  for (int i = 0; i < n; ++i) {
+    a.t[i] = t[i];
+    a.cols[i] = (t[i].C + 63) / 64;
+    a.tiles[i] = a.cols[i] * ((t[i].R + 63) / 64);
+  }
+  a.count = count;
+  hipLaunchKernelGGL(lora_transpose_kernel, dim3((uint32_t)(a.tiles[0] + a.tiles[1]), (uint32_t)L), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -208,37 +208,44 @@ struct Carve {      // sections of a caller buffer at 256-byte offsets
     return p;
   }
 };
+LoraFactor carve_factor(Carve& c, int64_t M, int R) {
+  LoraFactor f;
+  f.hi = c.take<uint16_t>(M * 2 * lora_rp(R));
+  f.inv = c.take<float>(M);
+  f.v = c.take<float>(M * R);
+  return f;
+}
+LoraFactor of_type(LoraFactor f, int32_t type) {      // bf16 needs neither scales nor the fp32 values
+  if (type == GMLP_BF16) f.inv = f.v = nullptr;
+  return f;
+}
 struct LoraCtx {
   int32_t* count;
   int32_t* order;
-  float* u;
-  int parts;
+  LoraFactor u;
 };
-LoraCtx carve_lora_ctx(Carve& c, int64_t M, int64_t K, int R, int L) {
+LoraCtx carve_lora_ctx(Carve& c, int64_t M, int R, int L) {
   LoraCtx x;
-  x.parts = lora_shrink_parts(M, K, R, L);
   x.count = c.take<int32_t>(L + 1);
   x.order = c.take<int32_t>(M);
-  x.u = c.take<float>((int64_t)x.parts * M * R);
+  x.u = carve_factor(c, M, R);
   return x;
 }
 struct LoraWs {
   uint16_t* at;      // [L, K, ldr]
   uint16_t* bt;      // [L, R, ldn]
-  float* du;
+  LoraFactor du;
   float* part;
   int64_t ldr, ldn;
-  int parts;
 };
 int64_t up8(int64_t v) { return (v + 7) & ~int64_t(7); }
 LoraWs carve_lora_ws(Carve& c, int64_t M, int64_t K, int64_t N, int R, int L) {
   LoraWs w;
   w.ldr = up8(R);
   w.ldn = up8(N);
-  w.parts = lora_shrink_parts(M, N, R, L);
   w.at = c.take<uint16_t>((int64_t)L * K * w.ldr);
   w.bt = c.take<uint16_t>((int64_t)L * R * w.ldn);
-  w.du = c.take<float>((int64_t)w.parts * M * R);
+  w.du = carve_factor(c, M, R);
   w.part = c.take<float>(std::max(lora_outer_part_floats(M, K, R, L), lora_outer_part_floats(M, N, R, L)));
   return w;
 }
@@ -270,7 +277,7 @@ extern "C" gmlp_status gmlp_lora_query_sizes(int64_t M, int64_t K, int64_t N, in
   const gmlp_status st = check_lora_sizes(M, K, N, R, L);
   if (st != GMLP_OK) return st;
   Carve c{nullptr}, w{nullptr};
-  carve_lora_ctx(c, M, K, R, L);
+  carve_lora_ctx(c, M, R, L);
   carve_lora_ws(w, M, K, N, R, L);
   out->ctx_bytes = c.off + 256;
   out->fwd_ws_bytes = order_ws(M, L + 1);
@@ -298,13 +305,14 @@ extern "C" gmlp_status gmlp_lora_forward(const gmlp_lora_fwd_args* p, hipStream_
   if (sz.fwd_ws_bytes && (!p->ws || p->ws_bytes < sz.fwd_ws_bytes || !aligned16(p->ws)))
     return set_error(GMLP_WORKSPACE, "workspace: %zu bytes, 16-byte aligned, are needed", sz.fwd_ws_bytes);
   Carve c{static_cast<uint8_t*>(p->ctx)};
-  const LoraCtx x = carve_lora_ctx(c, p->M, p->K, p->R, p->L);
+  const LoraCtx x = carve_lora_ctx(c, p->M, p->R, p->L);
   const LoraRows rows{x.count, x.order, p->M, p->L};
   hipError_t e = launch_group_order(p->ids, p->M, p->L + 1, true, x.count, nullptr, x.order, static_cast<int32_t*>(p->ws), stream);
   if (e != hipSuccess) return launched(e, "adapter order");
-  LoraShrink s{p->dtype, p->R, rows, p->x, p->ldx, p->w.a, p->w.lda, p->w.a_stride, p->K, nullptr, x.u, x.parts};
+  const LoraFactor u = of_type(x.u, p->dtype);
+  LoraShrink s{p->dtype, p->R, rows, p->x, p->ldx, p->w.a, p->w.lda, p->w.a_stride, p->K, nullptr, u};
   if ((e = launch_lora_shrink(s, stream)) != hipSuccess) return launched(e, "lora shrink");
-  LoraExpand ex{p->dtype, p->R, rows, x.u, x.parts, p->w.b, p->w.ldb, p->w.b_stride, p->N, p->w.scales,
+  LoraExpand ex{p->dtype, p->R, rows, u, p->w.b, p->w.ldb, p->w.b_stride, p->N, p->w.scales,
                 p->base, p->ldbase, p->y, p->ldy};
   return launched(launch_lora_expand(ex, stream), "lora expand");
 }
@@ -340,27 +348,27 @@ extern "C" gmlp_status gmlp_lora_backward(const gmlp_lora_bwd_args* p, hipStream
     return fine();
   }
   Carve c{const_cast<uint8_t*>(static_cast<const uint8_t*>(p->ctx))}, cw{static_cast<uint8_t*>(p->ws)};
-  const LoraCtx x = carve_lora_ctx(c, p->M, K, R, L);
+  const LoraCtx x = carve_lora_ctx(c, p->M, R, L);
   const LoraWs w = carve_lora_ws(cw, p->M, K, N, R, L);
   const LoraRows rows{x.count, x.order, p->M, L};
+  const LoraFactor u = of_type(x.u, p->dtype), du = of_type(w.du, p->dtype);
   if (p->db) {
-    LoraOuter o{p->dtype, R, rows, x.u, x.parts, p->dy, p->lddy, N, p->w.scales, p->db, true, w.part};
+    LoraOuter o{p->dtype, R, rows, u, p->dy, p->lddy, N, p->w.scales, p->db, true, w.part};
     if ((e = launch_lora_outer(o, stream)) != hipSuccess) return launched(e, "lora db");
   }
   if (!p->dx && !p->da) return fine();
-  // du = scale dy b: the shrink over N with b transposed
-  if ((e = launch_lora_transpose(p->w.b, p->w.ldb, p->w.b_stride, N, R, w.bt, w.ldn, R * w.ldn, x.count, L, stream)) != hipSuccess)
-    return launched(e, "lora transpose");
-  LoraShrink s{p->dtype, R, rows, p->dy, p->lddy, w.bt, w.ldn, R * w.ldn, N, p->w.scales, w.du, w.parts};
+  // du = scale dy b is the shrink over N with b transposed, dx the expand with a transposed
+  const LoraTranspose t[2] = {{p->w.b, p->w.ldb, p->w.b_stride, N, R, w.bt, w.ldn, R * w.ldn},
+                              {p->w.a, p->w.lda, p->w.a_stride, R, K, w.at, w.ldr, K * w.ldr}};
+  if ((e = launch_lora_transpose(t, p->dx ? 2 : 1, x.count, L, stream)) != hipSuccess) return launched(e, "lora transpose");
+  LoraShrink s{p->dtype, R, rows, p->dy, p->lddy, w.bt, w.ldn, R * w.ldn, N, p->w.scales, du};
   if ((e = launch_lora_shrink(s, stream)) != hipSuccess) return launched(e, "lora shrink");
   if (p->dx) {
-    if ((e = launch_lora_transpose(p->w.a, p->w.lda, p->w.a_stride, R, K, w.at, w.ldr, K * w.ldr, x.count, L, stream)) != hipSuccess)
-      return launched(e, "lora transpose");
-    LoraExpand ex{p->dtype, R, rows, w.du, w.parts, w.at, w.ldr, K * w.ldr, K, nullptr, p->dx_add, p->lddx_add, p->dx, p->lddx};
+    LoraExpand ex{p->dtype, R, rows, du, w.at, w.ldr, K * w.ldr, K, nullptr, p->dx_add, p->lddx_add, p->dx, p->lddx};
     if ((e = launch_lora_expand(ex, stream)) != hipSuccess) return launched(e, "lora dx");
   }
   if (p->da) {
-    LoraOuter o{p->dtype, R, rows, w.du, w.parts, p->x, p->ldx, K, nullptr, p->da, false, w.part};
+    LoraOuter o{p->dtype, R, rows, du, p->x, p->ldx, K, nullptr, p->da, false, w.part};
     if ((e = launch_lora_outer(o, stream)) != hipSuccess) return launched(e, "lora da");
   }
   return fine();
