@@ -51,14 +51,15 @@ __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float(
 
 // ----------------------------------------------------------------------------- shrink
 // RB x 16 positions by RT x 16 ranks per workgroup, the contraction in blocks of 32 SPB dealt to its
-// NW waves, fragments straight from memory with the next block's loads in flight.  The waves are
-// joined through LDS, in order.  A workgroup for the whole contraction keeps v out of memory until
+// NW waves, fragments straight from memory.  The waves are joined through LDS, in order.  A workgroup for the whole contraction keeps v out of memory until
 // it is whole; the waves of a workgroup give the loads in flight that few positions cannot.
 template <int TYPE, bool VEC, int RB, int RT, int NW>
 __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraShrink p) {
   using E = Elem<TYPE>;
-  // registers: 256 a lane with 8 waves, 128 with 16
-  constexpr int SPB = NW > 8 ? (RB + RT <= 2 ? 4 : RB + RT <= 3 ? 2 : 1) : RB + RT <= 3 ? 4 : RB + RT <= 6 ? 2 : 1;
+  // A lane has 256 registers with 8 waves and holds two blocks; 128 with 16, whose other waves cover the
+  // loads of one.  Blocks of 64 at least where they fit: a row's 128-byte line is then read by one wave.
+  constexpr bool TWO = NW <= 8;
+  constexpr int F = RB + RT, SPB = TWO ? (F <= 3 ? 4 : F <= 6 ? 2 : 1) : (F <= 2 ? 8 : F <= 3 ? 4 : 2);
   constexpr int LD = RT * 16 + 4;
   __shared__ __align__(16) float red[NW * RB * 16 * LD];
   __shared__ float s_mul[RB * 16];
@@ -83,7 +84,7 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraShrink p) {
     for (int t = 0; t < RT; ++t) acc[b][t] = v4f{0, 0, 0, 0};
   constexpr int64_t step = 32 * SPB;
   const int64_t nblk = (p.C + step - 1) / step;
-  v4i xf[2][SPB][RB], wf[2][SPB][RT];
+  v4i xf[TWO ? 2 : 1][SPB][RB], wf[TWO ? 2 : 1][SPB][RT];
   auto fetch = [&](int64_t blk, int s) {
     const int64_t c0 = blk * step;
 #pragma unroll
@@ -105,7 +106,12 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraShrink p) {
         for (int t = 0; t < RT; ++t) acc[b][t] = E::mma16(wf[s][k][t], xf[s][k][b], acc[b][t]);
   };
   int64_t blk = wave;
-  if (blk < nblk) {
+  if constexpr (!TWO) {
+    for (; blk < nblk; blk += NW) {
+      fetch(blk, 0);
+      mul(0);
+    }
+  } else if (blk < nblk) {
     fetch(blk, 0);
     while (true) {
       if (blk + NW < nblk) fetch(blk + NW, 1);
@@ -203,22 +209,28 @@ hipError_t launch_lora_shrink(const LoraShrink& p, hipStream_t s) {
 }
 
 // ----------------------------------------------------------------------------- expand
-// A tile of positions by 256 columns, 64 per wave.  A wave keeps W_l's fragments of its columns in
-// registers and walks the positions 16 at a time.  The product is taken transposed with the
-// columns dealt so that a lane ends with 16 consecutive ones of one row: 32 bytes of base and y.
-template <int TYPE, bool VEC, bool VECW, int RT>
-__global__ __launch_bounds__(256) void lora_expand_kernel(LoraExpand p, int tile_rows) {
+// A tile of 16 RB positions by 256 columns, 64 per wave.  A wave keeps W_l's fragments of its columns
+// in registers and takes the positions 16 at a time, all rows of base on their way from the start.
+// The product is taken transposed with the columns dealt so that a lane ends with 16 consecutive
+// ones of one row: 32 bytes of base and y.
+template <int TYPE, bool VEC, bool VECW, int RB, int RT>
+__global__ __launch_bounds__(256) void lora_expand_kernel(LoraExpand p) {
   using E = Elem<TYPE>;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const RowTile rt = find_row_tile(p.rows.count, p.rows.L + 1, (uint32_t)p.rows.M, tile_rows, 1, false, blockIdx.x, lane);
+  const RowTile rt = find_row_tile(p.rows.count, p.rows.L + 1, (uint32_t)p.rows.M, 16 * RB, 1, false, blockIdx.x, lane);
   if (rt.g < 0) return;
   const bool rest = rt.g == p.rows.L;                    // rows without an adapter
   if (rest && p.base == p.y) return;
-  const int64_t pos0 = (int64_t)rt.row0 + (int64_t)rt.t * tile_rows;
-  const int valid = min((int)(rt.m - rt.t * tile_rows), tile_rows);
+  const int64_t pos0 = (int64_t)rt.row0 + (int64_t)rt.t * (16 * RB);
+  const int valid = min((int)(rt.m - rt.t * (16 * RB)), 16 * RB);
   const int q = lane & 15, j = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.y * 256 + wave * 64;
   if (n0 >= p.C) return;
+  const int64_t c = n0 + 16 * j;
+  const int cols = (int)min(p.C - c, (int64_t)16);       // of this lane
+  int32_t row[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) row[b] = p.rows.order[pos0 + min(16 * b + q, valid - 1)];
   v4i wf[4][RT];
   if (!rest) {
     const uint16_t* w = static_cast<const uint16_t*>(p.w) + rt.g * p.w_stride;
@@ -232,49 +244,51 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraExpand p, int tile
       }
     }
   }
+  v4i old[RB][2];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    old[b][0] = old[b][1] = v4i{0, 0, 0, 0};
+    if (p.base && 16 * b + q < valid) {
+      const uint16_t* src = static_cast<const uint16_t*>(p.base) + row[b] * p.ldbase + c;
+      old[b][0] = load8<VEC>(src, cols);
+      old[b][1] = load8<VEC>(src + 8, cols - 8);
+    }
+  }
   const float sc = !rest && p.scales ? p.scales[rt.g] : 1.0f;
   const int rp = (p.R + 15) & ~15;
-  const int64_t c = n0 + 16 * j;
-  const int cols = (int)min(p.C - c, (int64_t)16);       // of this lane
-  for (int b = 0; b < valid; b += 16) {
-    const int at = min(b + q, valid - 1);
-    const bool live = b + q < valid;
-    const int64_t row = p.rows.order[pos0 + at];
-    v4i old[2] = {v4i{0, 0, 0, 0}, v4i{0, 0, 0, 0}};
-    if (p.base && live) {
-      const uint16_t* src = static_cast<const uint16_t*>(p.base) + row * p.ldbase + c;
-      old[0] = load8<VEC>(src, cols);
-      old[1] = load8<VEC>(src + 8, cols - 8);
-    }
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    if (16 * b >= valid) break;
     v4f acc[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f) acc[f] = v4f{0, 0, 0, 0};
     float mul = sc;
     if (!rest) {
-      const uint16_t* src = p.v.hi + (pos0 + at) * 2 * rp + (j >= 2 ? rp : 0) + 8 * (j & 1);
+      const int64_t at = pos0 + min(16 * b + q, valid - 1);
+      const uint16_t* src = p.v.hi + at * 2 * rp + (j >= 2 ? rp : 0) + 8 * (j & 1);
       v4i u[RT];
 #pragma unroll
       for (int t = 0; t < RT; ++t) u[t] = 16 * t < rp ? *reinterpret_cast<const v4i*>(src + 16 * t) : v4i{0, 0, 0, 0};
-      if (p.v.inv) mul *= p.v.inv[pos0 + at];
+      if (p.v.inv) mul *= p.v.inv[at];
 #pragma unroll
       for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int f = 0; f < 4; ++f) acc[f] = E::mma16(wf[f][t], u[t], acc[f]);
     }
     // mul is its row's: the accumulator's column is the lane's own position q
-    if (!live) continue;
-    uint16_t* dst = static_cast<uint16_t*>(p.y) + row * p.ldy + c;
+    if (16 * b + q >= valid) continue;
+    uint16_t* dst = static_cast<uint16_t*>(p.y) + row[b] * p.ldy + c;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint16_t o = (uint16_t)((uint32_t)old[h][i / 2] >> (16 * (i & 1)));
+        const uint16_t o = (uint16_t)((uint32_t)old[b][h][i / 2] >> (16 * (i & 1)));
         y[i] = rest ? 0.0f : mul * acc[2 * h + i / 4][i & 3];
         y[i] = p.base ? E::up(o) + y[i] : y[i];
       }
       v4i out;
-      if (rest) out = old[h];                            // bit for bit
+      if (rest) out = old[b][h];                         // bit for bit
       else
 #pragma unroll
         for (int i = 0; i < 4; ++i) out[i] = (int)E::down2(y[2 * i], y[2 * i + 1]);
@@ -289,17 +303,21 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraExpand p, int tile
   }
 }
 
+template <int TYPE, bool VEC, bool VECW, int RB>
+static hipError_t run_expand_rows(const LoraExpand& p, hipStream_t s) {
+  const dim3 grid((uint32_t)tiles_bound(p.rows.M, p.rows.L + 1, 16 * RB), (uint32_t)((p.C + 255) / 256));
+  if (p.R <= 16) hipLaunchKernelGGL((lora_expand_kernel<TYPE, VEC, VECW, RB, 1>), grid, dim3(256), 0, s, p);
+  else if (p.R <= 32) hipLaunchKernelGGL((lora_expand_kernel<TYPE, VEC, VECW, RB, 2>), grid, dim3(256), 0, s, p);
+  else if (p.R <= 64) hipLaunchKernelGGL((lora_expand_kernel<TYPE, VEC, VECW, RB, 4>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((lora_expand_kernel<TYPE, VEC, VECW, RB, 8>), grid, dim3(256), 0, s, p);
+  return hipGetLastError();
+}
 template <int TYPE, bool VEC, bool VECW>
 static hipError_t run_expand(const LoraExpand& p, hipStream_t s) {
   // a tile of 16 positions while those leave the device unfilled, else 64: W is read once per tile
   const int64_t cols = (p.C + 255) / 256;
-  const int rows = tiles_bound(p.rows.M, p.rows.L + 1, 16) * cols < 2048 ? 16 : 64;
-  const dim3 grid((uint32_t)tiles_bound(p.rows.M, p.rows.L + 1, rows), (uint32_t)cols);
-  if (p.R <= 16) hipLaunchKernelGGL((lora_expand_kernel<TYPE, VEC, VECW, 1>), grid, dim3(256), 0, s, p, rows);
-  else if (p.R <= 32) hipLaunchKernelGGL((lora_expand_kernel<TYPE, VEC, VECW, 2>), grid, dim3(256), 0, s, p, rows);
-  else if (p.R <= 64) hipLaunchKernelGGL((lora_expand_kernel<TYPE, VEC, VECW, 4>), grid, dim3(256), 0, s, p, rows);
-  else hipLaunchKernelGGL((lora_expand_kernel<TYPE, VEC, VECW, 8>), grid, dim3(256), 0, s, p, rows);
-  return hipGetLastError();
+  if (tiles_bound(p.rows.M, p.rows.L + 1, 16) * cols < 2048) return run_expand_rows<TYPE, VEC, VECW, 1>(p, s);
+  return run_expand_rows<TYPE, VEC, VECW, 4>(p, s);
 }
 template <int TYPE>
 static hipError_t expand_vec(const LoraExpand& p, hipStream_t s) {
@@ -528,11 +546,20 @@ __global__ __launch_bounds__(256) void lora_transpose_kernel(TransposeArgs a) {
   const uint16_t* src = static_cast<const uint16_t*>(t.src) + l * t.src_stride;
   uint16_t* dst = static_cast<uint16_t*>(t.dst) + l * t.dst_stride;
   const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  for (int k = y; k < 64; k += 4)
-    if (r0 + k < t.R && c0 + x < t.C) s[k][x] = src[(r0 + k) * t.lds + c0 + x];
+  uint16_t v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int64_t r = r0 + y + 4 * i;
+    v[i] = r < t.R && c0 + x < t.C ? src[r * t.lds + c0 + x] : (uint16_t)0;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[y + 4 * i][x] = v[i];
   __syncthreads();
-  for (int k = y; k < 64; k += 4)
-    if (c0 + k < t.C && r0 + x < t.ldd) dst[(c0 + k) * t.ldd + r0 + x] = r0 + x < t.R ? s[x][k] : (uint16_t)0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int64_t c = c0 + y + 4 * i;
+    if (c < t.C && r0 + x < t.ldd) dst[c * t.ldd + r0 + x] = s[x][y + 4 * i];
+  }
 }
 hipError_t launch_lora_transpose(const LoraTranspose* t, int n, const int32_t* count, int L, hipStream_t s) {
   TransposeArgs a{};
