@@ -152,12 +152,16 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraShrink p) {
       if (e < N) red[e / (RT * 16) * LD + e % (RT * 16)] = v[i];
     }
     __syncthreads();
-    if (tid < RB * 16) {
+    for (int row = wave; row < RB * 16; row += NW) {
       float top = 0.0f;
-      for (int r = 0; r < p.R; ++r) top = fmaxf(top, fabsf(red[tid * LD + r]));
-      const float s = fp16_scale(top);
-      s_mul[tid] = s;
-      if (tid < valid) p.out.inv[pos0 + tid] = inverse_pow2(s);
+#pragma unroll
+      for (int r = 0; r < RT * 16; r += 64)
+        if (r + lane < RT * 16) top = fmaxf(top, fabsf(red[row * LD + r + lane]));       // zero behind rank R
+      const float s = fp16_scale(wave_max(top));
+      if (lane == 0) {
+        s_mul[row] = s;
+        if (row < valid) p.out.inv[pos0 + row] = inverse_pow2(s);
+      }
     }
     __syncthreads();
   }
@@ -372,16 +376,24 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(LoraOuter p, int chunk_
   // a thread stages 8 columns of rows tid / 32 + 8 i
   const int xr = tid >> 5, xc = (tid & 31) * 8;
   const int xcols = (int)min(p.C - c0 - xc, (int64_t)8);
-  v4i xs[OP / 8];
-  auto fetch = [&](int b) {
+  // Two stages of rows in flight, their indices one stage further ahead.
+  v4i xs[2][OP / 8];
+  int32_t idx[OP / 8];
+  auto rows_of = [&](int b) {
 #pragma unroll
-    for (int i = 0; i < OP / 8; ++i) {
-      const int r = b + xr + 8 * i;
-      xs[i] = r < valid ? load8<VEC>(static_cast<const uint16_t*>(p.x) + p.rows.order[pos0 + r] * p.ldx + c0 + xc, xcols)
-                        : v4i{0, 0, 0, 0};
-    }
+    for (int i = 0; i < OP / 8; ++i) idx[i] = p.rows.order[pos0 + min(b + xr + 8 * i, valid - 1)];
   };
-  fetch(0);
+  auto fetch = [&](int b, v4i* x) {
+#pragma unroll
+    for (int i = 0; i < OP / 8; ++i)
+      x[i] = b + xr + 8 * i < valid ? load8<VEC>(static_cast<const uint16_t*>(p.x) + (int64_t)idx[i] * p.ldx + c0 + xc, xcols)
+                                    : v4i{0, 0, 0, 0};
+  };
+  rows_of(0);
+  fetch(0, xs[0]);
+  rows_of(OP);
+  fetch(OP, xs[1]);
+  rows_of(2 * OP);
   const int i16 = lane & 15, r4 = i16 >> 2, j = lane >> 4;
   const uint32_t sx0 = (uint32_t)(uintptr_t)sx, sv0 = (uint32_t)(uintptr_t)sv;
   typedef __attribute__((address_space(3))) v4s lds_v4s;
@@ -390,12 +402,12 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(LoraOuter p, int chunk_
     const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)(a + step)));
     return v4i{lo.x, lo.y, hi.x, hi.y};
   };
-  for (int b = 0; b < valid; b += OP) {
+  auto stage = [&](int b, v4i* x) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < OP / 8; ++i) {
       const int r = xr + 8 * i;
-      *reinterpret_cast<v4i*>(sx + r * OC + (((xc >> 3) ^ ((r & 3) << 2)) << 3)) = xs[i];
+      *reinterpret_cast<v4i*>(sx + r * OC + (((xc >> 3) ^ ((r & 3) << 2)) << 3)) = x[i];
     }
     if (TYPE == MM_FP16) {
       for (int i = tid; i < OP * VW; i += 256) {
@@ -409,7 +421,10 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(LoraOuter p, int chunk_
             b + m < valid && r < rp ? *reinterpret_cast<const v4i*>(p.v.hi + (pos0 + b + m) * 2 * rp + h * rp + r) : v4i{0, 0, 0, 0};
       }
     }
-    if (b + OP < valid) fetch(b + OP);
+    if (b + 2 * OP < valid) {
+      fetch(b + 2 * OP, x);
+      rows_of(b + 3 * OP);
+    }
     __syncthreads();
 #pragma unroll
     for (int ks = 0; ks < OP / 32; ++ks) {
@@ -429,6 +444,10 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(LoraOuter p, int chunk_
           for (int f = 0; f < 4; ++f) acc[t][f] = E::mma16(vf, xf[f], acc[t][f]);
         }
     }
+  };
+  for (int b = 0; b < valid; b += 2 * OP) {
+    stage(b, xs[0]);
+    if (b + OP < valid) stage(b + OP, xs[1]);
   }
   // lane: ranks 16 t + 4 j + i, column 16 f + lane % 16
   const float inv = inverse_pow2(scale);
