@@ -48,9 +48,14 @@ __device__ __forceinline__ uint64_t sgpr64(uint64_t v) {
 // for every outstanding DMA before each LDS read; the kernel counts them itself.  The compiler may
 // have written the scalar operands by a vector instruction just before (a lane read), which a
 // vector-memory instruction must not read for five wait states: the move and the s_nop are those.
+template <bool STREAM>
 __device__ __forceinline__ void dma16(v4i rsrc, uint32_t voff, uint32_t soff, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-               :: "v"(voff), "s"(rsrc), "s"(soff), "s"(m0) : "memory");
+  if constexpr (STREAM)
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"(m0) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"(m0) : "memory");
 }
 template <int VM>
 __device__ __forceinline__ void wait_stage() {      // all LDS reads back, at most VM DMAs in flight
@@ -61,8 +66,8 @@ __device__ __forceinline__ void wait_stage() {      // all LDS reads back, at mo
 
 constexpr uint32_t kNoLane = 0x80000000u;            // past every range: the lane reads zeros
 
-// One operand's stream of units.
-template <bool TR, int T, int NT>
+// One operand's stream of units.  ONCE: read by one tile only (non-temporal loads).
+template <bool TR, int T, int NT, bool ONCE = false>
 struct Feed {
   static constexpr int kDma = T * 128 / (NT * 16);   // DMAs per unit and wave
   uint64_t base;                // address of the current stage's unit
@@ -106,7 +111,7 @@ struct Feed {
   }
   // DMA number i of the unit (after next()).
   __device__ __forceinline__ void issue(int i, uint32_t slot, int wave) {
-    dma16(rsrc, v, (uint32_t)sgpr(i * step), (uint32_t)sgpr(slot + i * NT * 16 + wave * 1024));
+    dma16<ONCE>(rsrc, v, (uint32_t)sgpr(i * step), (uint32_t)sgpr(slot + i * NT * 16 + wave * 1024));
   }
   __device__ __forceinline__ void issue_all(uint32_t slot, int wave) {
     next();
@@ -206,7 +211,7 @@ struct Staged {
   }
 };
 
-template <int TYPE, int LAYOUT, int OUT, bool VEC>
+template <int TYPE, int LAYOUT, int OUT, bool VEC, bool ONCE>
 __global__ __launch_bounds__(256, 2) void gmm_ring_kernel(MmArgs p) {
   using E = Elem<TYPE>;
   constexpr int T = 128, NWN = 2, NT = 256, SLOT = T * 128;
@@ -304,7 +309,7 @@ __global__ __launch_bounds__(256, 2) void gmm_ring_kernel(MmArgs p) {
     static_assert(NA == 2 && NB == 2, "reads alternate between the operands");
     if constexpr (VEC) {
       Feed<AT, T, NT> fa;
-      Feed<BT, T, NT> fb;
+      Feed<BT, T, NT, ONCE> fb;
       fa.init(A, p.lda, arows, kn, tid);
       fb.init(B, p.ldb, bcols, kn, tid);
       constexpr int P = Feed<AT, T, NT>::kDma;
@@ -934,6 +939,15 @@ int64_t grouped_matmul_part_floats(int layout, int G, int64_t M, int64_t n, int6
   return parts > 1 ? parts * (layout == MM_WGRAD ? G * n * k : M * n) : 0;
 }
 
+// Non-temporal loads of the weights: groups of so few rows that a weight meets one row tile, and
+// weights past twice the last-level cache, so that none is still there from the call before.
+// Measured (us, forward, plain / non-temporal): 128 x 4096 x 7168 with 64 rows 558 / 511, with 128
+// rows 869 / 783; 64 x 2816 x 2048 (738 MB) at 16 rows a group 133 / 120, at 32 149 / 145, at 64
+// 155 / 162, at 128 203 / 254; 8 x 4096 x 4096 (268 MB) at 4 rows 53 / 59.
+static bool weights_once(const MmArgs& p) {
+  return p.M <= 32 * (int64_t)p.G && 2.0 * std::min<int64_t>(p.G, p.M) * p.n * p.k > 512e6;
+}
+
 template <int TYPE, int LAYOUT, int OUT, bool VEC>
 static hipError_t run_ring(const MmArgs& p, hipStream_t s) {
   constexpr int T = 128;
@@ -945,7 +959,8 @@ static hipError_t run_ring(const MmArgs& p, hipStream_t s) {
     grid = 8 * ((row_tiles_bound(p, T) * ((p.n + T - 1) / T) + 7) / 8);
   }
   grid = std::max<int64_t>(grid, 8);
-  auto* k = gmm_ring_kernel<TYPE, LAYOUT, OUT, VEC>;
+  const bool once = VEC && LAYOUT != MM_WGRAD && weights_once(p);
+  auto* k = once ? gmm_ring_kernel<TYPE, LAYOUT, OUT, VEC, VEC && LAYOUT != MM_WGRAD> : gmm_ring_kernel<TYPE, LAYOUT, OUT, VEC, false>;
   hipLaunchKernelGGL(k, dim3((uint32_t)grid, OUT == MM_OUT_PART ? p.parts : 1), dim3(256), 0, s, p);
   return hipGetLastError();
 }
