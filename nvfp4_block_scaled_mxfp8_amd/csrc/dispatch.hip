@@ -139,14 +139,19 @@ hipError_t launch_group_order(const int32_t* ids, int64_t n, int G, bool rest, i
 }
 
 // ----------------------------------------------------------------------------- moves
-// A thread owns V consecutive elements (16 bytes; one where rows are not 16-byte aligned) of one
-// token's row and its k rows on the other side.
+// A thread owns V consecutive elements of one token's row and its k rows on the other side: 16 bytes,
+// one element where a row holds less.  Rows that are not whole 16-byte chunks: the last chunk is the
+// row's last eight elements (the hardware takes any alignment), so it overlaps the one before, with
+// the same values.
 constexpr int MT = 256;
 
 template <int V>
 struct Chunk {
   uint16_t e[V];
 };
+typedef int v4i_any __attribute__((ext_vector_type(4), aligned(2)));
+template <int V>
+__device__ __forceinline__ int chunk_start(int c, int H) { return V == 8 ? min(c * 8, H - 8) : c; }
 // NT: non-temporal, for rows in expert order that do not fit the last-level cache: they are read or
 // written once, and dirty lines left in the cache slow the kernels behind.  Measured on 65536 rows of
 // 7168 (940 MB; us, plain / loads alone / loads and stores): combine 285 / 233 / 210, its gradient
@@ -155,7 +160,7 @@ struct Chunk {
 template <int V, bool NT = false>
 __device__ __forceinline__ Chunk<V> load_chunk(const uint16_t* p) {
   if constexpr (V == 8) {
-    const v4i* q = reinterpret_cast<const v4i*>(p);
+    const v4i_any* q = reinterpret_cast<const v4i_any*>(p);
     return __builtin_bit_cast(Chunk<8>, NT ? __builtin_nontemporal_load(q) : *q);
   }
   Chunk<V> c;
@@ -165,8 +170,9 @@ __device__ __forceinline__ Chunk<V> load_chunk(const uint16_t* p) {
 template <int V, bool NT = false>
 __device__ __forceinline__ void store_chunk(uint16_t* p, const Chunk<V>& c) {
   if constexpr (V == 8) {
-    if (NT) __builtin_nontemporal_store(__builtin_bit_cast(v4i, c), reinterpret_cast<v4i*>(p));
-    else *reinterpret_cast<v4i*>(p) = __builtin_bit_cast(v4i, c);
+    v4i_any* q = reinterpret_cast<v4i_any*>(p);
+    if (NT) __builtin_nontemporal_store(__builtin_bit_cast(v4i_any, c), q);
+    else *q = __builtin_bit_cast(v4i_any, c);
   } else {
     *p = c.e[0];
   }
@@ -211,12 +217,13 @@ __global__ __launch_bounds__(MT) void dispatch_kernel(MoveArgs p, int chunks, in
     for (int o = 32; o >= 1; o >>= 1) used += __shfl_xor(used, o, 64);
     const Chunk<V> zero = {};
     for (int64_t r = used + (blockIdx.x - blocks); r < M; r += kRestBlocks)
-      for (int c = threadIdx.x; c < chunks; c += MT) store_chunk<V>(dst + r * p.ld_dst + c * V, zero);
+      for (int c = threadIdx.x; c < chunks; c += MT) store_chunk<V>(dst + r * p.ld_dst + chunk_start<V>(c, p.H), zero);
     return;
   }
   const Place w = place_of(chunks, p.T, blockIdx.x, threadIdx.x);
   if (w.t < 0) return;
-  const Chunk<V> x = load_chunk<V>(static_cast<const uint16_t*>(p.src) + w.t * p.ld_src + w.c * V);
+  const int at = chunk_start<V>(w.c, p.H);
+  const Chunk<V> x = load_chunk<V>(static_cast<const uint16_t*>(p.src) + w.t * p.ld_src + at);
   for (int j = 0; j < p.k; ++j) {
     const int32_t r = p.rows[w.t * p.k + j];
     if ((uint64_t)(int64_t)r >= (uint64_t)M) continue;
@@ -226,7 +233,7 @@ __global__ __launch_bounds__(MT) void dispatch_kernel(MoveArgs p, int chunks, in
 #pragma unroll
       for (int i = 0; i < V; ++i) y.e[i] = E::down(f * E::up(x.e[i]));
     }
-    store_chunk<V, NT>(dst + r * p.ld_dst + w.c * V, y);
+    store_chunk<V, NT>(dst + r * p.ld_dst + at, y);
   }
 }
 
@@ -237,6 +244,7 @@ __global__ __launch_bounds__(MT) void combine_kernel(MoveArgs p, int chunks) {
   const int64_t M = p.T * p.k;
   const Place w = place_of(chunks, p.T, blockIdx.x, threadIdx.x);
   if (w.t < 0) return;
+  const int at = chunk_start<V>(w.c, p.H);
   float acc[V] = {};
   for (int j0 = 0; j0 < p.k; j0 += 8) {      // eight rows' loads in flight
     Chunk<V> x[8];
@@ -248,7 +256,7 @@ __global__ __launch_bounds__(MT) void combine_kernel(MoveArgs p, int chunks) {
       const int32_t r = in ? p.rows[w.t * p.k + j0 + j] : -1;
       live[j] = (uint64_t)(int64_t)r < (uint64_t)M;
       f[j] = SCALE && in ? p.probs[w.t * p.k + j0 + j] : 1.0f;
-      if (live[j]) x[j] = load_chunk<V, NT>(src + r * p.ld_src + w.c * V);
+      if (live[j]) x[j] = load_chunk<V, NT>(src + r * p.ld_src + at);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -259,7 +267,7 @@ __global__ __launch_bounds__(MT) void combine_kernel(MoveArgs p, int chunks) {
   Chunk<V> y;
 #pragma unroll
   for (int i = 0; i < V; ++i) y.e[i] = E::down(acc[i]);
-  store_chunk<V>(static_cast<uint16_t*>(p.dst) + w.t * p.ld_dst + w.c * V, y);
+  store_chunk<V>(static_cast<uint16_t*>(p.dst) + w.t * p.ld_dst + at, y);
 }
 
 // One block per token: the products of its gradient with its k rows, in fp32, summed by thread, by
@@ -281,16 +289,18 @@ __global__ __launch_bounds__(MT) void combine_dprobs_kernel(MoveArgs p, int chun
       if ((uint64_t)(int64_t)r[j] >= (uint64_t)M) r[j] = -1;
     }
     for (int c = tid; c < chunks; c += MT) {
-      const Chunk<V> d = load_chunk<V>(dy + c * V);
+      const int at = chunk_start<V>(c, p.H);
+      const Chunk<V> d = load_chunk<V>(dy + at);
       Chunk<V> x[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (r[j] >= 0) x[j] = load_chunk<V, NT>(v + r[j] * p.ld_src2 + c * V);
+        if (r[j] >= 0) x[j] = load_chunk<V, NT>(v + r[j] * p.ld_src2 + at);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (r[j] >= 0)
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[j] = fmaf(E::up(d.e[i]), E::up(x[j].e[i]), acc[j]);
+          for (int i = 0; i < V; ++i)
+            if (at + i >= c * V) acc[j] = fmaf(E::up(d.e[i]), E::up(x[j].e[i]), acc[j]);   // not the chunk before's
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -308,9 +318,6 @@ __global__ __launch_bounds__(MT) void combine_dprobs_kernel(MoveArgs p, int chun
   }
 }
 
-static bool rows16(const void* p, int64_t ld, int H) {
-  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ((ld | H) & 7) == 0;
-}
 static hipError_t grid_ok(int64_t blocks) { return blocks <= 0x7FFFFFFF ? hipSuccess : hipErrorInvalidValue; }
 
 // Half the 256 MB last-level cache.
@@ -353,19 +360,16 @@ static hipError_t run_dprobs(const MoveArgs& p, hipStream_t s) {
 }
 
 hipError_t launch_dispatch(const MoveArgs& p, hipStream_t s) {
-  const bool v = rows16(p.src, p.ld_src, p.H) && rows16(p.dst, p.ld_dst, p.H);
-  if (p.type == MM_BF16) return v ? run_dispatch<MM_BF16, 8>(p, s) : run_dispatch<MM_BF16, 1>(p, s);
-  return v ? run_dispatch<MM_FP16, 8>(p, s) : run_dispatch<MM_FP16, 1>(p, s);
+  if (p.type == MM_BF16) return p.H >= 8 ? run_dispatch<MM_BF16, 8>(p, s) : run_dispatch<MM_BF16, 1>(p, s);
+  return p.H >= 8 ? run_dispatch<MM_FP16, 8>(p, s) : run_dispatch<MM_FP16, 1>(p, s);
 }
 hipError_t launch_combine(const MoveArgs& p, hipStream_t s) {
-  const bool v = rows16(p.src, p.ld_src, p.H) && rows16(p.dst, p.ld_dst, p.H);
-  if (p.type == MM_BF16) return v ? run_combine<MM_BF16, 8>(p, s) : run_combine<MM_BF16, 1>(p, s);
-  return v ? run_combine<MM_FP16, 8>(p, s) : run_combine<MM_FP16, 1>(p, s);
+  if (p.type == MM_BF16) return p.H >= 8 ? run_combine<MM_BF16, 8>(p, s) : run_combine<MM_BF16, 1>(p, s);
+  return p.H >= 8 ? run_combine<MM_FP16, 8>(p, s) : run_combine<MM_FP16, 1>(p, s);
 }
 hipError_t launch_combine_dprobs(const MoveArgs& p, hipStream_t s) {
-  const bool v = rows16(p.src, p.ld_src, p.H) && rows16(p.src2, p.ld_src2, p.H);
-  if (p.type == MM_BF16) return v ? run_dprobs<MM_BF16, 8>(p, s) : run_dprobs<MM_BF16, 1>(p, s);
-  return v ? run_dprobs<MM_FP16, 8>(p, s) : run_dprobs<MM_FP16, 1>(p, s);
+  if (p.type == MM_BF16) return p.H >= 8 ? run_dprobs<MM_BF16, 8>(p, s) : run_dprobs<MM_BF16, 1>(p, s);
+  return p.H >= 8 ? run_dprobs<MM_FP16, 8>(p, s) : run_dprobs<MM_FP16, 1>(p, s);
 }
 
 }  // namespace gmlp

@@ -158,21 +158,6 @@ struct Frags {
 
 #define MM_FENCE() __builtin_amdgcn_sched_barrier(0)
 
-// Eight elements from any even address, `valid` of which exist.
-__device__ __forceinline__ v4i load8_any(const uint16_t* p, int valid) {
-  v4i v{0, 0, 0, 0};
-  if (valid >= 8) {
-    __builtin_memcpy(&v, p, 16);
-  } else {
-    uint32_t w[4] = {};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < valid) w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
-    v = v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-  }
-  return v;
-}
-
 // The same units as a Feed's, through registers.
 template <bool TR, int T, int NT>
 struct Staged {
@@ -180,10 +165,13 @@ struct Staged {
   const uint16_t* ptr;          // this thread's chunk of the next unit
   int64_t ld;
   int left, valid, row, chunk;
+  int have;                     // elements of the chunk that exist, in the unit loaded last
+  bool brief;                   // rows of fewer than eight elements
   v4i v[N];
-  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld_, int valid_, int64_t kn, int tid) {
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld_, int valid_, int64_t kn, bool brief_, int tid) {
     ld = ld_;
     valid = valid_;
+    brief = brief_;
     left = (int)min(kn, (int64_t)0x40000000);
     if (!TR) {
       row = tid >> 3;
@@ -196,18 +184,19 @@ struct Staged {
   }
   __device__ __forceinline__ void load() {
     constexpr int ROWS = TR ? NT / (T / 8) : NT / 8;
+    have = (TR ? valid : left) - 8 * chunk;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int r = row + i * ROWS;
-      const int n = TR ? (r < left ? valid - 8 * chunk : 0) : (r < valid ? left - 8 * chunk : 0);
-      v[i] = load8_any(ptr + i * ROWS * ld, n);
+      const int n = row + i * ROWS < (TR ? left : valid) ? have : 0;
+      v[i] = brief ? load8_short(ptr + i * ROWS * ld, n) : load8_raw(ptr + i * ROWS * ld, n);
     }
     ptr += TR ? 64 * ld : 64;
     left -= 64;
   }
   __device__ __forceinline__ void store(uint32_t slot, int tid) const {
 #pragma unroll
-    for (int i = 0; i < N; ++i) *(__attribute__((address_space(3))) v4i*)(uintptr_t)(slot + (i * NT + tid) * 16) = v[i];
+    for (int i = 0; i < N; ++i)
+      *(__attribute__((address_space(3))) v4i*)(uintptr_t)(slot + (i * NT + tid) * 16) = brief ? v[i] : shift8(v[i], have);
   }
 };
 
@@ -368,8 +357,8 @@ __global__ __launch_bounds__(256, 2) void gmm_ring_kernel(MmArgs p) {
     } else {
       Staged<AT, T, NT> fa;
       Staged<BT, T, NT> fb;
-      fa.init(A, p.lda, arows, kn, tid);
-      fb.init(B, p.ldb, bcols, kn, tid);
+      fa.init(A, p.lda, arows, kn, (AT ? p.n : p.k) < 8, tid);
+      fb.init(B, p.ldb, bcols, kn, (BT ? ncols : p.k) < 8, tid);
       fa.load();
       fb.load();
       for (int s = 0; s < nst; ++s) {

@@ -15,20 +15,17 @@
 namespace gmlp {
 
 // ----------------------------------------------------------------------------- loads
-// Eight consecutive elements from p, of which `valid` exist.
+// Eight consecutive elements of a row from p, of which `valid` exist: load8 then fix8 (which moves the
+// ragged end of an unaligned row down).  brief: rows of fewer than eight elements.
 template <bool VEC>
-__device__ __forceinline__ v4i load8(const uint16_t* p, int valid) {
-  if constexpr (VEC) {
-    return valid > 0 ? *reinterpret_cast<const v4i*>(p) : v4i{0, 0, 0, 0};
-  } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = 2 * i < valid ? p[2 * i] : 0u, hi = 2 * i + 1 < valid ? p[2 * i + 1] : 0u;
-      w[i] = lo | (hi << 16);
-    }
-    return v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-  }
+__device__ __forceinline__ v4i load8(const uint16_t* p, int valid, bool brief) {
+  if constexpr (VEC) return valid > 0 ? *reinterpret_cast<const v4i*>(p) : v4i{0, 0, 0, 0};
+  else return brief ? load8_short(p, valid) : load8_raw(p, valid);
+}
+template <bool VEC>
+__device__ __forceinline__ v4i fix8(v4i v, int valid, bool brief) {
+  if constexpr (VEC) return v;
+  else return brief ? v : shift8(v, valid);
 }
 
 // v as a factor of the 16-bit products: hi = T(v), lo = T(v - hi).
@@ -83,6 +80,7 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraShrink p) {
 #pragma unroll
     for (int t = 0; t < RT; ++t) acc[b][t] = v4f{0, 0, 0, 0};
   constexpr int64_t step = 32 * SPB;
+  const bool brief = p.C < 8;
   const int64_t nblk = (p.C + step - 1) / step;
   v4i xf[TWO ? 2 : 1][SPB][RB], wf[TWO ? 2 : 1][SPB][RT];
   auto fetch = [&](int64_t blk, int s) {
@@ -92,12 +90,22 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraShrink p) {
       const int64_t c = c0 + 32 * k;
       const int left = (int)min(p.C - c - 8 * j, (int64_t)8);
 #pragma unroll
-      for (int b = 0; b < RB; ++b) xf[s][k][b] = load8<VEC>(xr[b] + c, left);
+      for (int b = 0; b < RB; ++b) xf[s][k][b] = load8<VEC>(xr[b] + c, left, brief);
 #pragma unroll
-      for (int t = 0; t < RT; ++t) wf[s][k][t] = load8<VEC>(wr[t] + c, left);
+      for (int t = 0; t < RT; ++t) wf[s][k][t] = load8<VEC>(wr[t] + c, left, brief);
     }
   };
-  auto mul = [&](int s) {
+  auto mul = [&](int64_t blk, int s) {
+    if constexpr (!VEC) {
+#pragma unroll
+      for (int k = 0; k < SPB; ++k) {
+        const int left = (int)min(p.C - blk * step - 32 * k - 8 * j, (int64_t)8);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) xf[s][k][b] = fix8<VEC>(xf[s][k][b], left, brief);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) wf[s][k][t] = fix8<VEC>(wf[s][k][t], left, brief);
+      }
+    }
 #pragma unroll
     for (int k = 0; k < SPB; ++k)
 #pragma unroll
@@ -109,17 +117,17 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraShrink p) {
   if constexpr (!TWO) {
     for (; blk < nblk; blk += NW) {
       fetch(blk, 0);
-      mul(0);
+      mul(blk, 0);
     }
   } else if (blk < nblk) {
     fetch(blk, 0);
     while (true) {
       if (blk + NW < nblk) fetch(blk + NW, 1);
-      mul(0);
+      mul(blk, 0);
       blk += NW;
       if (blk >= nblk) break;
       if (blk + NW < nblk) fetch(blk + NW, 0);
-      mul(1);
+      mul(blk, 1);
       blk += NW;
       if (blk >= nblk) break;
     }
@@ -244,7 +252,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraExpand p) {
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         const int r = 16 * t + 8 * (j & 1);
-        wf[f][t] = load8<VECW>(w + n * p.ldw + r, min(p.R - r, 8));
+        wf[f][t] = load8<VECW>(w + n * p.ldw + r, min(p.R - r, 8), p.R < 8);
       }
     }
   }
@@ -254,15 +262,23 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraExpand p) {
     old[b][0] = old[b][1] = v4i{0, 0, 0, 0};
     if (p.base && 16 * b + q < valid) {
       const uint16_t* src = static_cast<const uint16_t*>(p.base) + row[b] * p.ldbase + c;
-      old[b][0] = load8<VEC>(src, cols);
-      old[b][1] = load8<VEC>(src + 8, cols - 8);
+      old[b][0] = load8<VEC>(src, cols, p.C < 8);
+      old[b][1] = load8<VEC>(src + 8, cols - 8, p.C < 8);
     }
+  }
+  if (!VECW && !rest) {
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) wf[f][t] = fix8<VECW>(wf[f][t], min(p.R - 16 * t - 8 * (j & 1), 8), p.R < 8);
   }
   const float sc = !rest && p.scales ? p.scales[rt.g] : 1.0f;
   const int rp = (p.R + 15) & ~15;
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
     if (16 * b >= valid) break;
+    old[b][0] = fix8<VEC>(old[b][0], cols, p.C < 8);
+    old[b][1] = fix8<VEC>(old[b][1], cols - 8, p.C < 8);
     v4f acc[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f) acc[f] = v4f{0, 0, 0, 0};
@@ -298,6 +314,8 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraExpand p) {
         for (int i = 0; i < 4; ++i) out[i] = (int)E::down2(y[2 * i], y[2 * i + 1]);
       if constexpr (VEC) {
         if (cols > 8 * h) *reinterpret_cast<v4i*>(dst + 8 * h) = out;
+      } else if (cols >= 8 * h + 8) {
+        __builtin_memcpy(dst + 8 * h, &out, 16);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -386,7 +404,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(LoraOuter p, int chunk_
   auto fetch = [&](int b, v4i* x) {
 #pragma unroll
     for (int i = 0; i < OP / 8; ++i)
-      x[i] = b + xr + 8 * i < valid ? load8<VEC>(static_cast<const uint16_t*>(p.x) + (int64_t)idx[i] * p.ldx + c0 + xc, xcols)
+      x[i] = b + xr + 8 * i < valid ? load8<VEC>(static_cast<const uint16_t*>(p.x) + (int64_t)idx[i] * p.ldx + c0 + xc, xcols, p.C < 8)
                                     : v4i{0, 0, 0, 0};
   };
   rows_of(0);
@@ -407,7 +425,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(LoraOuter p, int chunk_
 #pragma unroll
     for (int i = 0; i < OP / 8; ++i) {
       const int r = xr + 8 * i;
-      *reinterpret_cast<v4i*>(sx + r * OC + (((xc >> 3) ^ ((r & 3) << 2)) << 3)) = x[i];
+      *reinterpret_cast<v4i*>(sx + r * OC + (((xc >> 3) ^ ((r & 3) << 2)) << 3)) = fix8<VEC>(x[i], xcols, p.C < 8);
     }
     if (TYPE == MM_FP16) {
       for (int i = tid; i < OP * VW; i += 256) {

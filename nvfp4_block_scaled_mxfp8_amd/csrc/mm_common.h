@@ -58,6 +58,36 @@ struct Elem<MM_FP16> {
 
 __device__ __forceinline__ void mma32_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
+// ----------------------------------------------------------------------------- loads from any even address
+// Eight elements of a row from p, the first `valid` of which exist, zeros behind them, in two steps so
+// that many loads can be in flight: load8_raw issues one 16-byte load (the hardware takes any
+// alignment; a ragged end is read as the row's last eight elements) and shift8 moves a ragged end
+// down.  Rows of fewer than eight elements are read by element (load8_short, no shift).
+__device__ __forceinline__ v4i load8_raw(const uint16_t* p, int valid) {
+  v4i v{0, 0, 0, 0};
+  if (valid > 0) __builtin_memcpy(&v, p - max(8 - valid, 0), 16);
+  return v;
+}
+__device__ __forceinline__ v4i shift8(v4i v, int valid) {
+  uint64_t lo = (uint32_t)v.x | ((uint64_t)(uint32_t)v.y << 32), hi = (uint32_t)v.z | ((uint64_t)(uint32_t)v.w << 32);
+  const int s = 16 * min(max(8 - valid, 0), 8);
+  if (s >= 64) {
+    lo = s >= 128 ? 0 : hi >> (s - 64);
+    hi = 0;
+  } else if (s > 0) {
+    lo = (lo >> s) | (hi << (64 - s));
+    hi >>= s;
+  }
+  return v4i{(int)(uint32_t)lo, (int)(uint32_t)(lo >> 32), (int)(uint32_t)hi, (int)(uint32_t)(hi >> 32)};
+}
+__device__ __forceinline__ v4i load8_short(const uint16_t* p, int valid) {
+  uint32_t w[4] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < valid) w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+  return v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+}
+
 // ----------------------------------------------------------------------------- split sizes
 // Every wave walks m_splits by itself, 64 groups at a time (no table, no launch before the
 // product, no barrier).  Row counts are clamped like the split scan's: a negative count is 0 and

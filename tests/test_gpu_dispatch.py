@@ -125,6 +125,25 @@ def test_nan_in_unused_rows_reaches_nothing():
     assert torch.equal(y.cpu().float(), torch.tensor([1.0, 2.0, 1.0])[:, None].expand(3, 16))
 
 
+@pytest.mark.parametrize("H", [3, 9, 13, 17, 250])
+def test_odd_rows_count_every_element_once(H):
+    """Rows that are not whole 16-byte chunks, an infinity in the overlap of the last two loads: it
+    reaches its own column and the one product that holds it, exactly."""
+    T, k, E = 6, 2, 3
+    plan = g.dispatch_plan(torch.from_numpy(_experts(T, k, E, 9)).cuda(), E)
+    v = ints((T * k, H), torch.bfloat16, 1, 1, 3).cuda()
+    dy = ints((T, H), torch.bfloat16, 2, 1, 3).cuda()
+    dv, dp = g.combine_backward(dy, v, plan, torch.ones((T, k), device="cuda"))
+    r = plan.rows.long()
+    assert torch.equal(dp.double(), (dy.double()[:, None, :] * v.double()[r]).sum(2))
+    dyi = dy.clone()
+    dyi[4, max(H - 9, 0)] = float("inf")
+    dv2, dp2 = g.combine_backward(dyi, v, plan, torch.ones((T, k), device="cuda"))
+    rows = torch.arange(T) != 4
+    assert torch.equal(dp2[rows.cuda()], dp[rows.cuda()]) and bool((dp2[4] == float("inf")).all())
+    assert torch.equal(dv2[r[4]], dyi[4].expand(k, H))
+
+
 def test_autograd_against_formula_and_differences():
     T, k, E, H = 9, 3, 4, 24
     ids = _experts(T, k, E, 6, 0.1)
