@@ -48,14 +48,18 @@ __device__ __forceinline__ uint64_t sgpr64(uint64_t v) {
 // for every outstanding DMA before each LDS read; the kernel counts them itself.  The compiler may
 // have written the scalar operands by a vector instruction just before (a lane read), which a
 // vector-memory instruction must not read for five wait states: the move and the s_nop are those.
-template <bool STREAM>
 __device__ __forceinline__ void dma16(v4i rsrc, uint32_t voff, uint32_t soff, uint32_t m0) {
-  if constexpr (STREAM)
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
-                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"(m0) : "memory");
-  else
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"(m0) : "memory");
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               :: "v"(voff), "s"(rsrc), "s"(soff), "s"(m0) : "memory");
+}
+// The same, non-temporal where the tile's group has at most T rows (one row tile).  The comparison is
+// part of the asm: a truth value would come out of a vector register.
+template <int T>
+__device__ __forceinline__ void dma16_once(v4i rsrc, uint32_t voff, uint32_t soff, uint32_t m0, uint32_t rows) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_cmp_gt_u32 %4, %5\n\ts_nop 2\n\ts_cbranch_scc1 L_all_%=\n\t"
+               "buffer_load_dwordx4 %0, %1, %2 offen nt lds\n\ts_branch L_end_%=\n"
+               "L_all_%=:\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds\nL_end_%=:"
+               :: "v"(voff), "s"(rsrc), "s"(soff), "s"(m0), "s"(rows), "n"(T) : "memory", "scc");
 }
 template <int VM>
 __device__ __forceinline__ void wait_stage() {      // all LDS reads back, at most VM DMAs in flight
@@ -66,7 +70,7 @@ __device__ __forceinline__ void wait_stage() {      // all LDS reads back, at mo
 
 constexpr uint32_t kNoLane = 0x80000000u;            // past every range: the lane reads zeros
 
-// One operand's stream of units.  ONCE: read by one tile only (non-temporal loads).
+// One operand's stream of units.  ONCE: non-temporal loads where the tile's group has no other row tile.
 template <bool TR, int T, int NT, bool ONCE = false>
 struct Feed {
   static constexpr int kDma = T * 128 / (NT * 16);   // DMAs per unit and wave
@@ -79,6 +83,7 @@ struct Feed {
   uint32_t cols_bytes;          // TR: bytes from the tile's first column to the end of a row
   v4i rsrc;                     // the unit being issued
   uint32_t v;
+  uint32_t group_rows;
 
   __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int valid, int64_t kn, int tid) {
     base = sgpr64((uint64_t)(uintptr_t)p);
@@ -111,7 +116,9 @@ struct Feed {
   }
   // DMA number i of the unit (after next()).
   __device__ __forceinline__ void issue(int i, uint32_t slot, int wave) {
-    dma16<ONCE>(rsrc, v, (uint32_t)sgpr(i * step), (uint32_t)sgpr(slot + i * NT * 16 + wave * 1024));
+    const uint32_t so = (uint32_t)sgpr(i * step), m0 = (uint32_t)sgpr(slot + i * NT * 16 + wave * 1024);
+    if constexpr (ONCE) dma16_once<T>(rsrc, v, so, m0, group_rows);
+    else dma16(rsrc, v, so, m0);
   }
   __device__ __forceinline__ void issue_all(uint32_t slot, int wave) {
     next();
@@ -218,6 +225,7 @@ __global__ __launch_bounds__(256, 2) void gmm_ring_kernel(MmArgs p) {
   uint8_t* C = static_cast<uint8_t*>(p.c);
   int64_t crow0, kn, ldc = p.ldc;
   int arows, bcols, col0, ncols;
+  uint32_t group_rows = 0;
   constexpr uint32_t GR = 4;             // four row tiles to a column sweep
   if (LAYOUT == MM_WGRAD) {
     const uint32_t ntm = (p.n + T - 1) / T, ntn = (p.k + T - 1) / T, tpg = ntm * ntn;
@@ -258,6 +266,7 @@ __global__ __launch_bounds__(256, 2) void gmm_ring_kernel(MmArgs p) {
     arows = (int)(rt.m - tm);
     ncols = p.n;
     kn = rt.g < p.G ? p.k : 0;
+    group_rows = (uint32_t)sgpr((int)rt.m);
     crow0 = (int64_t)rt.row0 + tm;
     A += crow0 * p.lda;
     if (rt.g < p.G) B += (int64_t)rt.g * p.b_stride + (LAYOUT == MM_FPROP ? (int64_t)col0 * p.ldb : (int64_t)col0);
@@ -301,6 +310,7 @@ __global__ __launch_bounds__(256, 2) void gmm_ring_kernel(MmArgs p) {
       Feed<BT, T, NT, ONCE> fb;
       fa.init(A, p.lda, arows, kn, tid);
       fb.init(B, p.ldb, bcols, kn, tid);
+      fb.group_rows = group_rows;
       constexpr int P = Feed<AT, T, NT>::kDma;
       fa.issue_all(lds0 + 0 * SLOT, wave);
       fb.issue_all(lds0 + 1 * SLOT, wave);
@@ -928,14 +938,13 @@ int64_t grouped_matmul_part_floats(int layout, int G, int64_t M, int64_t n, int6
   return parts > 1 ? parts * (layout == MM_WGRAD ? G * n * k : M * n) : 0;
 }
 
-// Non-temporal loads of the weights: groups of so few rows that a weight meets one row tile, and
-// weights past twice the last-level cache, so that none is still there from the call before.
-// Measured (us, forward, plain / non-temporal): 128 x 4096 x 7168 with 64 rows 558 / 511, with 128
-// rows 869 / 783; 64 x 2816 x 2048 (738 MB) at 16 rows a group 133 / 120, at 32 149 / 145, at 64
-// 155 / 162, at 128 203 / 254; 8 x 4096 x 4096 (268 MB) at 4 rows 53 / 59.
-static bool weights_once(const MmArgs& p) {
-  return p.M <= 32 * (int64_t)p.G && 2.0 * std::min<int64_t>(p.G, p.M) * p.n * p.k > 512e6;
-}
+// Non-temporal loads of the weights of groups with one row tile, where the weights pass twice the
+// last-level cache, so that none is still there from the call before.  Measured (us, forward, plain /
+// non-temporal): 128 x 4096 x 7168 with 64 rows 556 / 512, with 128 rows 848 / 768; 64 x 2816 x 2048
+// (738 MB) at 16 rows a group 133 / 120, at 32 149 / 145, at 64 154 / 162 (dgrad 145 / 140), at 128
+// (most groups two tiles) 204 / 205, Zipf with 96 a group 187 / 176; 8 x 4096 x 4096 (268 MB) at 4
+// rows 53 / 59.
+static bool weights_once(const MmArgs& p) { return 2.0 * std::min<int64_t>(p.G, p.M) * p.n * p.k > 512e6; }
 
 template <int TYPE, int LAYOUT, int OUT, bool VEC>
 static hipError_t run_ring(const MmArgs& p, hipStream_t s) {

@@ -77,7 +77,7 @@ def test_products_against_64_bits(name, dt):
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))
-@pytest.mark.parametrize("name", ["ragged", "k_tail", "wide", "odd"])
+@pytest.mark.parametrize("name", ["ragged", "k_tail", "wide", "odd", "stream_k", "stream_w"])
 def test_strides_and_offsets(name, dt):
     """Views: rows inside wider tensors, starts that are not 16-byte aligned, weights with gaps, and
     transposed inputs (copied).  The same bits as the contiguous tensors where the kernel is the same."""
@@ -104,12 +104,11 @@ def test_strides_and_offsets(name, dt):
     assert torch.equal(g.grouped_matmul_forward(xt, v["w"], v["m"]), g.grouped_matmul_forward(v["x"], v["w"], v["m"]))
 
 
-@pytest.mark.parametrize("name", ["ragged", "wide"])
+@pytest.mark.parametrize("name", ["ragged", "wide", "stream_n", "stream_k"])
 def test_given_output_keeps_rows_behind(name):
     d, M, N, K = _case(name, torch.bfloat16)
     v = _up(d)
     _, used = spans(d["splits"], M)
-    assert used < M or name == "wide"
     y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
     dx = torch.full((M, K), 7.0, dtype=torch.bfloat16, device="cuda")
     g.grouped_matmul_forward(v["x"], v["w"], v["m"], out=y)
@@ -163,6 +162,36 @@ def test_nan_and_infinity_stay_in_their_rows(K):
     assert bool(dw[0, :, K - 1].isnan().all())
     if K > 1:
         assert torch.equal(dw[0, :, 1:K - 1], dw0[0, :, 1:K - 1])
+
+
+def test_nan_and_infinity_stay_in_their_rows_of_the_stream():
+    """The same for the 256 x 256 stream: rows, weights and gradients beside the ones that are not finite,
+    contraction and row tails inside a tile."""
+    splits, M, N, K = [700, 0, 1200, 49], 2048, 8200, 72
+    d = {"x": randn((M, K), torch.bfloat16, 1), "w": randn((4, N, K), torch.bfloat16, 2), "splits": splits}
+    v = _up(d)
+    y0 = g.grouped_matmul_forward(v["x"], v["w"], v["m"])
+    x, w = v["x"].clone(), v["w"].clone()
+    bad = [0, 255, 699, 700, 1899, 1948]
+    x[bad, K - 1] = float("nan")
+    x[1949:] = float("inf")
+    w[1] = float("nan")
+    y = g.grouped_matmul_forward(x, w, v["m"])
+    rows = torch.ones(M, dtype=torch.bool)
+    rows[bad] = False
+    assert torch.equal(y[rows], y0[rows]) and bool(y[bad].isnan().all())
+    splits, M, N, K = [0, 65, 1, 300, 64, 0, 17, 128, 5], 600, 1032, 1544
+    m = torch.tensor(splits, dtype=torch.int32, device="cuda")
+    x, dy = randn((M, K), torch.bfloat16, 3).cuda(), randn((M, N), torch.bfloat16, 4).cuda()
+    dw0 = g.grouped_matmul_wgrad(dy, x, m)
+    x[580:] = float("nan")
+    dy[580:] = float("inf")
+    x[66, 5] = float("nan")                              # the first row of group 3
+    dw = g.grouped_matmul_wgrad(dy, x, m)
+    others = [0, 1, 2, 4, 5, 6, 7, 8]
+    assert torch.equal(dw[others], dw0[others])
+    cols = torch.arange(K) != 5
+    assert torch.equal(dw[3][:, cols], dw0[3][:, cols]) and bool(dw[3][:, 5].isnan().all())
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))
