@@ -194,8 +194,9 @@ static hipError_t run_shrink(const LoraShrink& p, hipStream_t s) {
   hipLaunchKernelGGL((lora_shrink_kernel<TYPE, VEC, RB, RT, NW>), dim3((uint32_t)tiles), dim3(64 * NW), 0, s, p);
   return hipGetLastError();
 }
-// 32 positions a tile where those fill the device, with as many waves as four a SIMD take; 16
-// positions and 16 waves below.  (Above 64 ranks a wave's registers allow half as many.)
+// 32 positions a tile where those fill the device, 16 waves while one tile a CU is all there is, else 8;
+// 16 positions below.  (Above 64 ranks a wave's registers allow 8.)  Measured (us, whole forward): 6001
+// rows of 7168, rank 64 (194 tiles of 32): 32 positions 100.6 with 16 waves, 102.0 with 8; 16 positions 127.8.
 template <int TYPE, bool VEC, int RT>
 static hipError_t shrink_rank(const LoraShrink& p, hipStream_t s) {
   constexpr int NW = RT > 4 ? 8 : 16;
@@ -336,10 +337,13 @@ static hipError_t run_expand_rows(const LoraExpand& p, hipStream_t s) {
 }
 template <int TYPE, bool VEC, bool VECW>
 static hipError_t run_expand(const LoraExpand& p, hipStream_t s) {
-  // a tile of 16 positions while those leave the device unfilled, else 64: W is read once per tile
+  // W is read once per tile: 128 positions where those give three workgroups a CU, 16 where those give
+  // fewer than eight, else 64.  Measured (us, forward and gradients / forward): 16384 rows of 4096, rank
+  // 16, with 32, 64, 128 positions 286 / 289 / 280; 6001 rows of 4096, rank 64, 108 / 101 / 100.
   const int64_t cols = (p.C + 255) / 256;
   if (tiles_bound(p.rows.M, p.rows.L + 1, 16) * cols < 2048) return run_expand_rows<TYPE, VEC, VECW, 1>(p, s);
-  return run_expand_rows<TYPE, VEC, VECW, 4>(p, s);
+  if (tiles_bound(p.rows.M, p.rows.L + 1, 128) * cols < 768) return run_expand_rows<TYPE, VEC, VECW, 4>(p, s);
+  return run_expand_rows<TYPE, VEC, VECW, 8>(p, s);
 }
 template <int TYPE>
 static hipError_t expand_vec(const LoraExpand& p, hipStream_t s) {

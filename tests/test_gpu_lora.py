@@ -23,6 +23,8 @@ CASES = {
     "rank100": (65, 136, 72, 100, 2, 0.5),
     "none": (20, 64, 64, 16, 2, 1.0),
     "many": (500, 128, 128, 8, 200, 0.0),
+    "tiles64": (1100, 64, 4100, 16, 3, 0.1),          # expand tiles of 64 positions, shrink of 16
+    "tiles128": (5000, 64, 6000, 24, 2, 0.1),        # of 128 and 32
     "long": (3000, 256, 520, 16, 3, 0.05),
     "long33": (2100, 200, 264, 33, 1, 0.0),
     "no_rows": (0, 64, 64, 8, 2, 0.0),
