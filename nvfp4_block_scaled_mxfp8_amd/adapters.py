@@ -14,7 +14,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _SIGS, _check, _dev_ptr, lib
-from .matmul import _DTYPES, _check_rows_out, _dtype16, _gs, _ld, _packer, _row_major, _run, _same
+from .matmul import _DTYPES, _check_rows_out, _dtype16, _gs, _ld, _no_overlap, _packer, _row_major, _run, _same, once_differentiable
 
 
 class LoraWeights(ctypes.Structure):
@@ -119,6 +119,10 @@ def lora_forward(base, x, a, b, ids, scales=None, out=None):
         if tuple(base.shape) != (M, N):
             raise ValueError(f"base: shape {(M, N)} expected, got {tuple(base.shape)}")
         base = _row_major(base)
+    if out is not None:
+        _no_overlap(out, "out", x=x, a=a, b=b)
+        if base is not None and (out.data_ptr() != base.data_ptr() or _ld(out) != _ld(base)):
+            _no_overlap(out, "out", base=base)
     _dev_ptr(x, "x")
     x, a, b, ids = _row_major(x), _row_major(a), _row_major(b), ids.contiguous()
     scales = scales.contiguous() if scales is not None else None
@@ -174,12 +178,13 @@ class LoraFunction(torch.autograd.Function):
     @staticmethod
     def forward(fctx, base, x, a, b, ids, scales):
         y, fctx.lora = lora_forward(base, x, a, b, ids, scales)
-        fctx.save_for_backward(x, a, b)
+        fctx.save_for_backward(x, a, b, scales)
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(fctx, dy):
-        x, a, b = fctx.saved_tensors
+        x, a, b, _ = fctx.saved_tensors
         need = fctx.needs_input_grad
         dyt = dy.to(x.dtype)
         g = {"dx": None, "da": None, "db": None}

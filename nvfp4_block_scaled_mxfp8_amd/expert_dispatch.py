@@ -14,7 +14,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _SIGS, _check, _dev_ptr, lib
-from .matmul import _DTYPES, _check_rows_out, _dtype16, _ld, _packer, _row_major, _run
+from .matmul import _DTYPES, _check_rows_out, _dtype16, _ld, _no_overlap, _packer, _row_major, _run, once_differentiable
 
 
 class MoveArgs(ctypes.Structure):
@@ -118,6 +118,7 @@ def _to_rows(src, plan, probs, out):
     shape = (plan.rows.numel(), src.shape[1])
     if out is not None:
         _check_rows_out(out, shape, src, "out")
+        _no_overlap(out, "out", input=src)
     dst = out if out is not None else torch.empty(shape, dtype=src.dtype, device=src.device)
     return _move("gmlp_dispatch", plan, src, dst, probs, zero_rest=out is None)
 
@@ -126,6 +127,7 @@ def _to_tokens(src, plan, probs, out):
     shape = (plan.tokens, src.shape[1])
     if out is not None:
         _check_rows_out(out, shape, src, "out")
+        _no_overlap(out, "out", input=src)
     dst = out if out is not None else torch.empty(shape, dtype=src.dtype, device=src.device)
     return _move("gmlp_combine", plan, src, dst, probs)
 
@@ -167,27 +169,30 @@ def combine_backward(dy, v, plan, probs=None, need_dv=True, need_dprobs=True):
 class DispatchFunction(torch.autograd.Function):
     @staticmethod
     def forward(fctx, x, plan):
-        fctx.plan, fctx.dtype = plan, x.dtype
-        return dispatch_forward(x, plan)
+        fctx.dtype = x.dtype
+        xg = dispatch_forward(x, plan)
+        fctx.save_for_backward(plan.m_splits, plan.rows)
+        return xg
 
     @staticmethod
+    @once_differentiable
     def backward(fctx, dxg):
-        return dispatch_backward(dxg.to(fctx.dtype), fctx.plan), None
+        return dispatch_backward(dxg.to(fctx.dtype), DispatchPlan(*fctx.saved_tensors)), None
 
 
 class CombineFunction(torch.autograd.Function):
     @staticmethod
     def forward(fctx, v, probs, plan):
-        fctx.plan, fctx.has_probs = plan, probs is not None
-        fctx.save_for_backward(*((v, probs) if probs is not None else (v,)))
-        return combine_forward(v, plan, probs)
+        y = combine_forward(v, plan, probs)
+        fctx.save_for_backward(plan.m_splits, plan.rows, v, probs)
+        return y
 
     @staticmethod
+    @once_differentiable
     def backward(fctx, dy):
-        v = fctx.saved_tensors[0]
-        probs = fctx.saved_tensors[1] if fctx.has_probs else None
+        m_splits, rows, v, probs = fctx.saved_tensors
         need = fctx.needs_input_grad
-        dv, dp = combine_backward(dy.to(v.dtype), v, fctx.plan, probs, need[0], need[1])
+        dv, dp = combine_backward(dy.to(v.dtype), v, DispatchPlan(m_splits, rows), probs, need[0], need[1])
         return dv, dp, None
 
 

@@ -13,6 +13,7 @@ import functools
 import struct
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (_SIGS, _check, _check_out, _dev_ptr, _splits, GEMM_DGRAD, GEMM_FPROP, GEMM_WGRAD, OUT_FP32,
                OUT_FP32_ACCUMULATE, lib)
@@ -102,6 +103,33 @@ def _gs(t):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1] * _ld(t)
 
 
+def _extent(t):
+    """(first byte, byte behind the last) of a tensor's elements."""
+    n = sum((t.shape[d] - 1) * t.stride(d) for d in range(t.dim())) + 1
+    return t.data_ptr(), t.data_ptr() + n * t.element_size()
+
+
+def _no_overlap(out, name, **inputs):
+    """An output must not share elements with what the call reads while it is written (columns of one
+    wide tensor beside each other are fine)."""
+    if out.numel() == 0:
+        return
+    o0, o1 = _extent(out)
+    for k, t in inputs.items():
+        if t is None or t.numel() == 0:
+            continue
+        i0, i1 = _extent(t)
+        if o0 >= i1 or i0 >= o1:
+            continue
+        if out.dim() == 2 == t.dim() and out.element_size() == t.element_size() and _ld(out) == _ld(t):
+            es, ld = t.element_size(), _ld(t)
+            if (o0 - i0) % es == 0:
+                d = (o0 - i0) // es % ld
+                if d >= t.shape[1] and d + out.shape[1] <= ld:
+                    continue
+        raise ValueError(f"{name}: overlaps {k}")
+
+
 def _check_rows_out(t, shape, like, name):
     """A given output: like's dtype and device, the shape, last dimension contiguous, rows apart."""
     if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != like.dtype or t.device != like.device:
@@ -149,6 +177,7 @@ def grouped_matmul_forward(x, w, m_splits, out=None, ws=None):
     m_splits = _splits(m_splits, G)
     if out is not None:
         _check_rows_out(out, (x.shape[0], N), x, "out")
+        _no_overlap(out, "out", x=x, w=w)
     y = out if out is not None else torch.empty((x.shape[0], N), dtype=x.dtype, device=x.device)
     return _call(GEMM_FPROP, _row_major(x), _row_major(w), y, m_splits, x.shape[0], N, K, OUT_SAME, out is None, ws)
 
@@ -165,6 +194,7 @@ def grouped_matmul_dgrad(dy, w, m_splits, out=None, ws=None):
     m_splits = _splits(m_splits, G)
     if out is not None:
         _check_rows_out(out, (dy.shape[0], K), dy, "out")
+        _no_overlap(out, "out", dy=dy, w=w)
     dx = out if out is not None else torch.empty((dy.shape[0], K), dtype=dy.dtype, device=dy.device)
     return _call(GEMM_DGRAD, _row_major(dy), _row_major(w), dx, m_splits, dy.shape[0], K, N, OUT_SAME, out is None, ws)
 
@@ -187,6 +217,7 @@ def grouped_matmul_wgrad(dy, x, m_splits, out_dtype=OUT_SAME, out=None, ws=None)
         _check_out(out, shape, dt, "out")
         if out.device != dy.device:
             raise ValueError(f"out: on {out.device}, the other tensors are on {dy.device}")
+        _no_overlap(out, "out", dy=dy, x=x)
     dw = out if out is not None else torch.empty(shape, dtype=dt, device=dy.device)
     return _call(GEMM_WGRAD, _row_major(dy), _row_major(x), dw, m_splits, dy.shape[0], dy.shape[1], x.shape[1], out_dtype,
                  False, ws)
@@ -203,6 +234,7 @@ class GroupedMatmulFunction(torch.autograd.Function):
         return grouped_matmul_forward(x, w, m_splits)
 
     @staticmethod
+    @once_differentiable
     def backward(fctx, dy):
         x, w, m_splits = fctx.saved_tensors
         need = fctx.needs_input_grad

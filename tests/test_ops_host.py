@@ -40,6 +40,35 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         g.grouped_matmul(x, w, m, accumulate_main_grad=True)
 
 
+def test_outputs_that_overlap_inputs_are_refused():
+    """Shared elements are an error; columns of one wide tensor beside each other are not."""
+    m = torch.tensor([2, 2], dtype=torch.int32)
+    x, w = _t(4, 16), _t(2, 16, 16)
+    with pytest.raises(ValueError, match="overlaps x"):
+        g.grouped_matmul_forward(x, w, m, out=x)
+    with pytest.raises(ValueError, match="overlaps dy"):
+        g.grouped_matmul_dgrad(x, w, m, out=x)
+    buf = _t(5, 16)
+    with pytest.raises(ValueError, match="overlaps x"):
+        g.grouped_matmul_forward(buf[:4], w, m, out=buf[1:])
+    wide = _t(4, 40)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        g.grouped_matmul_forward(wide[:, :16], w, m, out=wide[:, 16:32])
+    with pytest.raises(ValueError, match="overlaps x"):
+        g.grouped_matmul_forward(wide[:, :16], w, m, out=wide[:, 8:24])
+    plan = g.DispatchPlan(m, torch.zeros((4, 1), dtype=torch.int32))
+    with pytest.raises(ValueError, match="overlaps input"):
+        g.dispatch_forward(x, plan, out=x)
+    a, b = _t(2, 4, 16), _t(2, 16, 4)
+    ids = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="overlaps x"):
+        g.lora_forward(_t(4, 16), x, a, b, ids, out=x)
+    with pytest.raises(ValueError, match="overlaps base"):
+        g.lora_forward(buf[:4], x, a, b, ids, out=buf[1:])
+    with pytest.raises(ValueError, match="GPU tensor"):
+        g.lora_forward(buf[:4], x, a, b, ids, out=buf[:4])
+
+
 def _mm(**kw):
     a = g.GroupedMatmulArgs()
     vals = dict(layout=0, dtype=0, out_dtype=0, zero_rest=0, a=256, lda=16, b=256, ldb=16, b_stride=128, c=256, ldc=8,
