@@ -937,13 +937,13 @@ static int cu_count() {
 }
 
 // Parts of the contraction: with fewer tiles than CUs and eight stages or more, as many as fill the
-// device twice, none shorter than four stages.
+// device twice, none shorter than four stages (one part where there is no tile at all).
 int grouped_matmul_parts(int layout, int G, int64_t M, int64_t n, int64_t k) {
   const int64_t tn = (n + 127) / 128, tk = (k + 127) / 128;
   const int64_t tiles = layout == MM_WGRAD ? G * tn * tk : row_tiles_even(M, G, 128) * tn;
   const int64_t stages = ((layout == MM_WGRAD ? M / std::min<int64_t>(G, std::max<int64_t>(M, 1)) : k) + 63) / 64;
-  if (tiles >= 256 || stages < 8) return 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(tiles, 1), stages / 4, 16}));
+  if (tiles == 0 || tiles >= 256 || stages < 8) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, stages / 4, 16}));
 }
 int64_t grouped_matmul_part_floats(int layout, int G, int64_t M, int64_t n, int64_t k) {
   const int parts = grouped_matmul_parts(layout, G, M, n, k);

@@ -21,6 +21,7 @@ CASES = {
     "odd_n": ([128, 65], 193, 129, 128),
     "empty": ([0, 0, 0], 5, 64, 64),
     "no_rows": ([0, 0], 0, 64, 64),
+    "no_rows_long": ([0, 0], 0, 1000, 1024),      # a contraction that would be cut into parts
     "tall": ([1000], 1000, 8, 2048),
     # the 256 x 256 stream: column tiles enough, groups of several row tiles and a ragged one, rows behind
     # the last group; as forward, as dgrad (and the other as a contraction cut into parts)
