@@ -44,6 +44,13 @@ class DispatchPlan:
     m_splits: torch.Tensor
     rows: torch.Tensor
 
+    def __post_init__(self):
+        for t, name, dim in ((self.m_splits, "m_splits", 1), (self.rows, "rows", 2)):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+                raise TypeError(f"{name}: a contiguous int32 tensor of {dim} dimensions is required")
+        if self.m_splits.device != self.rows.device or self.m_splits.numel() < 1 or self.rows.shape[1] < 1:
+            raise ValueError("plan: m_splits [E] and rows [T, k] on one device are required")
+
     @property
     def tokens(self):
         return self.rows.shape[0]

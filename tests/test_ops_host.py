@@ -40,6 +40,18 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         g.grouped_matmul(x, w, m, accumulate_main_grad=True)
 
 
+def test_a_plan_of_other_tensors_is_refused():
+    m, rows = torch.zeros(4, dtype=torch.int32), torch.zeros((8, 2), dtype=torch.int32)
+    assert g.DispatchPlan(m, rows).tokens == 8
+    for bad in ((m.long(), rows), (m, rows.long()), (m, rows[:, :1]), (m, rows.view(-1)), (m.view(2, 2), rows),
+                (None, rows)):
+        with pytest.raises(TypeError, match="int32"):
+            g.DispatchPlan(*bad)
+    for bad in ((m[:0], rows), (m, torch.zeros((8, 0), dtype=torch.int32))):
+        with pytest.raises(ValueError, match="plan"):
+            g.DispatchPlan(*bad)
+
+
 def test_outputs_that_overlap_inputs_are_refused():
     """Shared elements are an error; columns of one wide tensor beside each other are not."""
     m = torch.tensor([2, 2], dtype=torch.int32)
