@@ -14,9 +14,10 @@ namespace gmlp {
 // slots at a time.  Within a wave the lanes with the same id find each other by one ballot per bit
 // of the id; a wave's running position per group sits in LDS.  So positions depend on nothing but
 // the ids: the sort is stable and every run gives the same order.
-//   counting pass (several blocks): the chunk's slots per group -> ws[block][G]
+//   counting pass (many slots): the chunk's slots per group -> ws[block][G]
 //   placing pass: a group's first position (the slots of lower groups, and of this group in earlier
-//   blocks and waves), then one walk that places every slot.
+//   blocks and waves), then one walk that places every slot.  Without a counting pass (no ws) every
+//   block counts all slots by itself.
 constexpr int OT = 1024, OW = OT / 64;
 
 __device__ __forceinline__ uint64_t same_id_lanes(int id, int bits, bool in) {
@@ -42,6 +43,33 @@ __global__ __launch_bounds__(OT) void order_kernel(const int32_t* __restrict__ i
   const int64_t lo = (int64_t)blockIdx.x * chunk, hi = min(lo + chunk, n);
   const int64_t wchunk = chunk / OW;               // chunk is a multiple of OT
   const int64_t wlo = lo + wave * wchunk, whi = min(wlo + wchunk, hi);
+  int32_t before = 0, all = 0;                     // of group tid: slots in earlier blocks, in all
+  if (PLACE && nblocks > 1 && !ws) {
+    int32_t* rep = &at[0][0];                      // sixteen counters per group, one per lane % 16
+    auto count_ids = [&](int64_t from, int64_t to) {
+      for (int64_t i = from + tid; i < to; i += 4 * OT) {
+        int id[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          id[u] = i + u * OT < to ? ids[i + u * OT] : -1;
+          if (rest && i + u * OT < to && (uint32_t)id[u] >= (uint32_t)G) id[u] = G - 1;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if ((uint32_t)id[u] < (uint32_t)G) atomicAdd(&rep[id[u] * OW + (lane & (OW - 1))], 1);
+      }
+      __syncthreads();
+      int32_t sum = 0;
+      if (tid < G)
+        for (int w = 0; w < OW; ++w) sum += rep[tid * OW + w];
+      __syncthreads();
+      return sum;
+    };
+    for (int i = tid; i < G * OW; i += OT) rep[i] = 0;
+    __syncthreads();
+    before = count_ids(0, lo);
+    all = count_ids(lo, n);                        // the counters run on
+  }
   for (int g = lane; g < G; g += 64) at[wave][g] = 0;
   // LDS within a wave is in order; other waves read at[][] only after the barrier
   for (int64_t i = wlo; i < whi; i += 64) {
@@ -51,7 +79,7 @@ __global__ __launch_bounds__(OT) void order_kernel(const int32_t* __restrict__ i
   }
   __syncthreads();
   // the block's slots of group tid (G <= OT), as a running sum over its waves
-  int32_t mine = 0, before = 0, all = 0;
+  int32_t mine = 0;
   if (tid < G) {
     for (int w = 0; w < OW; ++w) {
       const int32_t v = at[w][tid];
@@ -65,7 +93,7 @@ __global__ __launch_bounds__(OT) void order_kernel(const int32_t* __restrict__ i
     }
   }
   if (!PLACE) return;
-  if (nblocks > 1) {                               // all threads add up the blocks' counts
+  if (nblocks > 1 && ws) {                         // all threads add up the blocks' counts
     __syncthreads();
     const int g = tid & ((1 << bits) - 1), per = OT >> bits;
     if (g < G) {
@@ -81,7 +109,7 @@ __global__ __launch_bounds__(OT) void order_kernel(const int32_t* __restrict__ i
     }
     __syncthreads();
   }
-  if (tid < G) {
+  if (tid < G && (nblocks == 1 || ws)) {
     before = nblocks > 1 ? s_before[tid] : 0;
     all = nblocks > 1 ? s_all[tid] : mine;
   }
@@ -126,15 +154,21 @@ static int64_t order_chunk(int64_t n) {
   const int64_t per = (n + kOrderMaxBlocks - 1) / kOrderMaxBlocks;
   return std::max<int64_t>((per + OT - 1) / OT, 1) * OT;
 }
-int order_blocks(int64_t n) { return (int)std::max<int64_t>((n + order_chunk(n) - 1) / order_chunk(n), 1); }
+static int order_grid(int64_t n) { return (int)std::max<int64_t>((n + order_chunk(n) - 1) / order_chunk(n), 1); }
+// Up to here every block counts all slots by itself, past it a pass of its own does.  Measured (us in a
+// graph, own pass / by itself): 64 groups: 2048 slots 6.0 / 4.6, 6144 6.2 / 5.2, 16384 6.3 / 6.0, 24576
+// 6.5 / 6.8, 65536 6.5 / 10.7; 1024 groups: 2048 slots 8.5 / 7.5, 16384 10.2 / 8.9, 65536 14.5 / 13.6.
+constexpr int64_t kOrderAlone = 16384;
+int order_blocks(int64_t n) { return n > kOrderAlone ? order_grid(n) : 1; }
 
 hipError_t launch_group_order(const int32_t* ids, int64_t n, int G, bool rest, int32_t* count, int32_t* rows,
                               int32_t* order, int32_t* ws, hipStream_t s) {
-  const int nb = order_blocks(n);
+  const int nb = order_grid(n);
   const int64_t chunk = order_chunk(n);
   int bits = 0;
   while ((1 << bits) < G) ++bits;
-  if (nb > 1)
+  if (order_blocks(n) == 1) ws = nullptr;
+  if (ws)
     hipLaunchKernelGGL(order_kernel<false>, dim3(nb), dim3(OT), 0, s, ids, n, chunk, G, bits, nb, rest, ws, count, rows, order);
   hipLaunchKernelGGL(order_kernel<true>, dim3(nb), dim3(OT), 0, s, ids, n, chunk, G, bits, nb, rest, ws, count, rows, order);
   return hipGetLastError();

@@ -30,7 +30,8 @@ def _order(ids, E):
 
 @pytest.mark.parametrize("T,k,E,bad", [(1, 1, 1, 0), (8, 8, 128, 0), (3, 6, 5, 0.3), (64, 1, 64, 0), (1024, 1, 7, 0.1),
                                        (1025, 1, 1024, 0), (777, 3, 1000, 0.2), (8192, 8, 128, 0), (40000, 8, 3, 0.01),
-                                       (5, 2, 4, 1.0), (0, 4, 9, 0)])
+                                       (5, 2, 4, 1.0), (0, 4, 9, 0), (16384, 1, 300, 0.1), (16385, 1, 300, 0.1),
+                                       (2049, 6, 1024, 0.01), (1500, 8, 1, 0.5)])
 def test_plan_is_the_stable_order(T, k, E, bad):
     print(f"plan T={T} k={k} E={E} bad={bad}", flush=True)
     ids = _experts(T, k, E, 1, bad)
