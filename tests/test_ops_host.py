@@ -234,7 +234,7 @@ def _lf(**kw):
     (dict(b=None), 1, "null"), (dict(x=257), 1, "aligned"), (dict(scales=258), 1, "aligned"), (dict(lda=15), 1, "strides"),
     (dict(ldb=3), 1, "strides"), (dict(a_stride=63), 1, "overlap"), (dict(ldx=15), 1, "strides"), (dict(ldy=7), 1, "strides"),
     (dict(ldbase=16), 1, "two row strides"), (dict(ctx=None), 3, "ctx"), (dict(ctx_bytes=16), 3, "ctx"), (dict(ctx=264), 3, "ctx"),
-    (dict(M=5000, ws=None), 3, "workspace"), (dict(M=0, x=None, y=None, ids=None, ctx=None), 0, ""),
+    (dict(M=20000, ctx_bytes=1 << 30, ws=None), 3, "workspace"), (dict(M=0, x=None, y=None, ids=None, ctx=None), 0, ""),
 ])
 def test_lora_abi_refusals(kw, status, why):
     assert _lf(**kw) == status and why in g.last_error(), g.last_error()
