@@ -845,7 +845,8 @@ __global__ __launch_bounds__(512, 2) void gmm_stream_kernel(StreamArgs args) {
     for (int n = 0; n < NR; ++n) read_one(0, n, a[0], b[0]);
     for (int s = 0; s + 1 < cur.nst; ++s) stage(Yes{}, s);
     stage(No{}, cur.nst - 1);
-    mma32_settle();
+    mma32_settle(acc);
+    MM_FENCE();
     // acc[i][j][e]: row 32 i + lane % 32, column 32 j + 8 (e / 4) + 4 (lane / 32) + e % 4 of the wave's
     // 128 x 64; staged by 32 rows of 128 bytes in the wave's 4 KB of the slot B left
     const uint32_t reg = sb + wave * 4096;

@@ -56,7 +56,13 @@ struct Elem<MM_FP16> {
   }
 };
 
-__device__ __forceinline__ void mma32_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+// The accumulators pass through the asm, so that no use of them can be moved above its 32 wait states (a
+// 32x32x16 product takes 16 passes).
+__device__ __forceinline__ void mma32_settle(v16f (&c)[4][2]) {
+  asm volatile("s_nop 15\n\ts_nop 15 ; settled %0 %1 %2 %3 %4 %5 %6 %7"
+               : "+v"(c[0][0]), "+v"(c[0][1]), "+v"(c[1][0]), "+v"(c[1][1]), "+v"(c[2][0]), "+v"(c[2][1]), "+v"(c[3][0]),
+                 "+v"(c[3][1]) :: "memory");
+}
 
 // ----------------------------------------------------------------------------- loads from any even address
 // Eight elements of a row from p, the first `valid` of which exist, zeros behind them, in two steps so
