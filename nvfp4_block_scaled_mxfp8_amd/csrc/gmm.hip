@@ -54,6 +54,7 @@ __device__ __forceinline__ uint64_t sgpr64(uint64_t v) {
 // for every outstanding DMA before each LDS read; the kernel counts them itself.  The compiler may
 // have written the scalar operands by a vector instruction just before (a lane read), which a
 // vector-memory instruction must not read for five wait states: the move and the s_nop are those.
+// m0 is reserved, so the compiler keeps nothing in it; no code of its own here may use it (none does).
 __device__ __forceinline__ void dma16(v4i rsrc, uint32_t voff, uint32_t soff, uint32_t m0) {
   asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                :: "v"(voff), "s"(rsrc), "s"(soff), "s"(m0) : "memory");

@@ -1,7 +1,10 @@
-"""The persistent grouped product multiplies in inline asm, so the compiler inserts no wait states
-between a matrix product and the first use of its accumulators: the kernel settles them itself.  Read
-off the assembly built from gmm.hip (CPU only, no GPU): in every such kernel the settle names all the
-accumulators, and no other instruction touches one between its product and the settle."""
+"""What the grouped products' inline asm leaves to its kernels, read off the assembly built from
+gmm.hip (CPU only, no GPU).  The persistent kernel multiplies in asm, so the compiler inserts no wait
+states between a matrix product and the first use of its accumulators: in every such kernel the settle
+names all the accumulators, and no other instruction touches one between its product and the settle.
+The DMAs set m0, a register that a clobber list cannot name (it is reserved: the compiler keeps no
+value in it, and sets it right before an instruction of its own that reads it): no code outside the asm
+uses it at all."""
 import os
 import re
 import subprocess
@@ -12,15 +15,21 @@ from nvfp4_block_scaled_mxfp8_amd.build import CSRC, HIPCC_FLAGS, hipcc
 
 
 @pytest.fixture(scope="module")
-def kernels(tmp_path_factory):
-    """{kernel name: its lines} of the stream kernels."""
+def assembly(tmp_path_factory):
+    """The lines of gmm.hip's device code."""
     out = str(tmp_path_factory.mktemp("asm") / "gmm.s")
     flags = [f for f in HIPCC_FLAGS if f not in ("-fPIC", "-shared")]
     r = subprocess.run([hipcc()] + flags + ["--cuda-device-only", "-S", os.path.join(CSRC, "gmm.hip"), "-o", out],
                        capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stderr[-2000:]
+    return open(out).read().splitlines(keepends=True)
+
+
+@pytest.fixture(scope="module")
+def kernels(assembly):
+    """{kernel name: its lines} of the stream kernels."""
     found, name = {}, None
-    for line in open(out):
+    for line in assembly:
         m = re.match(r"(_Z\S*gmm_stream_kernel\S*):", line)
         if m:
             name = m.group(1)
@@ -92,3 +101,16 @@ def test_accumulators_are_settled_before_they_are_read(kernels):
                 if not hot <= before[t]:
                     before[t] |= hot
                     todo.add(t)
+
+
+def test_no_other_code_uses_m0(assembly):
+    in_asm, set_by_asm = False, 0
+    for line in assembly:
+        if "#ASMSTART" in line or "#ASMEND" in line:
+            in_asm = "#ASMSTART" in line
+            continue
+        code = line.split(";")[0].strip()
+        if re.search(r"\bm0\b", code) and not code.startswith("."):
+            assert in_asm and code.startswith("s_mov_b32 m0,"), code
+            set_by_asm += 1
+    assert set_by_asm > 100
