@@ -14,7 +14,8 @@ from dataclasses import dataclass
 import torch
 
 from . import _SIGS, _check, _dev_ptr, lib
-from .matmul import _DTYPES, _check_rows_out, _dtype16, _gs, _ld, _no_overlap, _packer, _row_major, _run, _same, once_differentiable
+from .matmul import (_DTYPES, _check_rows_out, _dtype16, _gs, _ld, _no_overlap, _packer, _row_major, _run, _same, _written,
+                     once_differentiable)
 
 
 class LoraWeights(ctypes.Structure):
@@ -135,6 +136,8 @@ def lora_forward(base, x, a, b, ids, scales=None, out=None):
     args = _pack_fwd(_DTYPES[x.dtype], R, L, M, K, N, _ptr(base), _ld(base) if base is not None else 0, x.data_ptr(), _ld(x),
                      *_weights(a, b, scales), ids.data_ptr(), y.data_ptr(), _ld(y), p, ctx_bytes, p + at, ws_bytes)
     _run(lib().gmlp_lora_forward, args, dev)
+    if out is not None:
+        _written(out)
     return y, LoraContext(buf, M, K, N, R, L, x.dtype, scales)
 
 

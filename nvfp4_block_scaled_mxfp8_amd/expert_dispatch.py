@@ -14,7 +14,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _SIGS, _check, _dev_ptr, lib
-from .matmul import _DTYPES, _check_rows_out, _dtype16, _ld, _no_overlap, _packer, _row_major, _run, once_differentiable
+from .matmul import _DTYPES, _check_rows_out, _dtype16, _ld, _no_overlap, _packer, _row_major, _run, _written, once_differentiable
 
 
 class MoveArgs(ctypes.Structure):
@@ -118,7 +118,6 @@ def _move(fn, plan, src, dst, probs=None, zero_rest=False, src2=None, dprobs=Non
                       _ld(src2) if src2 is not None else 0, _ptr(dst), _ld(dst) if dst is not None else 0, T, src.shape[1],
                       k, plan.m_splits.numel(), plan.rows.data_ptr(), plan.m_splits.data_ptr(), _ptr(probs), _ptr(dprobs))
     _run(getattr(lib(), fn), args, src.device)
-    return dst
 
 
 def _to_rows(src, plan, probs, out):
@@ -127,7 +126,8 @@ def _to_rows(src, plan, probs, out):
         _check_rows_out(out, shape, src, "out")
         _no_overlap(out, "out", input=src)
     dst = out if out is not None else torch.empty(shape, dtype=src.dtype, device=src.device)
-    return _move("gmlp_dispatch", plan, src, dst, probs, zero_rest=out is None)
+    _move("gmlp_dispatch", plan, src, dst, probs, zero_rest=out is None)
+    return dst if out is None else _written(out)
 
 
 def _to_tokens(src, plan, probs, out):
@@ -136,7 +136,8 @@ def _to_tokens(src, plan, probs, out):
         _check_rows_out(out, shape, src, "out")
         _no_overlap(out, "out", input=src)
     dst = out if out is not None else torch.empty(shape, dtype=src.dtype, device=src.device)
-    return _move("gmlp_combine", plan, src, dst, probs)
+    _move("gmlp_combine", plan, src, dst, probs)
+    return dst if out is None else _written(out)
 
 
 def dispatch_forward(x, plan, out=None):

@@ -138,6 +138,13 @@ def _check_rows_out(t, shape, like, name):
         raise ValueError(f"{name}: the last dimension must be contiguous and rows must not overlap")
 
 
+def _written(t):
+    """A tensor of the caller's was written by its address: its version is raised, as an in-place torch
+    operation would, so that the backward of a node that saved it raises.  Returns t."""
+    torch.autograd.graph.increment_version(t)
+    return t
+
+
 @functools.lru_cache(maxsize=4096)
 def grouped_matmul_ws_bytes(layout, G, M, n, k):
     v = ctypes.c_size_t(0)
@@ -161,7 +168,6 @@ def _call(layout, a, b, c, m_splits, M, n, k, out_dtype, zero_rest, ws):
                     0 if wgrad else _gs(b), c.data_ptr(), _ld(c), _gs(c) if wgrad else 0, m_splits.data_ptr(), G, M, n, k,
                     ws.data_ptr(), ws.numel() * ws.element_size())
     _run(lib().gmlp_grouped_matmul, args, dev)
-    return c
 
 
 def grouped_matmul_forward(x, w, m_splits, out=None, ws=None):
@@ -179,7 +185,8 @@ def grouped_matmul_forward(x, w, m_splits, out=None, ws=None):
         _check_rows_out(out, (x.shape[0], N), x, "out")
         _no_overlap(out, "out", x=x, w=w)
     y = out if out is not None else torch.empty((x.shape[0], N), dtype=x.dtype, device=x.device)
-    return _call(GEMM_FPROP, _row_major(x), _row_major(w), y, m_splits, x.shape[0], N, K, OUT_SAME, out is None, ws)
+    _call(GEMM_FPROP, _row_major(x), _row_major(w), y, m_splits, x.shape[0], N, K, OUT_SAME, out is None, ws)
+    return y if out is None else _written(out)
 
 
 def grouped_matmul_dgrad(dy, w, m_splits, out=None, ws=None):
@@ -196,7 +203,8 @@ def grouped_matmul_dgrad(dy, w, m_splits, out=None, ws=None):
         _check_rows_out(out, (dy.shape[0], K), dy, "out")
         _no_overlap(out, "out", dy=dy, w=w)
     dx = out if out is not None else torch.empty((dy.shape[0], K), dtype=dy.dtype, device=dy.device)
-    return _call(GEMM_DGRAD, _row_major(dy), _row_major(w), dx, m_splits, dy.shape[0], K, N, OUT_SAME, out is None, ws)
+    _call(GEMM_DGRAD, _row_major(dy), _row_major(w), dx, m_splits, dy.shape[0], K, N, OUT_SAME, out is None, ws)
+    return dx if out is None else _written(out)
 
 
 def grouped_matmul_wgrad(dy, x, m_splits, out_dtype=OUT_SAME, out=None, ws=None):
@@ -219,8 +227,8 @@ def grouped_matmul_wgrad(dy, x, m_splits, out_dtype=OUT_SAME, out=None, ws=None)
             raise ValueError(f"out: on {out.device}, the other tensors are on {dy.device}")
         _no_overlap(out, "out", dy=dy, x=x)
     dw = out if out is not None else torch.empty(shape, dtype=dt, device=dy.device)
-    return _call(GEMM_WGRAD, _row_major(dy), _row_major(x), dw, m_splits, dy.shape[0], dy.shape[1], x.shape[1], out_dtype,
-                 False, ws)
+    _call(GEMM_WGRAD, _row_major(dy), _row_major(x), dw, m_splits, dy.shape[0], dy.shape[1], x.shape[1], out_dtype, False, ws)
+    return dw if out is None else _written(out)
 
 
 class GroupedMatmulFunction(torch.autograd.Function):
