@@ -180,19 +180,21 @@ def lora_backward(dy, x, a, b, ctx, dx_add=None, need_dx=True, need_da=True, nee
 class LoraFunction(torch.autograd.Function):
     @staticmethod
     def forward(fctx, base, x, a, b, ids, scales):
-        y, fctx.lora = lora_forward(base, x, a, b, ids, scales)
-        fctx.save_for_backward(x, a, b, scales)
+        y, c = lora_forward(base, x, a, b, ids, scales)
+        fctx.lora = (c.M, c.K, c.N, c.R, c.L, c.dtype)
+        fctx.save_for_backward(x, a, b, scales, c.buf)
         return y
 
     @staticmethod
     @once_differentiable
     def backward(fctx, dy):
-        x, a, b, _ = fctx.saved_tensors
+        x, a, b, scales, buf = fctx.saved_tensors
         need = fctx.needs_input_grad
         dyt = dy.to(x.dtype)
         g = {"dx": None, "da": None, "db": None}
         if need[1] or need[2] or need[3]:
-            g = lora_backward(dyt, x, a, b, fctx.lora, need_dx=need[1], need_da=need[2], need_db=need[3])
+            ctx = LoraContext(buf, *fctx.lora, scales.contiguous() if scales is not None else None)
+            g = lora_backward(dyt, x, a, b, ctx, need_dx=need[1], need_da=need[2], need_db=need[3])
         return dyt if need[0] else None, g["dx"], g["da"], g["db"], None, None
 
 

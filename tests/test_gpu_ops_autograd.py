@@ -69,3 +69,29 @@ def test_inputs_and_new_outputs_are_not_touched():
         out = torch.empty_like(y)
         g.grouped_matmul_forward(x, w, m, out=out)
     assert torch.equal(out, y)
+
+
+def test_the_adapters_context_passes_the_saved_tensor_hooks():
+    """Everything that lora's backward reads goes through the hooks (offloading to the host, say), gives the
+    same bits after a round trip, and is let go with the graph."""
+    t = [randn((M, N), BF, 1).cuda(), randn((M, K), BF, 2).cuda(), randn((2, R, K), BF, 3).cuda(), randn((2, N, R), BF, 4).cuda()]
+    ids = (torch.arange(M, device="cuda") % 3 - 1).to(torch.int32)
+    wide = torch.tensor([0.5, 9.0, 1.5, 9.0], device="cuda")
+    dy = randn((M, N), BF, 5).cuda()
+    for scales in (None, torch.tensor([0.5, 1.5], device="cuda"), wide[::2]):
+        grads, seen = [], []
+
+        def pack(s):
+            seen.append(s.nbytes)
+            return s.cpu()
+        for hooks in (False, True):
+            leaf = [v.clone().requires_grad_() for v in t]
+            if hooks:
+                with torch.autograd.graph.saved_tensors_hooks(pack, lambda s: s.cuda()):
+                    y = g.lora(*leaf, ids, scales)
+            else:
+                y = g.lora(*leaf, ids, scales)
+            y.backward(dy)
+            grads.append([v.grad for v in leaf])
+        assert all(torch.equal(p, q) for p, q in zip(*grads))
+        assert sum(seen) >= sum(v.nbytes for v in t[1:]) + g.lora_query_sizes(M, K, N, R, 2)["ctx_bytes"]
