@@ -4,6 +4,7 @@
 // of 128 experts, rows of 7168: order 10 us, moves 190 to 230 us each (4.6 to 5.6 TB/s; a plain copy
 // reaches 5.2).
 #include "mm_common.h"
+#include "op_sizes.h"
 
 #include <algorithm>
 
@@ -238,6 +239,7 @@ __device__ __forceinline__ Place place_of(int chunks, int64_t T, int64_t block, 
 static int64_t place_blocks(int chunks, int64_t T) {
   return chunks >= MT ? T * ((chunks + MT - 1) / MT) : (T + MT / chunks - 1) / (MT / chunks);
 }
+__device__ __forceinline__ int64_t block_number() { return blockIdx.x + (int64_t)blockIdx.y * gridDim.x; }
 
 constexpr int kRestBlocks = 64;      // blocks that clear the rows behind the last used one
 
@@ -245,18 +247,19 @@ template <int TYPE, int V, bool SCALE, bool NT>
 __global__ __launch_bounds__(MT) void dispatch_kernel(MoveArgs p, int chunks, int64_t blocks) {
   using E = Elem<TYPE>;
   uint16_t* dst = static_cast<uint16_t*>(p.dst);
-  const int64_t M = p.T * p.k;
-  if ((int64_t)blockIdx.x >= blocks) {
+  const int64_t M = p.T * p.k, block = block_number();
+  if (block >= blocks) {
+    if (!p.zero_rest || block >= blocks + kRestBlocks) return;
     long long used = 0;
     for (int e = threadIdx.x & 63; e < p.E; e += 64) used += max(p.count[e], 0);
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) used += __shfl_xor(used, o, 64);
     const Chunk<V> zero = {};
-    for (int64_t r = used + (blockIdx.x - blocks); r < M; r += kRestBlocks)
+    for (int64_t r = used + (block - blocks); r < M; r += kRestBlocks)
       for (int c = threadIdx.x; c < chunks; c += MT) store_chunk<V>(dst + r * p.ld_dst + chunk_start<V>(c, p.H), zero);
     return;
   }
-  const Place w = place_of(chunks, p.T, blockIdx.x, threadIdx.x);
+  const Place w = place_of(chunks, p.T, block, threadIdx.x);
   if (w.t < 0) return;
   const int at = chunk_start<V>(w.c, p.H);
   const Chunk<V> x = load_chunk<V>(static_cast<const uint16_t*>(p.src) + w.t * p.ld_src + at);
@@ -278,7 +281,7 @@ __global__ __launch_bounds__(MT) void combine_kernel(MoveArgs p, int chunks) {
   using E = Elem<TYPE>;
   const uint16_t* src = static_cast<const uint16_t*>(p.src);
   const int64_t M = p.T * p.k;
-  const Place w = place_of(chunks, p.T, blockIdx.x, threadIdx.x);
+  const Place w = place_of(chunks, p.T, block_number(), threadIdx.x);
   if (w.t < 0) return;
   const int at = chunk_start<V>(w.c, p.H);
   float acc[V] = {};
@@ -313,7 +316,8 @@ __global__ __launch_bounds__(MT) void combine_dprobs_kernel(MoveArgs p, int chun
   using E = Elem<TYPE>;
   __shared__ float red[MT / 64][8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t t = blockIdx.x, M = p.T * p.k;
+  const int64_t t = block_number(), M = p.T * p.k;
+  if (t >= p.T) return;
   const uint16_t* dy = static_cast<const uint16_t*>(p.src) + t * p.ld_src;
   const uint16_t* v = static_cast<const uint16_t*>(p.src2);
   for (int j0 = 0; j0 < p.k; j0 += 8) {
@@ -354,7 +358,10 @@ __global__ __launch_bounds__(MT) void combine_dprobs_kernel(MoveArgs p, int chun
   }
 }
 
-static hipError_t grid_ok(int64_t blocks) { return blocks <= 0x7FFFFFFF ? hipSuccess : hipErrorInvalidValue; }
+static dim3 grid_of(int64_t blocks) {
+  const FoldedGrid g = fold_grid(blocks, MT);
+  return dim3(g.x, g.y);
+}
 
 // Half the 256 MB last-level cache.
 static bool past_cache(const MoveArgs& p) { return (double)p.T * p.k * p.H * 2 > 128e6; }
@@ -362,10 +369,10 @@ static bool past_cache(const MoveArgs& p) { return (double)p.T * p.k * p.H * 2 >
 template <int TYPE, int V, bool NT>
 static hipError_t run_dispatch_nt(const MoveArgs& p, hipStream_t s) {
   const int chunks = (p.H + V - 1) / V;
-  const int64_t blocks = place_blocks(chunks, p.T), grid = blocks + (p.zero_rest ? kRestBlocks : 0);
-  if (hipError_t e = grid_ok(grid)) return e;
-  if (p.probs) hipLaunchKernelGGL((dispatch_kernel<TYPE, V, true, NT>), dim3((uint32_t)grid), dim3(MT), 0, s, p, chunks, blocks);
-  else hipLaunchKernelGGL((dispatch_kernel<TYPE, V, false, NT>), dim3((uint32_t)grid), dim3(MT), 0, s, p, chunks, blocks);
+  const int64_t blocks = place_blocks(chunks, p.T);
+  const dim3 grid = grid_of(blocks + (p.zero_rest ? kRestBlocks : 0));
+  if (p.probs) hipLaunchKernelGGL((dispatch_kernel<TYPE, V, true, NT>), grid, dim3(MT), 0, s, p, chunks, blocks);
+  else hipLaunchKernelGGL((dispatch_kernel<TYPE, V, false, NT>), grid, dim3(MT), 0, s, p, chunks, blocks);
   return hipGetLastError();
 }
 template <int TYPE, int V>
@@ -375,10 +382,9 @@ static hipError_t run_dispatch(const MoveArgs& p, hipStream_t s) {
 template <int TYPE, int V, bool NT>
 static hipError_t run_combine_nt(const MoveArgs& p, hipStream_t s) {
   const int chunks = (p.H + V - 1) / V;
-  const int64_t grid = place_blocks(chunks, p.T);
-  if (hipError_t e = grid_ok(grid)) return e;
-  if (p.probs) hipLaunchKernelGGL((combine_kernel<TYPE, V, true, NT>), dim3((uint32_t)grid), dim3(MT), 0, s, p, chunks);
-  else hipLaunchKernelGGL((combine_kernel<TYPE, V, false, NT>), dim3((uint32_t)grid), dim3(MT), 0, s, p, chunks);
+  const dim3 grid = grid_of(place_blocks(chunks, p.T));
+  if (p.probs) hipLaunchKernelGGL((combine_kernel<TYPE, V, true, NT>), grid, dim3(MT), 0, s, p, chunks);
+  else hipLaunchKernelGGL((combine_kernel<TYPE, V, false, NT>), grid, dim3(MT), 0, s, p, chunks);
   return hipGetLastError();
 }
 template <int TYPE, int V>
@@ -389,9 +395,9 @@ template <int TYPE, int V>
 static hipError_t run_dprobs(const MoveArgs& p, hipStream_t s) {
   const int chunks = (p.H + V - 1) / V;
   if (V == 8 && past_cache(p))
-    hipLaunchKernelGGL((combine_dprobs_kernel<TYPE, V, V == 8>), dim3((uint32_t)p.T), dim3(MT), 0, s, p, chunks);
+    hipLaunchKernelGGL((combine_dprobs_kernel<TYPE, V, V == 8>), grid_of(p.T), dim3(MT), 0, s, p, chunks);
   else
-    hipLaunchKernelGGL((combine_dprobs_kernel<TYPE, V, false>), dim3((uint32_t)p.T), dim3(MT), 0, s, p, chunks);
+    hipLaunchKernelGGL((combine_dprobs_kernel<TYPE, V, false>), grid_of(p.T), dim3(MT), 0, s, p, chunks);
   return hipGetLastError();
 }
 

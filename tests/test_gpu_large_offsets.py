@@ -125,3 +125,31 @@ def test_calls_on_two_streams_at_once():
         for i in range(2):
             for j, (p, q) in enumerate(zip(alone[i], out[i])):
                 assert torch.equal(p, q), (i, j)
+
+
+def test_moves_of_more_tokens_than_one_row_of_blocks():
+    """2^24 tokens and more: as many workgroups of 256 threads pass the 32 bits of a launch's threads along x."""
+    T, H, E = (1 << 24) + 5, 8, 3
+    print("moves of 2^24 + 5 short rows", flush=True)
+    experts = (torch.arange(T, device="cuda") % 4).to(torch.int32).view(T, 1)         # expert 3: dropped
+    plan = g.dispatch_plan(experts, E)
+    used = int(plan.m_splits.sum())
+    x = (torch.arange(T, device="cuda") % 251).to(torch.bfloat16)[:, None] + torch.arange(H, device="cuda").to(torch.bfloat16) * 0
+    xg = g.dispatch_forward(x, plan)
+    live = plan.rows[:, 0] >= 0
+    assert torch.equal(xg[plan.rows[live, 0].long()], x[live]) and not xg[used:].any()
+    _, dp = g.combine_backward(x, xg, plan, torch.ones((T, 1), device="cuda"), need_dv=False)
+    assert torch.equal(dp[:, 0], torch.where(live, (x.float() * x.float()).sum(1), torch.zeros((), device="cuda")))
+    del x, xg, dp
+    H = 1032                                             # one token a workgroup in dispatch and combine too
+    print("moves of 2^24 + 5 rows of 1032", flush=True)
+    x = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    x.copy_((torch.arange(T, device="cuda") % 251).to(torch.bfloat16)[:, None])
+    x[:, -1] = (torch.arange(T, device="cuda") % 127).to(torch.bfloat16)
+    xg = g.dispatch_forward(x, plan)
+    for c in (0, 7, H - 9, H - 1):
+        assert torch.equal(xg[plan.rows[live, 0].long(), c], x[live, c]) and not xg[used:, c].any()
+    want = [torch.where(live, x[:, c], torch.zeros((), dtype=x.dtype, device="cuda")) for c in (0, 7, H - 9, H - 1)]
+    g.combine_forward(xg, plan, out=x)
+    for c, w in zip((0, 7, H - 9, H - 1), want):
+        assert torch.equal(x[:, c], w)
