@@ -9,6 +9,7 @@
 // one V_MFMA_F32_16X16X32 takes 16 ranks, hi in its lower and lo in its upper sixteen contraction
 // steps.  fp16 scales each position's v by a power of two first, so that neither half leaves the range.
 #include "mm_common.h"
+#include "op_sizes.h"
 
 #include <algorithm>
 
@@ -63,7 +64,8 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraShrink p) {
   __shared__ __align__(16) float red[NW * RB * 16 * LD];
   __shared__ float s_mul[RB * 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const RowTile rt = find_row_tile(p.rows.count, p.rows.L, (uint32_t)p.rows.M, RB * 16, 1, false, blockIdx.x, lane);
+  const RowTile rt = find_row_tile(p.rows.count, p.rows.L, (uint32_t)p.rows.M, RB * 16, 1, false,
+                                   blockIdx.x + blockIdx.y * gridDim.x, lane);
   if (rt.g < 0) return;
   const int64_t pos0 = (int64_t)rt.row0 + rt.t * (RB * 16);
   const int valid = min((int)(rt.m - rt.t * (RB * 16)), RB * 16);
@@ -192,8 +194,8 @@ static int64_t tiles_bound(int64_t M, int groups, int64_t h) { return (M + (h - 
 
 template <int TYPE, bool VEC, int RB, int RT, int NW>
 static hipError_t run_shrink(const LoraShrink& p, hipStream_t s) {
-  const int64_t tiles = tiles_bound(p.rows.M, p.rows.L, 16 * RB);
-  hipLaunchKernelGGL((lora_shrink_kernel<TYPE, VEC, RB, RT, NW>), dim3((uint32_t)tiles), dim3(64 * NW), 0, s, p);
+  const FoldedGrid grid = fold_grid(tiles_bound(p.rows.M, p.rows.L, 16 * RB), 64 * NW);
+  hipLaunchKernelGGL((lora_shrink_kernel<TYPE, VEC, RB, RT, NW>), dim3(grid.x, grid.y), dim3(64 * NW), 0, s, p);
   return hipGetLastError();
 }
 // 32 positions a tile where those fill the device, 16 waves while one tile a CU is all there is, else 8;

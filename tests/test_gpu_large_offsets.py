@@ -153,3 +153,22 @@ def test_moves_of_more_tokens_than_one_row_of_blocks():
     g.combine_forward(xg, plan, out=x)
     for c, w in zip((0, 7, H - 9, H - 1), want):
         assert torch.equal(x[:, c], w)
+
+
+def test_adapters_of_more_rows_than_one_row_of_blocks():
+    """2^28 rows and more: their tiles of 32 by workgroups of 512 threads pass the 32 bits of a launch's
+    threads along x.  Small integers, so every value is exact."""
+    M, K, N, R, L = (1 << 28) + 37, 8, 8, 1, 2
+    print("adapters of 2^28 + 37 short rows", flush=True)
+    x = (torch.arange(M, device="cuda", dtype=torch.int32) % 13).to(torch.bfloat16)[:, None].expand(M, K).contiguous()
+    ids = (torch.arange(M, device="cuda", dtype=torch.int32) % 3 - 1).to(torch.int32)
+    a = torch.ones((L, R, K), dtype=torch.bfloat16, device="cuda")
+    b = torch.arange(1, N + 1, device="cuda").to(torch.bfloat16).view(1, N, 1).expand(L, N, R).contiguous()
+    y, ctx = g.lora_forward(None, x, a, b, ids)
+    for c in (0, N - 1):                                  # 8 x (c + 1): at most 8 x 12 x 8 = 768, in steps of 8 (c + 1)
+        want = torch.where(ids >= 0, x[:, 0].float() * (8 * (c + 1)), torch.zeros((), device="cuda")).to(torch.bfloat16)
+        assert torch.equal(y[:, c], want), c
+    y.fill_(1)
+    dx = g.lora_backward(y, x, a, b, ctx, need_da=False, need_db=False)["dx"]
+    want = torch.where(ids >= 0, torch.full((), float(sum(range(1, N + 1))), device="cuda"), torch.zeros((), device="cuda"))
+    assert torch.equal(dx[:, 0], want.to(torch.bfloat16)) and torch.equal(dx[:, K - 1], want.to(torch.bfloat16))
