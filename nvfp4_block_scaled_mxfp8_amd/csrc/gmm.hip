@@ -3,6 +3,7 @@
 // accumulated in fp32 on the matrix cores and rounded once.  The split sizes are read on the
 // device (mm_common.h).
 #include "mm_common.h"
+#include "op_sizes.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -222,7 +223,8 @@ __global__ __launch_bounds__(256, 2) void gmm_ring_kernel(MmArgs p) {
   constexpr int WM = 64, WN = 64, NA = WM / 32, NB = WN / 32;
   __shared__ __align__(1024) uint8_t lds[(VEC ? 5 : 4) * SLOT];
   const int tid = threadIdx.x, lane = tid & 63, wave = sgpr(tid >> 6);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) {
+  const uint32_t block = blockIdx.x + blockIdx.z * gridDim.x;
+  if (block == 0 && blockIdx.y == 0 && wave == 0) {
     const uint32_t f = wave_split_flags(p.m_splits, p.G, p.M, lane);
     if (lane == 0) *p.flags = f;
   }
@@ -238,13 +240,13 @@ __global__ __launch_bounds__(256, 2) void gmm_ring_kernel(MmArgs p) {
     const uint32_t ntm = (p.n + T - 1) / T, ntn = (p.k + T - 1) / T, tpg = ntm * ntn;
     uint32_t g, t;
     if (tpg >= 64) {                     // XCD x takes the x-th eighth of every group's tiles
-      const uint32_t per = (tpg + 7) / 8, x = blockIdx.x & 7, l = blockIdx.x >> 3;
+      const uint32_t per = (tpg + 7) / 8, x = block & 7, l = block >> 3;
       g = l / per;
       t = x * per + l % per;
       if (t >= tpg || (int)g >= p.G) return;
     } else {
-      g = blockIdx.x / tpg;
-      t = blockIdx.x % tpg;
+      g = block / tpg;
+      t = block % tpg;
       if ((int)g >= p.G) return;
     }
     const RowTile rt = find_group_rows(p.m_splits, p.G, (uint32_t)p.M, (int)g, lane);
@@ -262,9 +264,9 @@ __global__ __launch_bounds__(256, 2) void gmm_ring_kernel(MmArgs p) {
   } else {
     const uint32_t ntn = (p.n + T - 1) / T;
     const uint32_t total = row_tiles_total(p.m_splits, p.G, (uint32_t)p.M, T, ntn, p.zero_rest, lane);
-    const uint32_t per = (total + 7) / 8, l = blockIdx.x >> 3;     // XCD x takes the x-th eighth of the tiles
+    const uint32_t per = (total + 7) / 8, l = block >> 3;          // XCD x takes the x-th eighth of the tiles
     if (l >= per) return;
-    const RowTile rt = find_row_tile(p.m_splits, p.G, (uint32_t)p.M, T, ntn, p.zero_rest, (blockIdx.x & 7) * per + l, lane);
+    const RowTile rt = find_row_tile(p.m_splits, p.G, (uint32_t)p.M, T, ntn, p.zero_rest, (block & 7) * per + l, lane);
     if (rt.g < 0) return;
     const uint32_t ntm = (rt.m + T - 1) / T;
     const uint32_t grp = rt.t / (GR * ntn), rem = rt.t % (GR * ntn), rh = min(GR, ntm - grp * GR);
@@ -970,10 +972,10 @@ static hipError_t run_ring(const MmArgs& p, hipStream_t s) {
   } else {
     grid = 8 * ((row_tiles_bound(p, T) * ((p.n + T - 1) / T) + 7) / 8);
   }
-  grid = std::max<int64_t>(grid, 8);
+  const FoldedGrid f = fold_grid(std::max<int64_t>(grid, 8), 256);
   const bool once = VEC && LAYOUT != MM_WGRAD && weights_once(p);
   auto* k = once ? gmm_ring_kernel<TYPE, LAYOUT, OUT, VEC, VEC && LAYOUT != MM_WGRAD> : gmm_ring_kernel<TYPE, LAYOUT, OUT, VEC, false>;
-  hipLaunchKernelGGL(k, dim3((uint32_t)grid, OUT == MM_OUT_PART ? p.parts : 1), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(k, dim3(f.x, OUT == MM_OUT_PART ? p.parts : 1, f.y), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 template <int TYPE, int LAYOUT, int OUT, bool VEC>

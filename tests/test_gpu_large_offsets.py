@@ -172,3 +172,18 @@ def test_adapters_of_more_rows_than_one_row_of_blocks():
     dx = g.lora_backward(y, x, a, b, ctx, need_da=False, need_db=False)["dx"]
     want = torch.where(ids >= 0, torch.full((), float(sum(range(1, N + 1))), device="cuda"), torch.zeros((), device="cuda"))
     assert torch.equal(dx[:, 0], want.to(torch.bfloat16)) and torch.equal(dx[:, K - 1], want.to(torch.bfloat16))
+
+
+def test_products_of_more_tiles_than_one_row_of_blocks():
+    """4096 groups of one row and 2^19 + 128 columns: the tiles' workgroups of 256 threads pass the 32 bits of a
+    launch's threads along x.  A contraction of one element, small integers: exact."""
+    G, N = 4096, (1 << 19) + 128
+    print("products of 2^24 + 4096 tiles", flush=True)
+    m = torch.ones(G, dtype=torch.int32, device="cuda")
+    x = (torch.arange(G, device="cuda") % 7 - 3).to(torch.bfloat16)[:, None].contiguous()
+    w = ((torch.arange(G, device="cuda")[:, None] + torch.arange(N, device="cuda", dtype=torch.int32)) % 13).to(torch.bfloat16)
+    want = x * w
+    assert torch.equal(g.grouped_matmul_forward(x, w[:, :, None], m), want)
+    assert torch.equal(g.grouped_matmul_dgrad(x, w[:, None, :], m), want)
+    assert torch.equal(g.grouped_matmul_wgrad(w, x, m)[:, :, 0], want)
+    assert torch.equal(g.grouped_matmul_wgrad(x, w, m)[:, 0], want)
