@@ -361,7 +361,7 @@ typedef enum { GMLP_BF16 = 0, GMLP_FP16 = 1 } gmlp_dtype;
  * (DGRAD reads the same weight [G, N, K] as FPROP with k = N, n = K.)  The last dimension of every
  * tensor is contiguous; lda, ldb, ldc are the row strides and b_stride (FPROP, DGRAD), c_stride
  * (WGRAD) the group strides, in elements; every size, stride and element alignment is taken
- * (multiples of 16 bytes run on the fast kernels).  Sizes n, k >= 1, row strides < 2^20.
+ * (multiples of 16 bytes run on the fast kernels).  Sizes n, k >= 1, row strides < 2^20, 1 <= G <= 65536.
  * out_dtype: 0 the operands' type, GMLP_OUT_FP32, GMLP_OUT_FP32_ACCUMULATE (the last two WGRAD
  * only, else GMLP_UNSUPPORTED); an empty group's c[g] is zero, or left as it is when accumulating.
  * Rows of c behind the last group (splits that sum short of M) are zeroed when zero_rest != 0,

@@ -11,6 +11,10 @@ namespace {
 
 constexpr int64_t kMaxRows = 1LL << 30;
 constexpr int64_t kMaxLd = 1LL << 20;      // a tile's rows then span less than 2^31 bytes
+// Every workgroup of a grouped product walks the split sizes, 64 groups at a time, so that the time grows with the
+// groups' square where each has a tile: 0.6 ms for 4096 groups of one row, 9 ms for 16384, 147 ms for 65536; 2^20
+// would take 40 s and 2^24 hours.
+constexpr int32_t kMaxGroups = 1 << 16;
 
 gmlp_status fine() { return set_error(GMLP_OK, "%s", ""); }
 gmlp_status launched(hipError_t e, const char* what) {
@@ -34,6 +38,7 @@ gmlp_status check_mm_sizes(int32_t layout, int32_t G, int64_t M, int64_t n, int6
   if (layout != GMLP_GEMM_FPROP && layout != GMLP_GEMM_WGRAD && layout != GMLP_GEMM_DGRAD)
     return set_error(GMLP_INVALID_ARG, "layout: unknown layout %d", layout);
   if (G < 1) return set_error(GMLP_INVALID_ARG, "dims: number of groups must be >= 1, got %d", G);
+  if (G > kMaxGroups) return set_error(GMLP_UNSUPPORTED, "dims: at most %d groups are supported, got %d", kMaxGroups, G);
   if (M < 0 || M > kMaxRows) return set_error(GMLP_UNSUPPORTED, "dims: M = %lld rows is out of range", (long long)M);
   if (n < 1 || k < 1 || n >= kMaxLd || k >= kMaxLd)
     return set_error(GMLP_UNSUPPORTED, "dims: n and k must be in [1, 2^20), got %lld and %lld", (long long)n, (long long)k);

@@ -113,6 +113,15 @@ def test_grouped_matmul_null_arguments():
     assert g.grouped_matmul_ws_bytes(g.GEMM_WGRAD, 128, 65536, 4096, 7168) >= 256
 
 
+def test_grouped_matmul_group_limit():
+    """Each workgroup walks the groups: more than 2^16 would take minutes to hours."""
+    assert _mm(G=(1 << 16) + 1, b_stride=128) == 2 and "at most 65536 groups" in g.last_error()
+    assert _mm(G=1 << 24, M=1 << 24, n=1, k=1, lda=1, ldb=1, ldc=1, b_stride=1) == 2 and "65536 groups" in g.last_error()
+    with pytest.raises(g.GmlpError, match="65536 groups"):
+        g.grouped_matmul_ws_bytes(g.GEMM_WGRAD, (1 << 16) + 1, 4, 8, 8)
+    assert g.grouped_matmul_ws_bytes(g.GEMM_WGRAD, 1 << 16, 4, 8, 8) > 0
+
+
 def test_dispatch_binding_refusals():
     with pytest.raises(TypeError, match="experts"):
         g.dispatch_plan(torch.zeros((4, 2), dtype=torch.int64), 8)
