@@ -366,9 +366,9 @@ typedef enum { GMLP_BF16 = 0, GMLP_FP16 = 1 } gmlp_dtype;
  * only, else GMLP_UNSUPPORTED); an empty group's c[g] is zero, or left as it is when accumulating.
  * Rows of c behind the last group (splits that sum short of M) are zeroed when zero_rest != 0,
  * else left as they are.  Splits are clamped on the device as everywhere (gmlp_read_device_flags
- * on ws).  c must not overlap a or b.
- * ws: >= gmlp_grouped_matmul_ws_bytes for the same sizes, 16-byte aligned; two calls that may run
- * at the same time need two. */
+ * on ws).  c must not overlap a, b or m_splits.
+ * ws: >= gmlp_grouped_matmul_ws_bytes for the same sizes, 16-byte aligned, apart from every tensor of the
+ * call; two calls that may run at the same time need two. */
 typedef struct {
   int32_t layout;             /* gmlp_gemm_layout */
   int32_t dtype;              /* gmlp_dtype of a and b */

@@ -109,7 +109,7 @@ def _extent(t):
     return t.data_ptr(), t.data_ptr() + n * t.element_size()
 
 
-def _no_overlap(out, name, **inputs):
+def _no_overlap(out, name, /, **inputs):
     """An output must not share elements with what the call reads while it is written (columns of one
     wide tensor beside each other are fine)."""
     if out.numel() == 0:
@@ -157,12 +157,16 @@ def _call(layout, a, b, c, m_splits, M, n, k, out_dtype, zero_rest, ws):
     G = m_splits.numel()
     if m_splits.device != dev:
         raise ValueError(f"m_splits: on {m_splits.device}, the other tensors are on {dev}")
+    if ws is not None:
+        if not isinstance(ws, torch.Tensor) or ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws: a contiguous tensor on {dev} is required")
+        # the kernels address what the tables in it say
+        _no_overlap(ws, "ws", out=c, m_splits=m_splits, **{"x" if layout == GEMM_FPROP else "dy": a,
+                                                           "x" if layout == GEMM_WGRAD else "w": b})
     if dev.type != "cuda":
         _dev_ptr(a, "dy" if layout != GEMM_FPROP else "x")          # refuses host tensors
     if ws is None:
         ws = torch.empty(grouped_matmul_ws_bytes(layout, G, M, n, k), dtype=torch.uint8, device=dev)
-    elif ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"ws: a contiguous tensor on {dev} is required")
     wgrad = layout == GEMM_WGRAD
     args = _pack_mm(layout, _DTYPES[a.dtype], out_dtype, zero_rest, a.data_ptr(), _ld(a), b.data_ptr(), _ld(b),
                     0 if wgrad else _gs(b), c.data_ptr(), _ld(c), _gs(c) if wgrad else 0, m_splits.data_ptr(), G, M, n, k,

@@ -81,6 +81,25 @@ def test_outputs_that_overlap_inputs_are_refused():
         g.lora_forward(buf[:4], x, a, b, ids, out=buf[:4])
 
 
+def test_a_workspace_inside_a_tensor_of_the_call_is_refused():
+    """The kernels address what the tables in the workspace say, so nothing else may be written there."""
+    m = torch.tensor([2, 2], dtype=torch.int32)
+    x, w, dy = _t(4, 16), _t(2, 8, 16), _t(4, 8)
+    y, dx, dw = _t(4, 8), _t(4, 16), _t(2, 8, 16)
+    fwd = lambda ws: g.grouped_matmul_forward(x, w, m, out=y, ws=ws)
+    dgrad = lambda ws: g.grouped_matmul_dgrad(dy, w, m, out=dx, ws=ws)
+    wgrad = lambda ws: g.grouped_matmul_wgrad(dy, x, m, out=dw, ws=ws)
+    for call, names in ((fwd, dict(x=x, w=w, out=y, m_splits=m)), (dgrad, dict(dy=dy, w=w, out=dx, m_splits=m)),
+                        (wgrad, dict(dy=dy, x=x, out=dw, m_splits=m))):
+        for name, t in names.items():
+            with pytest.raises(ValueError, match=f"ws: overlaps {name}"):
+                call(t.view(torch.uint8)[-1:])
+        with pytest.raises(ValueError, match="GPU tensor"):
+            call(_t(4096))
+        with pytest.raises(ValueError, match="ws: a contiguous"):
+            call(_t(64, 64)[:, :32])
+
+
 def _mm(**kw):
     a = g.GroupedMatmulArgs()
     vals = dict(layout=0, dtype=0, out_dtype=0, zero_rest=0, a=256, lda=16, b=256, ldb=16, b_stride=128, c=256, ldc=8,
