@@ -406,7 +406,7 @@ gmlp_status gmlp_dispatch_plan(const int32_t* experts, int64_t n, int32_t E, int
  *   combine           dst[t] = sum_j probs[t, j] src[rows[t, j]]  (src by row; also dispatch's gradient)
  *   combine_dprobs    dprobs[t, j] = sum_h src[t, h] src2[rows[t, j], h]   (0 for a dropped slot)
  * Rows of dispatch's dst behind the sum of m_splits [E] are zeroed when zero_rest != 0, else left as
- * they are.  Outputs must not overlap inputs. */
+ * they are.  Outputs must not overlap inputs, the rows, splits and probabilities among them. */
 typedef struct {
   int32_t dtype;              /* gmlp_dtype */
   int32_t zero_rest;
@@ -439,7 +439,7 @@ gmlp_status gmlp_combine_dprobs(const gmlp_move_args* args, hipStream_t stream);
  * at least 16 of their bits.  a [L, R, K], b [L, N, R] with row strides lda, ldb and adapter
  * strides a_stride, b_stride; x [M, K], base, y, dy [M, N], dx, dx_add [M, K] with row strides; the
  * last dimension contiguous everywhere, da, db contiguous; strides in elements.  base and dx_add
- * may be NULL (zeros) or the output itself; other overlaps are not allowed.  scales: device fp32
+ * may be NULL (zeros) or the output itself; other overlaps (ids and scales among them) are not allowed.  scales: device fp32
  * [L], or NULL for 1.  1 <= R <= 128, 1 <= L <= 1023.
  * The forward leaves in ctx the rows' order by adapter and u; the backward of the same M, K, N, R, L
  * reads it (keep it untouched in between).  dx, da, db: NULL where not needed (x is read for da). */

@@ -121,7 +121,7 @@ def lora_forward(base, x, a, b, ids, scales=None, out=None):
             raise ValueError(f"base: shape {(M, N)} expected, got {tuple(base.shape)}")
         base = _row_major(base)
     if out is not None:
-        _no_overlap(out, "out", x=x, a=a, b=b)
+        _no_overlap(out, "out", x=x, a=a, b=b, ids=ids, scales=scales)
         if base is not None and (out.data_ptr() != base.data_ptr() or _ld(out) != _ld(base)):
             _no_overlap(out, "out", base=base)
     _dev_ptr(x, "x")

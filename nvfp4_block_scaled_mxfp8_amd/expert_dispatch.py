@@ -124,7 +124,7 @@ def _to_rows(src, plan, probs, out):
     shape = (plan.rows.numel(), src.shape[1])
     if out is not None:
         _check_rows_out(out, shape, src, "out")
-        _no_overlap(out, "out", input=src)
+        _no_overlap(out, "out", input=src, probs=probs, rows=plan.rows, m_splits=plan.m_splits)
     dst = out if out is not None else torch.empty(shape, dtype=src.dtype, device=src.device)
     _move("gmlp_dispatch", plan, src, dst, probs, zero_rest=out is None)
     return dst if out is None else _written(out)
@@ -134,7 +134,7 @@ def _to_tokens(src, plan, probs, out):
     shape = (plan.tokens, src.shape[1])
     if out is not None:
         _check_rows_out(out, shape, src, "out")
-        _no_overlap(out, "out", input=src)
+        _no_overlap(out, "out", input=src, probs=probs, rows=plan.rows, m_splits=plan.m_splits)
     dst = out if out is not None else torch.empty(shape, dtype=src.dtype, device=src.device)
     _move("gmlp_combine", plan, src, dst, probs)
     return dst if out is None else _written(out)

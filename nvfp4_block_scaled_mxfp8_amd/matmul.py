@@ -187,7 +187,7 @@ def grouped_matmul_forward(x, w, m_splits, out=None, ws=None):
     m_splits = _splits(m_splits, G)
     if out is not None:
         _check_rows_out(out, (x.shape[0], N), x, "out")
-        _no_overlap(out, "out", x=x, w=w)
+        _no_overlap(out, "out", x=x, w=w, m_splits=m_splits)
     y = out if out is not None else torch.empty((x.shape[0], N), dtype=x.dtype, device=x.device)
     _call(GEMM_FPROP, _row_major(x), _row_major(w), y, m_splits, x.shape[0], N, K, OUT_SAME, out is None, ws)
     return y if out is None else _written(out)
@@ -205,7 +205,7 @@ def grouped_matmul_dgrad(dy, w, m_splits, out=None, ws=None):
     m_splits = _splits(m_splits, G)
     if out is not None:
         _check_rows_out(out, (dy.shape[0], K), dy, "out")
-        _no_overlap(out, "out", dy=dy, w=w)
+        _no_overlap(out, "out", dy=dy, w=w, m_splits=m_splits)
     dx = out if out is not None else torch.empty((dy.shape[0], K), dtype=dy.dtype, device=dy.device)
     _call(GEMM_DGRAD, _row_major(dy), _row_major(w), dx, m_splits, dy.shape[0], K, N, OUT_SAME, out is None, ws)
     return dx if out is None else _written(out)
@@ -229,7 +229,7 @@ def grouped_matmul_wgrad(dy, x, m_splits, out_dtype=OUT_SAME, out=None, ws=None)
         _check_out(out, shape, dt, "out")
         if out.device != dy.device:
             raise ValueError(f"out: on {out.device}, the other tensors are on {dy.device}")
-        _no_overlap(out, "out", dy=dy, x=x)
+        _no_overlap(out, "out", dy=dy, x=x, m_splits=m_splits)
     dw = out if out is not None else torch.empty(shape, dtype=dt, device=dy.device)
     _call(GEMM_WGRAD, _row_major(dy), _row_major(x), dw, m_splits, dy.shape[0], dy.shape[1], x.shape[1], out_dtype, False, ws)
     return dw if out is None else _written(out)

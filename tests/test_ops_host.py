@@ -81,6 +81,32 @@ def test_outputs_that_overlap_inputs_are_refused():
         g.lora_forward(buf[:4], x, a, b, ids, out=buf[:4])
 
 
+def test_outputs_over_splits_orders_and_scales_are_refused():
+    """What a call reads besides its 16-bit tensors must not lie in its output either."""
+    def beside(out, n, dtype):
+        return out.view(-1).view(torch.uint8)[-n * dtype.itemsize:].view(dtype)
+    x, w, dy = _t(4, 16), _t(2, 8, 16), _t(4, 8)
+    y, dx, dw = _t(4, 8), _t(4, 16), _t(2, 8, 16)
+    with pytest.raises(ValueError, match="out: overlaps m_splits"):
+        g.grouped_matmul_forward(x, w, beside(y, 2, torch.int32), out=y)
+    with pytest.raises(ValueError, match="out: overlaps m_splits"):
+        g.grouped_matmul_dgrad(dy, w, beside(dx, 2, torch.int32), out=dx)
+    with pytest.raises(ValueError, match="out: overlaps m_splits"):
+        g.grouped_matmul_wgrad(dy, x, beside(dw, 2, torch.int32), out=dw)
+    m, rows, xg = torch.zeros(3, dtype=torch.int32), torch.zeros((4, 2), dtype=torch.int32), _t(8, 16)
+    with pytest.raises(ValueError, match="out: overlaps rows"):
+        g.dispatch_forward(x, g.DispatchPlan(m, beside(xg, 8, torch.int32).view(4, 2)), out=xg)
+    with pytest.raises(ValueError, match="out: overlaps m_splits"):
+        g.dispatch_forward(x, g.DispatchPlan(beside(xg, 3, torch.int32), rows), out=xg)
+    with pytest.raises(ValueError, match="out: overlaps probs"):
+        g.combine_forward(xg, g.DispatchPlan(m, rows), beside(x, 8, torch.float32).view(4, 2), out=x)
+    a, b = _t(2, 4, 16), _t(2, 8, 4)
+    with pytest.raises(ValueError, match="out: overlaps ids"):
+        g.lora_forward(None, x, a, b, beside(y, 4, torch.int32), out=y)
+    with pytest.raises(ValueError, match="out: overlaps scales"):
+        g.lora_forward(None, x, a, b, torch.zeros(4, dtype=torch.int32), beside(y, 2, torch.float32), out=y)
+
+
 def test_a_workspace_inside_a_tensor_of_the_call_is_refused():
     """The kernels address what the tables in the workspace say, so nothing else may be written there."""
     m = torch.tensor([2, 2], dtype=torch.int32)
