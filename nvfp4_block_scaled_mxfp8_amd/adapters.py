@@ -156,8 +156,11 @@ def lora_backward(dy, x, a, b, ctx, dx_add=None, need_dx=True, need_da=True, nee
     _same(x, dy, 2, "x")
     if tuple(x.shape) != (M, K):
         raise ValueError(f"x: shape {(M, K)} expected, got {tuple(x.shape)}")
+    ctx_bytes, _, ws_bytes = _sizes(M, K, N, R, L)
     if ctx.buf.device != dev:
         raise ValueError(f"ctx: on {ctx.buf.device}, the other tensors are on {dev}")
+    if not ctx.buf.is_contiguous() or ctx.buf.numel() * ctx.buf.element_size() < ctx_bytes:
+        raise ValueError(f"ctx: a contiguous buffer of at least {ctx_bytes} bytes is required, got {ctx.buf.numel() * ctx.buf.element_size()}")
     if dx_add is not None:
         _same(dx_add, dy, 2, "dx_add")
         if tuple(dx_add.shape) != (M, K):
@@ -165,7 +168,6 @@ def lora_backward(dy, x, a, b, ctx, dx_add=None, need_dx=True, need_da=True, nee
         dx_add = _row_major(dx_add)
     _dev_ptr(dy, "dy")
     dy, x, a, b = _row_major(dy), _row_major(x), _row_major(a), _row_major(b)
-    ctx_bytes, _, ws_bytes = _sizes(M, K, N, R, L)
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     dx = torch.empty((M, K), dtype=dy.dtype, device=dev) if need_dx else None
     da = torch.empty((L, R, K), dtype=dy.dtype, device=dev) if need_da else None

@@ -269,6 +269,21 @@ def test_lora_sizes_and_scale_gradient_refused():
         g.lora_backward(_t(4, 8), _t(4, 16), _t(2, 4, 16), _t(2, 8, 4), None)
 
 
+def test_lora_context_of_another_size_is_refused():
+    """The kernels address the context by the call's sizes, not by the buffer's."""
+    need = g.lora_query_sizes(4, 16, 8, 4, 2)["ctx_bytes"]
+    args = (_t(4, 8), _t(4, 16), _t(2, 4, 16), _t(2, 8, 4))
+
+    def ctx(buf):
+        return g.LoraContext(buf, 4, 16, 8, 4, 2, torch.bfloat16, None)
+    u8 = dict(dtype=torch.uint8)
+    for buf in (torch.zeros(need - 1, **u8), torch.zeros(0, **u8), torch.zeros((need, 2), **u8)[:, 0]):
+        with pytest.raises(ValueError, match="ctx: a contiguous buffer"):
+            g.lora_backward(*args, ctx(buf))
+    with pytest.raises(ValueError, match="GPU tensor"):
+        g.lora_backward(*args, ctx(torch.zeros(need, **u8)))
+
+
 def _lf(**kw):
     a = g.LoraFwdArgs()
     w = dict(a=256, lda=16, a_stride=64, b=256, ldb=4, b_stride=32, scales=256)
