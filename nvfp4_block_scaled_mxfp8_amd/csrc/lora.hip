@@ -29,11 +29,13 @@ __device__ __forceinline__ v4i fix8(v4i v, int valid, bool brief) {
   else return brief ? v : shift8(v, valid);
 }
 
-// v as a factor of the 16-bit products: hi = T(v), lo = T(v - hi).
+// v as a factor of the 16-bit products: hi = T(v), lo = T(v - hi); hi is the largest finite value where a finite
+// v rounds to infinity (bf16 above 2^128 (1 - 2^-9); lo then holds the rest).
 template <int TYPE>
 __device__ __forceinline__ void split(float v, uint16_t& hi, uint16_t& lo) {
   using E = Elem<TYPE>;
   hi = E::down(v);
+  if (__builtin_isfinite(v) && !__builtin_isfinite(E::up(hi))) --hi;
   const float h = E::up(hi);
   lo = E::down(__builtin_isfinite(h) ? v - h : 0.0f);
 }
@@ -168,7 +170,10 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraShrink p) {
       float top = 0.0f;
 #pragma unroll
       for (int r = 0; r < RT * 16; r += 64)
-        if (r + lane < RT * 16) top = fmaxf(top, fabsf(red[row * LD + r + lane]));       // zero behind rank R
+        if (r + lane < RT * 16) {                        // zero behind rank R
+          const float f = fabsf(red[row * LD + r + lane]);
+          top = fmaxf(top, __builtin_isfinite(f) ? f : 0.0f);
+        }
       const float s = fp16_scale(wave_max(top));
       if (lane == 0) {
         s_mul[row] = s;

@@ -185,6 +185,24 @@ def test_nan_and_infinity_stay_where_they_belong():
     assert bool(got["da"][1].isnan().all()) and torch.equal(got["da"][0], clean["da"][0]) and torch.equal(got["db"][2], clean["db"][2])
 
 
+def test_large_factors_keep_their_value():
+    """A finite u past the operands' largest value stays finite: in fp16 beside another rank's infinity (u =
+    inf, 120001), in bf16 between its largest value and fp32's."""
+    ids = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x, a, b = torch.zeros(1, 16), torch.zeros(1, 2, 16), torch.tensor([[[1.0, -1.0], [-0.5, 0.25]]])
+    x[0, :2] = torch.tensor([1.0, 40000.0])
+    a[0, :, :2] = torch.tensor([[float("inf"), 1.0], [1.0, 3.0]])
+    y, _ = g.lora_forward(None, x.half().cuda(), a.half().cuda(), b.half().cuda(), ids)
+    assert y.tolist() == [[float("inf"), -float("inf")]]
+    x[0, :2] = torch.tensor([2.0 ** 127, 2.0 ** 119])
+    a = torch.zeros(1, 1, 16)
+    a[0, 0, :2] = torch.tensor([1.9921875, 1.5])         # u = 2^127 1.998046875
+    b = torch.tensor([[[2.0 ** -126], [-(2.0 ** -125)]]])
+    t = torch.bfloat16
+    y, _ = g.lora_forward(None, x.to(t).cuda(), a.to(t).cuda(), b.to(t).cuda(), ids)
+    assert y.tolist() == [[4.0, -8.0]]                   # 3.99609375 and -7.9921875 to eight bits
+
+
 def test_fp16_range():
     """fp16: u above 65504 and du below 2^-24 keep their bits (powers of two through the factors)."""
     M, K, N, R = 20, 64, 64, 16
