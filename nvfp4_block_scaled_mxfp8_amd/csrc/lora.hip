@@ -39,6 +39,35 @@ __device__ __forceinline__ void split(float v, uint16_t& hi, uint16_t& lo) {
   const float h = E::up(hi);
   lo = E::down(__builtin_isfinite(h) ? v - h : 0.0f);
 }
+// W's (or X's) elements for the product with lo: infinities and NaN as zeros.  hi times them is already what v
+// times them is; lo, zero or of the other sign, would make a NaN of an infinity.
+template <int TYPE>
+__device__ __forceinline__ v4i finite_only(v4i w) {
+  constexpr uint32_t E = TYPE == MM_BF16 ? 0x7F80u : 0x7C00u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t v = (uint32_t)w[i];
+    if ((v & E) == E) v &= 0xFFFF0000u;
+    if ((v >> 16 & E) == E) v &= 0xFFFFu;
+    w[i] = (int)v;
+  }
+  return w;
+}
+// The largest magnitude of elements, by their bits.
+template <int TYPE>
+struct Top {
+  typedef uint16_t v2u __attribute__((ext_vector_type(2)));
+  v2u m = {0, 0};
+  __device__ __forceinline__ void add(v4i v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(v2u, v[i] & 0x7FFF7FFF));
+  }
+  __device__ __forceinline__ bool not_finite() const {
+    constexpr uint16_t E = TYPE == MM_BF16 ? 0x7F80 : 0x7C00;
+    return m.x >= E || m.y >= E;
+  }
+};
+__device__ __forceinline__ int any_nan(v4f c) { return (int)__builtin_isunordered(c[0], c[1]) | (int)__builtin_isunordered(c[2], c[3]); }
 // A power of two that brings a largest magnitude m to [2^14, 2^15) (fp16 operands: hi then never
 // overflows and lo resolves 2^-39 of m), 1 where m is zero or not finite.  Exponents are kept where
 // the factor and its inverse are normal numbers.
@@ -306,6 +335,17 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraExpand p) {
       for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int f = 0; f < 4; ++f) acc[f] = E::mma16(wf[f][t], u[t], acc[f]);
+      if (__any(any_nan(acc[0]) | any_nan(acc[1]) | any_nan(acc[2]) | any_nan(acc[3]))) {      // again, lo times finite W
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          acc[f] = v4f{0, 0, 0, 0};
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            if (j >= 2) wf[f][t] = finite_only<TYPE>(wf[f][t]);
+            acc[f] = E::mma16(wf[f][t], u[t], acc[f]);
+          }
+        }
+      }
     }
     // mul is its row's: the accumulator's column is the lane's own position q
     if (16 * b + q >= valid) continue;
@@ -381,7 +421,9 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(LoraOuter p, int chunk_
   __shared__ __align__(1024) uint16_t sx[OP * OC];
   __shared__ __align__(1024) uint16_t sv[2][OP * VW];             // hi, lo
   __shared__ float s_top[4];
+  __shared__ int s_odd[2];                                        // a stage's X holds what is not finite
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (tid < 2) s_odd[tid] = 0;
   const RowTile rt = find_row_tile(p.rows.count, p.rows.L, (uint32_t)p.rows.M, chunk_rows, 1, false, blockIdx.x, lane);
   if (rt.g < 0) return;
   const int64_t pos0 = (int64_t)rt.row0 + (int64_t)rt.t * chunk_rows;
@@ -436,12 +478,18 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(LoraOuter p, int chunk_
     return v4i{lo.x, lo.y, hi.x, hi.y};
   };
   auto stage = [&](int b, v4i* x) {
+    const int odd = b / OP & 1;
     __syncthreads();
+    if (tid == 0) s_odd[odd ^ 1] = 0;                             // the next stage's
+    Top<TYPE> top;
 #pragma unroll
     for (int i = 0; i < OP / 8; ++i) {
       const int r = xr + 8 * i;
-      *reinterpret_cast<v4i*>(sx + r * OC + (((xc >> 3) ^ ((r & 3) << 2)) << 3)) = fix8<VEC>(x[i], xcols, p.C < 8);
+      const v4i v = fix8<VEC>(x[i], xcols, p.C < 8);
+      top.add(v);
+      *reinterpret_cast<v4i*>(sx + r * OC + (((xc >> 3) ^ ((r & 3) << 2)) << 3)) = v;
     }
+    if (top.not_finite()) s_odd[odd] = 1;
     if (TYPE == MM_FP16) {
       for (int i = tid; i < OP * VW; i += 256) {
         const int m = i / VW, r = i % VW;
@@ -459,6 +507,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(LoraOuter p, int chunk_
       rows_of(b + 3 * OP);
     }
     __syncthreads();
+    const bool clean = __builtin_amdgcn_readfirstlane(s_odd[odd]) != 0;
 #pragma unroll
     for (int ks = 0; ks < OP / 32; ++ks) {
       const int row = 32 * ks + 8 * j + r4;
@@ -469,13 +518,18 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(LoraOuter p, int chunk_
         xf[f] = tr(sx0 + row * (OC * 2) + chunk * 16 + (i16 & 1) * 8, 4 * OC * 2);
       }
 #pragma unroll
-      for (int t = 0; t < RT; ++t)
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && clean) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+          for (int f = 0; f < 4; ++f) xf[f] = finite_only<TYPE>(xf[f]);
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
           const v4i vf = tr(sv0 + h * (OP * VW * 2) + row * (VW * 2) + t * 32 + (i16 & 3) * 8, 4 * VW * 2);
 #pragma unroll
           for (int f = 0; f < 4; ++f) acc[t][f] = E::mma16(vf, xf[f], acc[t][f]);
         }
+      }
     }
   };
   for (int b = 0; b < valid; b += 2 * OP) {

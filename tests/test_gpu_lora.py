@@ -185,6 +185,53 @@ def test_nan_and_infinity_stay_where_they_belong():
     assert bool(got["da"][1].isnan().all()) and torch.equal(got["da"][0], clean["da"][0]) and torch.equal(got["db"][2], clean["db"][2])
 
 
+def _elementwise(d):
+    """y, dx, da, db by the formulas, every product written out in 64 bits (an infinity times zero is NaN)."""
+    x, a, b, dy, s = (d[k].double() for k in ("x", "a", "b", "dy", "scales"))
+    out = {"y": d["base"].double().clone(), "dx": torch.zeros_like(x), "da": torch.zeros_like(a), "db": torch.zeros_like(b)}
+    for l in range(a.shape[0]):
+        m = (d["ids"] == l).nonzero().flatten()
+        if m.numel() == 0:
+            continue
+        u = (x[m][:, None] * a[l]).sum(2)
+        du = s[l] * (dy[m][:, :, None] * b[l]).sum(1)
+        out["y"][m] += s[l] * (u[:, None] * b[l]).sum(2)
+        out["dx"][m] = (du[:, :, None] * a[l]).sum(1)
+        out["da"][l] = (du[:, :, None] * x[m][:, None]).sum(0)
+        out["db"][l] = s[l] * (dy[m][:, :, None] * u[:, None]).sum(0)
+    return out
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("R", [4, 24, 100])
+@pytest.mark.parametrize("where", ["b", "a", "x", "dy"])
+@pytest.mark.parametrize("whole", [True, False])
+def test_infinities_as_in_the_formula(whole, where, R, dt):
+    """An infinity in a factor gives infinities of the formula's sign, and NaN where the formula has one: the
+    rank-sized factors' second 16-bit value (zero, or of the other sign) does not turn them into NaN.
+    Whole numbers: every finite result is exact."""
+    M, K, N, L = 140, 24, 40, 2
+    make = (lambda s, i, lo: ints(s, DTYPES[dt], i, lo, 1)) if whole else (lambda s, i, lo: randn(s, DTYPES[dt], i))
+    d = {"base": make((M, N), 1, -1), "x": make((M, K), 2, -1), "a": make((L, R, K), 3, -1), "b": make((L, N, R), 4, -1),
+         "dy": make((M, N), 5, -1), "ids": (torch.arange(M) % 3 - 1).to(torch.int32), "scales": torch.tensor([1.0, 2.0])}
+    inf = float("inf")
+    if where == "b":
+        d["b"][0, 3, 1], d["b"][1, N - 1, R - 1] = inf, -inf
+    elif where == "a":
+        d["a"][0, 2, 5], d["a"][1, R - 1, K - 1] = -inf, inf
+    elif where == "x":
+        d["x"][1, 4], d["x"][M - 1, K - 1] = inf, -inf
+    else:
+        d["dy"][4, 7], d["dy"][M - 1, N - 1] = -inf, inf
+    ref, got = _elementwise(d), _run(d)
+    for k, want in ref.items():
+        v = got[k].cpu().double()
+        assert torch.equal(v.isnan(), want.isnan()), (k, int(v.isnan().sum()), int(want.isnan().sum()))
+        assert torch.equal(v == inf, want == inf) and torch.equal(v == -inf, want == -inf), k
+        if whole:
+            assert torch.equal(v[want.isfinite()], want[want.isfinite()].to(DTYPES[dt]).double()), k
+
+
 def test_large_factors_keep_their_value():
     """A finite u past the operands' largest value stays finite: in fp16 beside another rank's infinity (u =
     inf, 120001), in bf16 between its largest value and fp32's."""
