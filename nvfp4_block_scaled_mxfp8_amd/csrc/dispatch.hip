@@ -19,7 +19,7 @@ namespace gmlp {
 //   placing pass: a group's first position (the slots of lower groups, and of this group in earlier
 //   blocks and waves), then one walk that places every slot.  Without a counting pass (no ws) every
 //   block counts all slots by itself.
-constexpr int OT = 1024, OW = OT / 64;
+constexpr int OT = sizes::kOrderThreads, OW = OT / 64;
 
 __device__ __forceinline__ uint64_t same_id_lanes(int id, int bits, bool in) {
   uint64_t m = __ballot(in);
@@ -151,21 +151,12 @@ __global__ __launch_bounds__(OT) void order_kernel(const int32_t* __restrict__ i
     for (int64_t i = s_total + (int64_t)blockIdx.x * OT + tid; i < n; i += (int64_t)gridDim.x * OT) order[i] = -1;
 }
 
-static int64_t order_chunk(int64_t n) {
-  const int64_t per = (n + kOrderMaxBlocks - 1) / kOrderMaxBlocks;
-  return std::max<int64_t>((per + OT - 1) / OT, 1) * OT;
-}
-static int order_grid(int64_t n) { return (int)std::max<int64_t>((n + order_chunk(n) - 1) / order_chunk(n), 1); }
-// Up to here every block counts all slots by itself, past it a pass of its own does.  Measured (us in a
-// graph, own pass / by itself): 64 groups: 2048 slots 6.0 / 4.6, 6144 6.2 / 5.2, 16384 6.3 / 6.0, 24576
-// 6.5 / 6.8, 65536 6.5 / 10.7; 1024 groups: 2048 slots 8.5 / 7.5, 16384 10.2 / 8.9, 65536 14.5 / 13.6.
-constexpr int64_t kOrderAlone = 16384;
-int order_blocks(int64_t n) { return n > kOrderAlone ? order_grid(n) : 1; }
+int order_blocks(int64_t n) { return sizes::order_blocks(n); }
 
 hipError_t launch_group_order(const int32_t* ids, int64_t n, int G, bool rest, int32_t* count, int32_t* rows,
                               int32_t* order, int32_t* ws, hipStream_t s) {
-  const int nb = order_grid(n);
-  const int64_t chunk = order_chunk(n);
+  const int nb = sizes::order_grid(n);
+  const int64_t chunk = sizes::order_chunk(n);
   int bits = 0;
   while ((1 << bits) < G) ++bits;
   if (order_blocks(n) == 1) ws = nullptr;

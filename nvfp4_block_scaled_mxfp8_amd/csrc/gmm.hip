@@ -532,7 +532,7 @@ __global__ __launch_bounds__(256) void gmm_sum_kernel(MmArgs p) {
 // tiles, so that those resident together share A rows and B columns in its L2, and from round to
 // round a workgroup moves on by one within its XCD, as tiles of one group's full and last row
 // blocks alternate.
-constexpr int kTableWords = 8;
+using sizes::kTableWords;
 constexpr int kTableSort = 1024;       // groups that one workgroup sorts; more keep their order
 
 // n / d for any n < 2^32: the product with floor((2^32 - 1) / d) is at most two below.
@@ -923,16 +923,6 @@ __global__ __launch_bounds__(512, 2) void gmm_stream_kernel(StreamArgs args) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no DMA may land after the LDS is given away
 }
 
-// The most row tiles of height h that any splits of M rows give: at most min(G + 1, M) runs of rows
-// (the groups and the rows behind them), each with less than one tile of padding.
-static int64_t row_tiles_bound(const MmArgs& p, int h) {
-  return (p.M + (h - 1) * std::min<int64_t>((int64_t)p.G + 1, p.M)) / h;
-}
-// Row tiles of height h when the M rows are spread evenly.
-static int64_t row_tiles_even(int64_t M, int G, int h) {
-  const int64_t used = std::min<int64_t>(G, std::max<int64_t>(M, 1));
-  return used * ((M / used + h - 1) / h);
-}
 static int cu_count() {
   int dev = 0, n = 0;
   if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 8)
@@ -940,19 +930,11 @@ static int cu_count() {
   return n;
 }
 
-// Parts of the contraction: with fewer tiles than CUs and eight stages or more, as many as fill the
-// device twice, none shorter than four stages (one part where there is no tile at all).
-int grouped_matmul_parts(int layout, int G, int64_t M, int64_t n, int64_t k) {
-  const int64_t tn = (n + 127) / 128, tk = (k + 127) / 128;
-  const int64_t tiles = layout == MM_WGRAD ? G * tn * tk : row_tiles_even(M, G, 128) * tn;
-  const int64_t stages = ((layout == MM_WGRAD ? M / std::min<int64_t>(G, std::max<int64_t>(M, 1)) : k) + 63) / 64;
-  if (tiles == 0 || tiles >= 256 || stages < 8) return 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, stages / 4, 16}));
-}
+int grouped_matmul_parts(int layout, int G, int64_t M, int64_t n, int64_t k) { return sizes::parts(layout == MM_WGRAD, G, M, n, k); }
 int64_t grouped_matmul_part_floats(int layout, int G, int64_t M, int64_t n, int64_t k) {
-  const int parts = grouped_matmul_parts(layout, G, M, n, k);
-  return parts > 1 ? parts * (layout == MM_WGRAD ? G * n * k : M * n) : 0;
+  return sizes::part_floats(layout == MM_WGRAD, G, M, n, k);
 }
+size_t grouped_matmul_table_bytes(int G, int64_t M) { return sizes::table_bytes(G, M); }
 
 // Non-temporal loads of the weights of groups with one row tile, where the weights pass twice the
 // last-level cache, so that none is still there from the call before.  Measured (us, forward, plain /
@@ -964,15 +946,7 @@ static bool weights_once(const MmArgs& p) { return 2.0 * std::min<int64_t>(p.G, 
 
 template <int TYPE, int LAYOUT, int OUT, bool VEC>
 static hipError_t run_ring(const MmArgs& p, hipStream_t s) {
-  constexpr int T = 128;
-  int64_t grid;
-  if (LAYOUT == MM_WGRAD) {
-    const int64_t tpg = (int64_t)((p.n + T - 1) / T) * ((p.k + T - 1) / T);
-    grid = tpg >= 64 ? 8 * ((tpg + 7) / 8) * p.G : tpg * p.G;
-  } else {
-    grid = 8 * ((row_tiles_bound(p, T) * ((p.n + T - 1) / T) + 7) / 8);
-  }
-  const FoldedGrid f = fold_grid(std::max<int64_t>(grid, 8), 256);
+  const FoldedGrid f = fold_grid(sizes::ring_blocks(LAYOUT == MM_WGRAD, p.G, p.M, p.n, p.k), 256);
   const bool once = VEC && LAYOUT != MM_WGRAD && weights_once(p);
   auto* k = once ? gmm_ring_kernel<TYPE, LAYOUT, OUT, VEC, VEC && LAYOUT != MM_WGRAD> : gmm_ring_kernel<TYPE, LAYOUT, OUT, VEC, false>;
   hipLaunchKernelGGL(k, dim3(f.x, OUT == MM_OUT_PART ? p.parts : 1, f.y), dim3(256), 0, s, p);
@@ -982,7 +956,7 @@ template <int TYPE, int LAYOUT, int OUT, bool VEC>
 static hipError_t run_tiles(const MmArgs& p, hipStream_t s) {
   if (p.parts <= 1) return run_ring<TYPE, LAYOUT, OUT, VEC>(p, s);
   MmArgs q = p;
-  q.part_stride = (LAYOUT == MM_WGRAD ? (int64_t)p.G * p.n : p.M) * (LAYOUT == MM_WGRAD ? p.k : p.n);
+  q.part_stride = sizes::part_stride(LAYOUT == MM_WGRAD, p.G, p.M, p.n, p.k);
   q.zero_rest = 0;
   if (hipError_t e = run_ring<TYPE, LAYOUT, MM_OUT_PART, VEC>(q, s)) return e;
   q.zero_rest = p.zero_rest;
@@ -1016,13 +990,8 @@ static hipError_t run_stream(const MmArgs& p, hipStream_t s) {
 static bool use_stream(const MmArgs& p) {
   const int64_t tn = (p.n + 255) / 256, tk = (p.k + 255) / 256;
   if (p.layout == MM_WGRAD) return p.G * tn * tk >= 256;
-  return p.M >= (int64_t)160 * p.G && row_tiles_even(p.M, p.G, 256) * tn >= 256;
+  return p.M >= (int64_t)160 * p.G && sizes::row_tiles_even(p.M, p.G, 256) * tn >= 256;
 }
-size_t grouped_matmul_table_bytes(int G, int64_t M) {
-  const int64_t rows = (M + 255 * std::min<int64_t>((int64_t)G + 1, M)) / 256;
-  return 4 * (8 + (size_t)std::max<int64_t>(rows, G) * kTableWords);
-}
-
 // 16-byte loads and stores throughout.
 static bool vec_ok(const MmArgs& p) {
   const uintptr_t addr = reinterpret_cast<uintptr_t>(p.a) | reinterpret_cast<uintptr_t>(p.b) | reinterpret_cast<uintptr_t>(p.c);

@@ -202,7 +202,6 @@ hipError_t launch_grouped_matmul(const MmArgs& a, hipStream_t s);
 //   order [n]  the slot at each position, -1 behind the last (may be null)
 //   count [G]  slots per group
 constexpr int kOrderMaxGroups = 1024;
-constexpr int kOrderMaxBlocks = 256;
 int order_blocks(int64_t n);          // of the counting pass: 1: none and no workspace; else order_blocks(n) x G int32
 // rest: ids outside [0, G - 1) count as group G - 1 (so every slot has a position).
 hipError_t launch_group_order(const int32_t* ids, int64_t n, int G, bool rest, int32_t* count, int32_t* rows,

@@ -224,7 +224,7 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraShrink p) {
   }
 }
 
-static int64_t tiles_bound(int64_t M, int groups, int64_t h) { return (M + (h - 1) * std::min<int64_t>(groups, M)) / h; }
+using sizes::tiles_bound;
 
 template <int TYPE, bool VEC, int RB, int RT, int NW>
 static hipError_t run_shrink(const LoraShrink& p, hipStream_t s) {
@@ -412,7 +412,7 @@ hipError_t launch_lora_expand(const LoraExpand& p, hipStream_t s) {
 // one adapter by 256 columns, 64 positions a stage.  Both factors are contracted over positions, so
 // both are read from LDS by ds_read_b64_tr_b16 (as the ring kernel's transposed units).  The chunks
 // of an adapter are joined in order by lora_outer_sum_kernel.  16384 rows of 4096, rank 16: 43 us and 5.
-constexpr int OP = 64, OC = 256;
+constexpr int OP = sizes::kOuterRows, OC = sizes::kOuterCols;
 
 template <int TYPE, bool VEC, int RT>
 __global__ __launch_bounds__(256) void lora_outer_kernel(LoraOuter p, int chunk_rows) {
@@ -604,18 +604,10 @@ __global__ __launch_bounds__(256) void lora_outer_sum_kernel(LoraOuter p, int ch
   }
 }
 
-// Positions of a chunk: about 512 workgroups over the tensor, at least 256 (the chunks' results are
-// written and read once more) and at most 2048.
-static int outer_rows(int64_t M, int64_t C) {
-  const int64_t r = M * ((C + OC - 1) / OC) / 512;
-  return (int)(std::min<int64_t>(std::max<int64_t>(r, 256), 2048) + OP - 1) / OP * OP;
-}
-int64_t lora_outer_part_floats(int64_t M, int64_t C, int R, int L) {
-  return tiles_bound(M, L, outer_rows(M, C)) * R * C;
-}
+int64_t lora_outer_part_floats(int64_t M, int64_t C, int R, int L) { return sizes::outer_part_floats(M, C, R, L); }
 template <int TYPE, bool VEC>
 static hipError_t run_outer(const LoraOuter& p, hipStream_t s) {
-  const int rows = outer_rows(p.rows.M, p.C);
+  const int rows = sizes::outer_rows(p.rows.M, p.C);
   const dim3 grid((uint32_t)tiles_bound(p.rows.M, p.rows.L, rows), (uint32_t)((p.C + OC - 1) / OC));
   if (p.R <= 16) hipLaunchKernelGGL((lora_outer_kernel<TYPE, VEC, 1>), grid, dim3(256), 0, s, p, rows);
   else if (p.R <= 32) hipLaunchKernelGGL((lora_outer_kernel<TYPE, VEC, 2>), grid, dim3(256), 0, s, p, rows);
