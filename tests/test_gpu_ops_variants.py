@@ -44,6 +44,31 @@ def test_weights_that_are_loaded_once(dt):
     _grouped(splits, sum(splits) + 11, 2048, 2304, DTYPES[dt], wgrad=False)
 
 
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_weights_that_are_loaded_once_in_parts(dt):
+    """One group's weights of 525 MB and few rows: a contraction cut into parts, non-temporal.  Every 41st column
+    and the last ones."""
+    print(f"weights once in parts {dt}", flush=True)
+    M, N, K = 50, 32000, 8200
+    t = DTYPES[dt]
+    w = torch.empty((1, N, K), dtype=t, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(2))
+    x, m = randn((M, K), t, 1), torch.tensor([47], dtype=torch.int32, device="cuda")
+    cols = list(range(0, N, 41)) + list(range(N - 9, N))
+    y = g.grouped_matmul_forward(x.cuda(), w, m)
+    assert_close(y[:47, cols], *product(x[:47], w[0, cols].cpu().t()), K, "y")
+    dx = g.grouped_matmul_dgrad(x.cuda(), w.view(1, K, N), m)          # the same memory as [K, N]
+    assert_close(dx[:47, cols], *product(x[:47], w.view(K, N)[:, cols].cpu()), K, "dx")
+    assert not y[47:].any() and not dx[47:].any()
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("N,K", [(33, 17), (40, 24), (129, 264), (5, 700)])
+def test_long_groups_of_small_weight_gradients(N, K, dt):
+    """Few tiles and many rows: weight gradients cut into parts, aligned and not."""
+    print(f"parts of wgrad {N} x {K} {dt}", flush=True)
+    _grouped([1200, 3, 0, 2000], 3210, N, K, DTYPES[dt])
+
+
 @pytest.mark.parametrize("rest", [0, 70])
 @pytest.mark.parametrize("G", [1023, 1024, 1100])
 def test_more_groups_than_the_table_sorts(G, rest):
@@ -113,6 +138,22 @@ def test_adapters_by_large_tiles(name, dt):
         _close(got[k], ref[k], f"{name} {dt} {k}")
     none = d["ids"] < 0
     assert torch.equal(got["y"].cpu()[none], d["base"][none]) and not got["dx"].cpu()[none].any()
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("R", [12, 16, 28, 32, 60, 64, 100, 128])
+@pytest.mark.parametrize("M,K,N", [(90, 72, 136), (90, 71, 135), (5000, 24, 2000), (5000, 23, 1999), (5000, 24, 6000),
+                                   (5000, 23, 5999), (17000, 72, 64), (17000, 71, 63)])
+def test_adapters_of_every_tile_and_alignment(M, K, N, R, dt):
+    """Every kernel of the forward: tiles of 16 and 32 positions with 8 and 16 waves, of 16, 64 and 128, each
+    group of ranks, rows and weights of whole 16-byte chunks or not."""
+    print(f"adapters M={M} K={K} N={N} R={R} {dt}", flush=True)
+    t, L = DTYPES[dt], 3
+    d = {"base": randn((M, N), t, 1), "x": randn((M, K), t, 2), "a": randn((L, R, K), t, 3, K ** -0.5), "b": randn((L, N, R), t, 4),
+         "dy": torch.zeros((M, N), dtype=t), "ids": torch.from_numpy(np_ids(M, L, 6, 0.1)), "scales": torch.tensor([0.5, 1.0, 1.75])}
+    v = {k: e.cuda() for k, e in d.items()}
+    y, _ = g.lora_forward(v["base"], v["x"], v["a"], v["b"], v["ids"], v["scales"])
+    _close(y, _reference(d)["y"], f"{R} {dt}")
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))
