@@ -230,7 +230,7 @@ __device__ __forceinline__ Place place_of(int chunks, int64_t T, int64_t block, 
 static int64_t place_blocks(int chunks, int64_t T) {
   return chunks >= MT ? T * ((chunks + MT - 1) / MT) : (T + MT / chunks - 1) / (MT / chunks);
 }
-__device__ __forceinline__ int64_t block_number() { return blockIdx.x + (int64_t)blockIdx.y * gridDim.x; }
+__device__ __forceinline__ int64_t block_number(const MoveArgs& p) { return blockIdx.x + (int64_t)blockIdx.y * p.row_blocks; }
 
 constexpr int kRestBlocks = 64;      // blocks that clear the rows behind the last used one
 
@@ -238,7 +238,7 @@ template <int TYPE, int V, bool SCALE, bool NT>
 __global__ __launch_bounds__(MT) void dispatch_kernel(MoveArgs p, int chunks, int64_t blocks) {
   using E = Elem<TYPE>;
   uint16_t* dst = static_cast<uint16_t*>(p.dst);
-  const int64_t M = p.T * p.k, block = block_number();
+  const int64_t M = p.T * p.k, block = block_number(p);
   if (block >= blocks) {
     if (!p.zero_rest || block >= blocks + kRestBlocks) return;
     long long used = 0;
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(MT) void combine_kernel(MoveArgs p, int chunks) {
   using E = Elem<TYPE>;
   const uint16_t* src = static_cast<const uint16_t*>(p.src);
   const int64_t M = p.T * p.k;
-  const Place w = place_of(chunks, p.T, block_number(), threadIdx.x);
+  const Place w = place_of(chunks, p.T, block_number(p), threadIdx.x);
   if (w.t < 0) return;
   const int at = chunk_start<V>(w.c, p.H);
   float acc[V] = {};
@@ -307,7 +307,7 @@ __global__ __launch_bounds__(MT) void combine_dprobs_kernel(MoveArgs p, int chun
   using E = Elem<TYPE>;
   __shared__ float red[MT / 64][8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t t = block_number(), M = p.T * p.k;
+  const int64_t t = block_number(p), M = p.T * p.k;
   if (t >= p.T) return;
   const uint16_t* dy = static_cast<const uint16_t*>(p.src) + t * p.ld_src;
   const uint16_t* v = static_cast<const uint16_t*>(p.src2);
@@ -349,8 +349,9 @@ __global__ __launch_bounds__(MT) void combine_dprobs_kernel(MoveArgs p, int chun
   }
 }
 
-static dim3 grid_of(int64_t blocks) {
+static dim3 grid_of(int64_t blocks, MoveArgs& p) {
   const FoldedGrid g = fold_grid(blocks, MT);
+  p.row_blocks = g.x;
   return dim3(g.x, g.y);
 }
 
@@ -358,10 +359,10 @@ static dim3 grid_of(int64_t blocks) {
 static bool past_cache(const MoveArgs& p) { return (double)p.T * p.k * p.H * 2 > 128e6; }
 
 template <int TYPE, int V, bool NT>
-static hipError_t run_dispatch_nt(const MoveArgs& p, hipStream_t s) {
+static hipError_t run_dispatch_nt(MoveArgs p, hipStream_t s) {
   const int chunks = (p.H + V - 1) / V;
   const int64_t blocks = place_blocks(chunks, p.T);
-  const dim3 grid = grid_of(blocks + (p.zero_rest ? kRestBlocks : 0));
+  const dim3 grid = grid_of(blocks + (p.zero_rest ? kRestBlocks : 0), p);
   if (p.probs) hipLaunchKernelGGL((dispatch_kernel<TYPE, V, true, NT>), grid, dim3(MT), 0, s, p, chunks, blocks);
   else hipLaunchKernelGGL((dispatch_kernel<TYPE, V, false, NT>), grid, dim3(MT), 0, s, p, chunks, blocks);
   return hipGetLastError();
@@ -371,9 +372,9 @@ static hipError_t run_dispatch(const MoveArgs& p, hipStream_t s) {
   return V == 8 && past_cache(p) ? run_dispatch_nt<TYPE, V, V == 8>(p, s) : run_dispatch_nt<TYPE, V, false>(p, s);
 }
 template <int TYPE, int V, bool NT>
-static hipError_t run_combine_nt(const MoveArgs& p, hipStream_t s) {
+static hipError_t run_combine_nt(MoveArgs p, hipStream_t s) {
   const int chunks = (p.H + V - 1) / V;
-  const dim3 grid = grid_of(place_blocks(chunks, p.T));
+  const dim3 grid = grid_of(place_blocks(chunks, p.T), p);
   if (p.probs) hipLaunchKernelGGL((combine_kernel<TYPE, V, true, NT>), grid, dim3(MT), 0, s, p, chunks);
   else hipLaunchKernelGGL((combine_kernel<TYPE, V, false, NT>), grid, dim3(MT), 0, s, p, chunks);
   return hipGetLastError();
@@ -383,12 +384,13 @@ static hipError_t run_combine(const MoveArgs& p, hipStream_t s) {
   return V == 8 && past_cache(p) ? run_combine_nt<TYPE, V, V == 8>(p, s) : run_combine_nt<TYPE, V, false>(p, s);
 }
 template <int TYPE, int V>
-static hipError_t run_dprobs(const MoveArgs& p, hipStream_t s) {
+static hipError_t run_dprobs(MoveArgs p, hipStream_t s) {
   const int chunks = (p.H + V - 1) / V;
+  const dim3 grid = grid_of(p.T, p);
   if (V == 8 && past_cache(p))
-    hipLaunchKernelGGL((combine_dprobs_kernel<TYPE, V, V == 8>), grid_of(p.T), dim3(MT), 0, s, p, chunks);
+    hipLaunchKernelGGL((combine_dprobs_kernel<TYPE, V, V == 8>), grid, dim3(MT), 0, s, p, chunks);
   else
-    hipLaunchKernelGGL((combine_dprobs_kernel<TYPE, V, false>), grid_of(p.T), dim3(MT), 0, s, p, chunks);
+    hipLaunchKernelGGL((combine_dprobs_kernel<TYPE, V, false>), grid, dim3(MT), 0, s, p, chunks);
   return hipGetLastError();
 }
 

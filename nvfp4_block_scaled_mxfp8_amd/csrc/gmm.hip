@@ -223,7 +223,7 @@ __global__ __launch_bounds__(256, 2) void gmm_ring_kernel(MmArgs p) {
   constexpr int WM = 64, WN = 64, NA = WM / 32, NB = WN / 32;
   __shared__ __align__(1024) uint8_t lds[(VEC ? 5 : 4) * SLOT];
   const int tid = threadIdx.x, lane = tid & 63, wave = sgpr(tid >> 6);
-  const uint32_t block = blockIdx.x + blockIdx.z * gridDim.x;
+  const uint32_t block = blockIdx.x + blockIdx.z * p.row_blocks;
   if (block == 0 && blockIdx.y == 0 && wave == 0) {
     const uint32_t f = wave_split_flags(p.m_splits, p.G, p.M, lane);
     if (lane == 0) *p.flags = f;
@@ -951,6 +951,7 @@ static hipError_t run_ring(const MmArgs& p, hipStream_t s) {
   auto* k = once ? gmm_ring_kernel<TYPE, LAYOUT, OUT, VEC, VEC && LAYOUT != MM_WGRAD> : gmm_ring_kernel<TYPE, LAYOUT, OUT, VEC, false>;
   hipLaunchKernelGGL(k, dim3(f.x, OUT == MM_OUT_PART ? p.parts : 1, f.y), dim3(256), 0, s, p);
   return hipGetLastError();
+  p.row_blocks = f.x;
 }
 template <int TYPE, int LAYOUT, int OUT, bool VEC>
 static hipError_t run_tiles(const MmArgs& p, hipStream_t s) {

@@ -190,6 +190,7 @@ struct MmArgs {
   int parts;              // grouped_matmul_parts, and its scratch of grouped_matmul_part_floats
   float* part;
   int64_t part_stride;    // set by the launcher
+  uint32_t row_blocks;    // workgroups along x, set by the launcher
 };
 size_t grouped_matmul_table_bytes(int G, int64_t M);
 int grouped_matmul_parts(int layout, int G, int64_t M, int64_t n, int64_t k);
@@ -236,6 +237,7 @@ struct LoraShrink {
   int64_t C;
   const float* scales;      // [L] or null (1)
   LoraFactor out;
+  uint32_t row_blocks;      // workgroups along x, set by the launcher
 };
 hipError_t launch_lora_shrink(const LoraShrink& a, hipStream_t s);
 // Y[row p, c] = base[row p, c] + scale sum_r v[p][r] W_l[c, r]; W [L, C, R]; base null: 0
@@ -292,6 +294,7 @@ struct MoveArgs {
   const int32_t* count;      // [E]: rows of dst in use (for zero_rest)
   int E;
   int zero_rest;
+  uint32_t row_blocks;       // workgroups along x, set by the launcher
 };
 hipError_t launch_dispatch(const MoveArgs& a, hipStream_t s);            // dst[rows[t, j]] = probs src[t]
 hipError_t launch_combine(const MoveArgs& a, hipStream_t s);             // dst[t] = sum_j probs src[rows[t, j]]

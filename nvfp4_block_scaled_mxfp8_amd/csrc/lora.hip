@@ -96,7 +96,7 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraShrink p) {
   __shared__ float s_mul[RB * 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const RowTile rt = find_row_tile(p.rows.count, p.rows.L, (uint32_t)p.rows.M, RB * 16, 1, false,
-                                   blockIdx.x + blockIdx.y * gridDim.x, lane);
+                                   blockIdx.x + blockIdx.y * p.row_blocks, lane);
   if (rt.g < 0) return;
   const int64_t pos0 = (int64_t)rt.row0 + rt.t * (RB * 16);
   const int valid = min((int)(rt.m - rt.t * (RB * 16)), RB * 16);
@@ -230,6 +230,7 @@ template <int TYPE, bool VEC, int RB, int RT, int NW>
 static hipError_t run_shrink(const LoraShrink& p, hipStream_t s) {
   const FoldedGrid grid = fold_grid(tiles_bound(p.rows.M, p.rows.L, 16 * RB), 64 * NW);
   hipLaunchKernelGGL((lora_shrink_kernel<TYPE, VEC, RB, RT, NW>), dim3(grid.x, grid.y), dim3(64 * NW), 0, s, p);
+  p.row_blocks = grid.x;
   return hipGetLastError();
 }
 // 32 positions a tile where those fill the device, 16 waves while one tile a CU is all there is, else 8;

@@ -9,7 +9,8 @@ namespace gmlp {
 
 // A launch of `blocks` workgroups.  A launch's threads along x are counted in 32 bits (2^24 + 5 workgroups of
 // 256 ran as 5, without an error), so more workgroups than that are folded over y: the kernel's block
-// number is x + y gridDim.x, and numbers from `blocks` on have nothing to do.
+// number is blockIdx.x + blockIdx.y x, and numbers from `blocks` on have nothing to do.  x is an argument of
+// the kernels: gridDim would add 256 bytes to what every launch writes for them.
 struct FoldedGrid {
   uint32_t x, y;
 };
