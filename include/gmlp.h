@@ -429,19 +429,20 @@ gmlp_status gmlp_combine_dprobs(const gmlp_move_args* args, hipStream_t stream);
 
 /* Low-rank adapters of many requests at once beside a shared projection (bf16 or fp16): row m takes
  * the adapter l = ids[m] (device int32 [M]; outside [0, L): none)
- *   u[m] = a[l] x[m]                        fp32 [R]
+ *   u[m] = a[l] x[m]                        [R]
  *   y[m] = base[m] + scales[l] b[l] u[m]    rounded once; y = base for a row without an adapter
  * and with dy the gradient for y
- *   du[m] = scales[l] b[l]^T dy[m]          fp32 [R]
+ *   du[m] = scales[l] b[l]^T dy[m]          [R]
  *   dx[m] = dx_add[m] + a[l]^T du[m]        da[l] = sum du[m] x[m]^T     db[l] = scales[l] sum dy[m] u[m]^T
- * with the sums over the adapter's rows (an adapter without rows gets zeros).  u and du stay in
- * fp32; as factors of the matrix products they enter as the sum of two 16-bit values, which keeps
- * at least 16 of their bits.  a [L, R, K], b [L, N, R] with row strides lda, ldb and adapter
+ * with the sums over the adapter's rows (an adapter without rows gets zeros).  u and du are
+ * summed in fp32 and enter the matrix products as the sum of two values of the operands' type, which
+ * keeps at least 16 of their bits (bf16: nothing else is kept of them; fp16: about 22, scaled by a power
+ * of two).  Infinities and NaN come out as these formulas give them.  a [L, R, K], b [L, N, R] with row strides lda, ldb and adapter
  * strides a_stride, b_stride; x [M, K], base, y, dy [M, N], dx, dx_add [M, K] with row strides; the
  * last dimension contiguous everywhere, da, db contiguous; strides in elements.  base and dx_add
  * may be NULL (zeros) or the output itself; other overlaps (ids and scales among them) are not allowed.  scales: device fp32
  * [L], or NULL for 1.  1 <= R <= 128, 1 <= L <= 1023.
- * The forward leaves in ctx the rows' order by adapter and u; the backward of the same M, K, N, R, L
+ * The forward leaves in ctx the rows' order by adapter and u as these factors; the backward of the same M, K, N, R, L
  * reads it (keep it untouched in between).  dx, da, db: NULL where not needed (x is read for da). */
 typedef struct {
   const void* a; int64_t lda; int64_t a_stride;

@@ -66,8 +66,8 @@ def lora_query_sizes(M, K, N, R, L):
 
 @dataclass
 class LoraContext:
-    """What a forward leaves for the backward: the rows' order by adapter and u = a x (fp32), opaque,
-    and the call's sizes and scales."""
+    """What a forward leaves for the backward: the rows' order by adapter and u = a x (the sum of two
+    16-bit values; fp16: in fp32 as well), opaque, and the call's sizes and scales."""
     buf: torch.Tensor
     M: int
     K: int

@@ -32,15 +32,15 @@ namespace gmlp {
 // a contraction tail inside a row (k % 64) is cut per lane in the last stage.
 //
 // Where rows are not multiples of 16 bytes the DMA cannot read them: the units then come through
-// registers into two pairs of slots, 16 bytes per lane from any address, the ragged chunk at a
-// row's end by element.
+// registers into two pairs of slots, 16 bytes per lane from any address; the ragged chunk at a row's
+// end is the row's last eight elements, shifted down (by element in rows of fewer than eight).
 //
 // Few tiles with a long contraction (PART): the contraction is cut over blockIdx.y, each part's
 // fp32 tile goes to scratch, and gmm_sum_kernel adds the parts in order.
 //
-// Measured: 64 rows over 128 experts of 4096 x 7168 471 us, 6.3 TB/s of weights (bound by their
-// read); 6144 rows, Zipf over 64 experts of 2816 x 2048, 176 us, 4.5 TB/s (the large groups' MFMAs
-// beside the small ones' reads); 32768 x 4096 x 1536, forward, 503 us, 820 TFLOP/s (bound by what
+// Measured: 64 rows over 128 experts of 4096 x 7168 470 to 520 us from run to run, 5.7 to 6.3 TB/s of
+// weights (bound by their read); 6144 rows, Zipf over 60 of 64 experts of 2816 x 2048 (752 MB), 174 to 190 us,
+// 4.0 to 4.3 TB/s (the large groups' MFMAs beside the small ones' reads); 32768 x 4096 x 1536, forward, 503 us, 820 TFLOP/s (bound by what
 // 128-wide tiles fetch from L2; the stream's 256-wide ones take 430).  Unaligned rows: 16384 rows,
 // 8 x 4095 x 2047, 730 us (4096 x 2048: 270), bound by the trip through registers.
 constexpr int MM_OUT_PART = 3;
@@ -508,12 +508,16 @@ __global__ __launch_bounds__(256) void gmm_sum_kernel(MmArgs p) {
 // their way while the one before it ends, and its stores drain under the next one's products.
 //
 // At a tile's last stage the slot that held B is not refilled: it takes the tile's results (4 KB per
-// wave, 32 rows of 128 bytes at a time), which are read back as whole rows, and is refilled then; the
-// stores are issued behind those DMAs, so that the next tile's first stage need not wait for them.  Every wave issues the same count of DMAs and stores for every tile (the buffer
-// range check drops what lies outside), which is what the vmcnt bounds count on.
+// wave, 32 rows of 128 bytes at a time), which are read back as whole rows, and is refilled then; 16-bit
+// results are stored behind those DMAs, so that the next tile's first stage need not wait for them.  Every
+// wave issues the same count of DMAs and stores for every tile (the buffer range check drops what lies
+// outside), which is what the vmcnt bounds count on.  fp32 results (WGRAD) are stored piece by piece before
+// the refill, and added to c each of a tile's 32 pieces waits for its old values, and so for the stores and
+// DMAs before them: 8 x 4096 x 1536 of 32768 rows 381 us in 16 bits, 388 in fp32, 444 added; 128 x 4096 x
+// 7168 of 65536 rows 4.50, 5.43 and 9.3 ms.
 //
 // Measured: 32768 x 4096 x 7168 in one group 1.28 PFLOP/s forward, 1.26 dgrad, 1.14 wgrad; 8 experts
-// of 4096 x 1536 three products 1.14 ms (1.08 PFLOP/s); 128 uneven experts of 4096 x 7168 12.3 ms
+// of 4096 x 1536 three products 1.14 to 1.16 ms (1.07 PFLOP/s); 128 uneven experts of 4096 x 7168 12.3 ms
 // (0.94 PFLOP/s, a third of it the 7.5 GB of weight gradients and the ragged tiles).  Counters on the
 // one-group case: the matrix cores busy 66% of the cycles at 1.84 GHz (1.61 PFLOP/s on zeros, where
 // the clock stays up), LDS 26%, bank conflicts 1%, L2 hits 80%.
@@ -945,13 +949,13 @@ size_t grouped_matmul_table_bytes(int G, int64_t M) { return sizes::table_bytes(
 static bool weights_once(const MmArgs& p) { return 2.0 * std::min<int64_t>(p.G, p.M) * p.n * p.k > 512e6; }
 
 template <int TYPE, int LAYOUT, int OUT, bool VEC>
-static hipError_t run_ring(const MmArgs& p, hipStream_t s) {
+static hipError_t run_ring(MmArgs p, hipStream_t s) {
   const FoldedGrid f = fold_grid(sizes::ring_blocks(LAYOUT == MM_WGRAD, p.G, p.M, p.n, p.k), 256);
+  p.row_blocks = f.x;
   const bool once = VEC && LAYOUT != MM_WGRAD && weights_once(p);
   auto* k = once ? gmm_ring_kernel<TYPE, LAYOUT, OUT, VEC, VEC && LAYOUT != MM_WGRAD> : gmm_ring_kernel<TYPE, LAYOUT, OUT, VEC, false>;
   hipLaunchKernelGGL(k, dim3(f.x, OUT == MM_OUT_PART ? p.parts : 1, f.y), dim3(256), 0, s, p);
   return hipGetLastError();
-  p.row_blocks = f.x;
 }
 template <int TYPE, int LAYOUT, int OUT, bool VEC>
 static hipError_t run_tiles(const MmArgs& p, hipStream_t s) {

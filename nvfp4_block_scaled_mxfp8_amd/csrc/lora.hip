@@ -89,6 +89,7 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraShrink p) {
   using E = Elem<TYPE>;
   // A lane has 256 registers with 8 waves and holds two blocks; 128 with 16, whose other waves cover the
   // loads of one.  Blocks of 64 at least where they fit: a row's 128-byte line is then read by one wave.
+  // (Unaligned rows take more registers for their addresses: three of these shapes spill 14 to 38 then.)
   constexpr bool TWO = NW <= 8;
   constexpr int F = RB + RT, SPB = TWO ? (F <= 3 ? 4 : F <= 6 ? 2 : 1) : (F <= 2 ? 8 : F <= 3 ? 4 : 2);
   constexpr int LD = RT * 16 + 4;
@@ -227,15 +228,22 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraShrink p) {
 using sizes::tiles_bound;
 
 template <int TYPE, bool VEC, int RB, int RT, int NW>
-static hipError_t run_shrink(const LoraShrink& p, hipStream_t s) {
+static hipError_t run_shrink(LoraShrink p, hipStream_t s) {
   const FoldedGrid grid = fold_grid(tiles_bound(p.rows.M, p.rows.L, 16 * RB), 64 * NW);
-  hipLaunchKernelGGL((lora_shrink_kernel<TYPE, VEC, RB, RT, NW>), dim3(grid.x, grid.y), dim3(64 * NW), 0, s, p);
   p.row_blocks = grid.x;
+  hipLaunchKernelGGL((lora_shrink_kernel<TYPE, VEC, RB, RT, NW>), dim3(grid.x, grid.y), dim3(64 * NW), 0, s, p);
   return hipGetLastError();
 }
 // 32 positions a tile where those fill the device, 16 waves while one tile a CU is all there is, else 8;
-// 16 positions below.  (Above 64 ranks a wave's registers allow 8.)  Measured (us, whole forward): 6001
-// rows of 7168, rank 64 (194 tiles of 32): 32 positions 100.6 with 16 waves, 102.0 with 8; 16 positions 127.8.
+// 16 positions below.  (Above 64 ranks a wave's registers allow 8.)  Measured (bf16, us, whole forward, rows
+// of 4096 to 4096 / of 7168 to 2048, by 16 positions, by 32 with 16 waves, with 8):
+//   tiles of 32      rank 16                                   rank 64
+//       71      29.2 33.1 33.3 / 30.1 36.2 36.0       47.7 51.5 51.9 / 55.4 61.9 62.0
+//      135      35.8 39.3 40.2 / 35.7 41.1 41.1       58.8 62.4 62.9 / 61.5 67.4 67.5
+//      195      53.6 49.8 49.9 / 51.6 44.4 44.3       86.0 71.0 71.8 / 93.8 68.9 69.1
+//      519       122  119  119 /  119  108  108        185  155  157 /  211  157  158
+// so the sides meet at about 150 tiles, and 16 waves or 8 make 1% at most (fp16, 6001 rows of 7168, rank 64:
+// 100.6 and 102.0).  Rank 128: 65.0 69.6 at 71 tiles, 86.8 90.9 at 135, 145 116 at 195.
 template <int TYPE, bool VEC, int RT>
 static hipError_t shrink_rank(const LoraShrink& p, hipStream_t s) {
   constexpr int NW = RT > 4 ? 8 : 16;
@@ -390,8 +398,14 @@ static hipError_t run_expand_rows(const LoraExpand& p, hipStream_t s) {
 template <int TYPE, bool VEC, bool VECW>
 static hipError_t run_expand(const LoraExpand& p, hipStream_t s) {
   // W is read once per tile: 128 positions where those give three workgroups a CU, 16 where those give
-  // fewer than eight, else 64.  Measured (us, forward and gradients / forward): 16384 rows of 4096, rank
-  // 16, with 32, 64, 128 positions 286 / 289 / 280; 6001 rows of 4096, rank 64, 108 / 101 / 100.
+  // fewer than eight, else 64.  Measured (bf16, us, whole forward, by 16, 64 and 128 positions):
+  //   workgroups of 16 (of 128)   rank 16              rank 64              rank 128
+  //     1136 (240), 4096 wide    22.6 24.4 26.7       41.0 40.0 40.6       66.5 61.5 59.2
+  //     2160 (368)               29.3 29.2 32.2       55.0 47.7 48.9       88.8 65.0 77.4
+  //     4208 (624)               41.7 39.2 41.1       79.3 62.4 54.2        134 90.9 85.1
+  //     8304 (1136)              54.9 51.5 56.1        123 84.2 74.4        218  125  122
+  //    16496 (2160)               118  120  119        246  170  157        443  255  250
+  // and 16384 rows of 4096, rank 16, with gradients 289 by 64 and 280 by 128.
   const int64_t cols = (p.C + 255) / 256;
   if (tiles_bound(p.rows.M, p.rows.L + 1, 16) * cols < 2048) return run_expand_rows<TYPE, VEC, VECW, 1>(p, s);
   if (tiles_bound(p.rows.M, p.rows.L + 1, 128) * cols < 768) return run_expand_rows<TYPE, VEC, VECW, 4>(p, s);

@@ -129,3 +129,22 @@ def test_layer_captured_and_replayed():
             torch.cuda.synchronize()
             assert torch.equal(out, refs[r % 2]), r
     del graph
+
+
+def test_ids_and_probabilities_by_row():
+    """A token's adapter and a slot's probability brought to the slot's row with one indexed write each, dropped
+    slots to a spare entry: as an explicit loop over the slots."""
+    d, experts, request = _inputs(torch.bfloat16)
+    experts[7] = torch.tensor([-1, E, 9])
+    plan = g.dispatch_plan(experts.cuda(), E)
+    ids = torch.full((T * k + 1,), -1, dtype=torch.int32, device="cuda")
+    ids[plan.rows.long()] = request.cuda()[:, None].expand(T, k)
+    probs = torch.zeros(T * k + 1, device="cuda")
+    probs[plan.rows.long()] = d["probs"].cuda()
+    want_ids, want_probs = torch.full((T * k,), -1, dtype=torch.int32), torch.zeros(T * k)
+    rows = plan.rows.cpu()
+    for t in range(T):
+        for j in range(k):
+            if rows[t, j] >= 0:
+                want_ids[rows[t, j]], want_probs[rows[t, j]] = request[t], d["probs"][t, j]
+    assert torch.equal(ids[:-1].cpu(), want_ids) and torch.equal(probs[:-1].cpu(), want_probs)
