@@ -485,6 +485,131 @@ gmlp_status gmlp_lora_query_sizes(int64_t M, int64_t K, int64_t N, int32_t R, in
 gmlp_status gmlp_lora_forward(const gmlp_lora_fwd_args* args, hipStream_t stream);
 gmlp_status gmlp_lora_backward(const gmlp_lora_bwd_args* args, hipStream_t stream);
 
+/* ------------------------------------------------------------------ routing to experts */
+
+/* The experts of T tokens from the router's logits [T, E] (dtype GMLP_BF16, GMLP_FP16 or GMLP_LOGITS_FP32;
+ * row stride ld in elements, the last dimension contiguous), as gmlp_dispatch_plan takes them:
+ *   s = softmax(logits of the row) or 1 / (1 + exp(-logit))
+ *   order: by s + bias (bias: device fp32 [E]), compared as in 64 bits; bias NULL: by the logits
+ *   groups > 1 (E / groups consecutive experts each): a group's value is the sum of its group_best (1 or 2)
+ *     largest s + bias (group_best 1 without a bias: its largest logit); experts of the top_groups groups of
+ *     largest value take part
+ *   experts[t, j] = the j-th in that order, j < k; probs[t, j] = scale s (renormalize: scale s / sum of the row's
+ *     chosen s), fp32
+ * Ties go to the lowest index, NaN ranks above all numbers.  A logit (or s + bias) of -inf masks its expert:
+ * it is never chosen; slots that find none, and all slots of a row without an expert, get expert -1 and
+ * probability 0.  1 <= E <= 1024, 1 <= k <= 64, k <= top_groups E / groups, E a multiple of groups <= 64.
+ * experts and probs [T, k] are contiguous and overlap no input.  No workspace.
+ * The backward writes dlogits [T, E] (the logits' type, every element) from dprobs [T, k] and the forward's
+ * experts (an expert outside [0, E) or one masked by its logit adds nothing); the choice and the bias have no gradient. */
+typedef enum { GMLP_SCORE_SOFTMAX = 0, GMLP_SCORE_SIGMOID = 1 } gmlp_score;
+enum { GMLP_LOGITS_FP32 = 2 };
+typedef struct {
+  int32_t dtype;              /* of the logits */
+  int32_t score;              /* gmlp_score */
+  const void* logits; int64_t ld;
+  int64_t T;
+  int32_t E, k;
+  const float* bias;
+  int32_t groups, top_groups, group_best;
+  int32_t renormalize;
+  float scale;
+  int32_t* experts;
+  float* probs;
+} gmlp_route_args;
+typedef struct {
+  int32_t dtype;
+  int32_t score;
+  const void* logits; int64_t ld;
+  int64_t T;
+  int32_t E, k;
+  const int32_t* experts;
+  const float* dprobs;
+  int32_t renormalize;
+  float scale;
+  void* dlogits; int64_t ld_dlogits;
+} gmlp_route_bwd_args;
+gmlp_status gmlp_route(const gmlp_route_args* args, hipStream_t stream);
+gmlp_status gmlp_route_backward(const gmlp_route_bwd_args* args, hipStream_t stream);
+
+/* ------------------------------------------------------------------ norms around a block */
+
+/* The residual sum behind a block with the norms on both sides of it, rows of H (bf16 or fp16):
+ *   n = branch / sqrt(mean(branch^2) + eps) * branch_weight      (branch_weight NULL: n = branch)
+ *   y = x + scale gate n                                         (branch NULL: y = x, not written)
+ *   h = y / sqrt(mean(y^2) + eps) * weight                       (weight NULL: none)
+ * in fp32, y and h rounded once (h from the unrounded y).  gate: gmlp_gate says which it is, by channel
+ * [H], by token [T] (strides ld_gate) or of every element [T, H] (rows of ld_gate).  weight, branch_weight and
+ * gate are of the rows' type, or fp32 where their *_fp32 is not 0.  y may be x or branch itself with the
+ * same row stride; other overlaps of outputs with inputs are not allowed.  1 <= H <= 32768.
+ * stats: fp32 [2 T], for the backward: the factors 1 / sqrt(..) of branch and of y (written where the norm exists).
+ * Backward, from dy (gradient of y, NULL: zeros) and dh (of h, NULL without weight): dx, dbranch
+ * (row strides), dgate (of the gate's type and layout, contiguous), dweight, dbranch_weight; NULL where not
+ * needed.  Column sums are taken in fp32 in an order that the sizes fix and rounded once. */
+typedef enum { GMLP_GATE_NONE = 0, GMLP_GATE_CHANNEL = 1, GMLP_GATE_TOKEN = 2, GMLP_GATE_FULL = 3 } gmlp_gate;
+typedef struct {
+  int32_t dtype;              /* gmlp_dtype */
+  int32_t gate_kind;          /* gmlp_gate */
+  int32_t weight_fp32, branch_weight_fp32, gate_fp32;
+  float eps, scale;
+  int64_t T, H;
+  const void* x; int64_t ldx;
+  const void* branch; int64_t ldbranch;
+  const void* weight;
+  const void* branch_weight;
+  const void* gate; int64_t ld_gate;
+} gmlp_norm_inputs;
+typedef struct {
+  gmlp_norm_inputs in;
+  void* y; int64_t ldy;
+  void* h; int64_t ldh;
+  float* stats;               /* may be NULL: no backward follows */
+} gmlp_norm_args;
+typedef struct {
+  gmlp_norm_inputs in;
+  const void* dy; int64_t lddy;
+  const void* dh; int64_t lddh;
+  const float* stats;
+  void* dx; int64_t lddx;
+  void* dbranch; int64_t lddbranch;
+  void* dgate;
+  void* dweight;
+  void* dbranch_weight;
+  void* ws; size_t ws_bytes;
+} gmlp_norm_bwd_args;
+gmlp_status gmlp_residual_norm(const gmlp_norm_args* args, hipStream_t stream);
+gmlp_status gmlp_residual_norm_bwd_ws_bytes(int64_t T, int64_t H, size_t* bytes);
+gmlp_status gmlp_residual_norm_backward(const gmlp_norm_bwd_args* args, hipStream_t stream);
+
+/* ------------------------------------------------------------------ grouped products with 4-bit weights */
+
+/* y[r, :] = x[r, :] w[g]^T for the rows of group g by m_splits (as gmlp_grouped_matmul), x [M, K] bf16 or fp16, with
+ * weights of 4 bits: codes [G, N, K / 2] bytes, contiguous, the even element of a pair in the low four bits.
+ *   GMLP_W4_INT     w = (q - zero) s; s [G, N, K / group] of x's type, zero uint8 of the same shape (its values
+ *                   at most 15; NULL: 8); group 32, 64 or 128, K a multiple of it
+ *   GMLP_W4_NVFP4   w = E2M1(q) E4M3(s) / S, blocks of 16 along K (group 16): codes and block scales as gmlp_weight_quantize
+ *                   leaves them in row_data and row_scale, S = fp32(2688 / amax[g]) clipped to FLT_MAX (1 for amax 0); K a multiple of 32
+ * Sums are fp32 on the matrix cores over exact products (a group's integers are summed before its scale), rounded once.
+ * For few rows, as decoding has them; any M runs.  Rows of y behind the last group are zeroed when zero_rest != 0, else left
+ * as they are.  Splits are clamped on the device as everywhere.  y must not overlap what is read.  No workspace. */
+typedef enum { GMLP_W4_INT = 0, GMLP_W4_NVFP4 = 1 } gmlp_w4_kind;
+typedef struct {
+  int32_t dtype;              /* gmlp_dtype of x, y and the integer kind's scales */
+  int32_t kind;               /* gmlp_w4_kind */
+  int32_t group;
+  int32_t zero_rest;
+  const void* x; int64_t ldx;
+  const uint8_t* codes;
+  const void* scales;
+  const uint8_t* zeros;
+  const float* amax;          /* NVFP4: [G] */
+  void* y; int64_t ldy;
+  const int32_t* m_splits;
+  int32_t G;
+  int64_t M, N, K;
+} gmlp_w4_args;
+gmlp_status gmlp_grouped_matmul_w4(const gmlp_w4_args* args, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -716,3 +716,8 @@ from .expert_dispatch import (CombineFunction, DispatchFunction, DispatchPlan, M
                        dispatch_plan)
 from .adapters import (LoraBwdArgs, LoraContext, LoraFunction, LoraFwdArgs, LoraSizes, LoraWeights, lora,  # noqa: E402
                        lora_backward, lora_forward, lora_query_sizes)
+from .routing import RouteArgs, RouteBwdArgs, RouteFunction, route, route_backward, route_forward  # noqa: E402
+from .norms import (GATE_CHANNEL, GATE_FULL, GATE_NONE, GATE_TOKEN, NormArgs, NormBwdArgs, NormInputs,  # noqa: E402
+                    ResidualNormFunction, residual_norm, residual_norm_backward, residual_norm_forward, rms_norm,
+                    rms_norm_backward, rms_norm_forward)
+from .weights4 import W4_INT, W4_NVFP4, Int4Weights, W4Args, grouped_matmul_w4  # noqa: E402

@@ -1,0 +1,372 @@
+// Routing to experts: each token's k experts and their weights from the router's logits, and the gradient
+// for the logits.  Bound by memory (the logits once, 8 k bytes out) or, in a decode step, by the launch.
+//
+// A row of logits belongs to LPR lanes of one wave, V = J W values each in registers (W to a 16-byte load,
+// element (j LPR + lane) W + i), so nothing but a row's own lanes meets and no barrier is needed.
+#include "block_ops.h"
+#include "block_sizes.h"
+#include "mm_common.h"
+#include "wave_ops.h"
+
+#include <math.h>
+
+namespace gmlp {
+
+constexpr int RT = 256;      // threads of a workgroup
+
+// ----------------------------------------------------------------------------- logits
+template <int TYPE>
+struct Logit {
+  using T = uint16_t;
+  static constexpr int W = 8;
+  static __device__ __forceinline__ float up(uint16_t v) { return Elem<TYPE>::up(v); }
+  static __device__ __forceinline__ uint16_t down(float f) { return Elem<TYPE>::down(f); }
+};
+template <>
+struct Logit<ROUTE_FP32> {
+  using T = float;
+  static constexpr int W = 4;
+  static __device__ __forceinline__ float up(float v) { return v; }
+  static __device__ __forceinline__ float down(float f) { return f; }
+};
+constexpr float kMasked = -INFINITY;
+
+// The lane's values of a row, kMasked behind the last expert (the hardware takes any alignment).
+template <int TYPE, int LPR, int J>
+__device__ __forceinline__ void load_row(const typename Logit<TYPE>::T* row, int E, int lane, float* l) {
+  using L = Logit<TYPE>;
+  constexpr int W = L::W;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e0 = (j * LPR + lane) * W;
+    typename L::T t[W];
+    if (e0 + W <= E) {
+      __builtin_memcpy(t, row + e0, 16);
+#pragma unroll
+      for (int i = 0; i < W; ++i) l[j * W + i] = L::up(t[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) l[j * W + i] = e0 + i < E ? L::up(row[e0 + i]) : kMasked;
+    }
+  }
+}
+template <int LPR, int W>
+__device__ __forceinline__ int expert_of(int v, int lane) { return (v / W * LPR + lane) * W + v % W; }
+
+// ----------------------------------------------------------------------------- order
+// Keys that compare as the numbers do, without a sign: 0 for a masked expert, the largest for NaN.
+__device__ __forceinline__ uint32_t key_of(float f) {
+  if (f != f) return ~0u;
+  const uint32_t u = __float_as_uint(f + 0.0f);               // -0 as +0
+  return f == kMasked ? 0u : (u >> 31) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t key_of(double d) {
+  if (d != d) return ~0ull;
+  const uint64_t u = (uint64_t)__double_as_longlong(d + 0.0);
+  return d == -INFINITY ? 0ull : (u >> 63) ? ~u : u | (1ull << 63);
+}
+__device__ __forceinline__ double value_of(uint64_t key) {
+  return __longlong_as_double((long long)((key >> 63) ? key & ~(1ull << 63) : ~key));
+}
+
+// The row's scores in 64 bits, whose sums with the bias are compared.
+template <int LPR, int V>
+__device__ __forceinline__ void scores64(const float* l, float top, bool sigmoid, double* s) {
+  double sum = 0.0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    s[v] = sigmoid ? 1.0 / (1.0 + exp(-(double)l[v])) : exp((double)l[v] - (double)top);
+    if (l[v] == kMasked) s[v] = 0.0;
+    sum += s[v];
+  }
+  if (sigmoid) return;
+  sum = lanes_sum<LPR>(sum);
+#pragma unroll
+  for (int v = 0; v < V; ++v) s[v] /= sum;
+}
+
+// The k experts of a row in order into sel (LDS, -1: none), in exact order: keys of 64 bits, from the
+// logits or from scores in 64 bits.
+template <int LPR, int J, int W>
+__device__ void select_exact(const RouteArgs& p, const float* l, float top, int lane, uint64_t* keys, uint64_t* group_key,
+                             int32_t* sel) {
+  constexpr int V = J * W;
+  uint64_t key[V], wide[V];
+  const bool need = p.bias || (p.groups > 1 && p.group_best > 1);
+  if (need) {
+    double s[V];
+    scores64<LPR, V>(l, top, p.sigmoid, s);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = expert_of<LPR, W>(v, lane);
+      const double c = p.bias && e < p.E ? s[v] + (double)p.bias[e] : s[v];
+      wide[v] = l[v] == kMasked ? 0ull : key_of(c);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (!need) wide[v] = (uint64_t)key_of(l[v]) << 32;
+    key[v] = p.bias ? wide[v] : (uint64_t)key_of(l[v]) << 32;
+  }
+  if (p.groups > 1) {
+    const int per = p.E / p.groups;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = expert_of<LPR, W>(v, lane);
+      if (e < p.E) keys[e] = wide[v];
+    }
+    wave_fence();
+    for (int g = lane; g < p.groups; g += LPR) {
+      uint64_t a = 0, b = 0;                                   // the two largest
+      for (int i = 0; i < per; ++i) {
+        const uint64_t x = keys[g * per + i];
+        b = x > a ? a : x > b ? x : b;
+        a = x > a ? x : a;
+      }
+      if (p.group_best > 1 && b && a != ~0ull) a = b == ~0ull ? b : key_of(value_of(a) + value_of(b));
+      group_key[g] = a;
+    }
+    wave_fence();
+    for (int g = lane; g < p.groups; g += LPR) {
+      const uint64_t mine = group_key[g];
+      int better = 0;
+      for (int o = 0; o < p.groups; ++o) {
+        const uint64_t x = group_key[o];
+        better += x > mine || (x == mine && o < g);
+      }
+      keys[g] = better < p.top_groups;                         // every element's key has been read
+    }
+    wave_fence();
+    const float inv = 1.0f / (float)per;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = expert_of<LPR, W>(v, lane);
+      if (e < p.E && !keys[(int)(((float)e + 0.5f) * inv)]) key[v] = 0;
+    }
+    wave_fence();
+  }
+  for (int j = 0; j < p.k; ++j) {
+    uint64_t best = 0;
+    uint32_t at = ~0u;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (key[v] > best) {
+        best = key[v];
+        at = (uint32_t)expert_of<LPR, W>(v, lane);
+      }
+    const uint64_t most = lanes_reduce<LPR>(best, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
+    const uint32_t e = lanes_reduce<LPR>(best == most ? at : ~0u, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if ((uint32_t)expert_of<LPR, W>(v, lane) == e) key[v] = 0;
+    if (lane == j % LPR) sel[j] = (int32_t)e;                  // ~0u where nothing is left
+  }
+  wave_fence();
+}
+
+// ----------------------------------------------------------------------------- weights
+// Weights of the row's chosen experts, slot i LPR + lane, before the scale; sum over the chosen where
+// they are renormalized.  The largest exponent is taken out of all of them (sigmoid(l) =
+// exp(min(l, 0)) / (1 + exp(-|l|))), so that scores too small for fp32 still have their ratios.
+template <int LPR, int S>
+__device__ __forceinline__ void slot_weights(const RouteArgs& p, const float* l, const bool* live, float top, float inv_sum,
+                                             float* w) {
+  float most = kMasked;
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    const float x = p.sigmoid ? (l[i] > 0.0f ? 0.0f : l[i]) : l[i];
+    if (live[i]) most = fmaxf(most, x);
+  }
+  most = lanes_max<LPR>(most);
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    if (!p.renormalize) {
+      w[i] = p.sigmoid ? 1.0f / (1.0f + expf(-l[i])) : expf(l[i] - top) * inv_sum;
+    } else if (p.sigmoid) {
+      w[i] = expf((l[i] > 0.0f ? 0.0f : l[i]) - most) / (1.0f + expf(-fabsf(l[i])));
+    } else {
+      w[i] = expf(l[i] - most);
+    }
+    if (!live[i]) w[i] = 0.0f;
+    sum += w[i];
+  }
+  if (!p.renormalize) return;
+  sum = lanes_sum<LPR>(sum);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < S; ++i) w[i] = sum == w[i] ? live[i] : w[i] * inv;      // one expert alone: 1
+}
+// The largest logit of the row (0 without one) and 1 / sum of exp(l - top), of a softmax over all experts.
+template <int LPR, int V>
+__device__ __forceinline__ float row_top(const float* l) {
+  float top = kMasked;
+#pragma unroll
+  for (int v = 0; v < V; ++v) top = fmaxf(top, l[v]);
+  top = lanes_max<LPR>(top);
+  return top == kMasked ? 0.0f : top;
+}
+template <int LPR, int V>
+__device__ __forceinline__ float row_inv_sum(const float* l, float top) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) sum += expf(l[v] - top);
+  sum = lanes_sum<LPR>(sum);
+  return sum == 0.0f ? 0.0f : 1.0f / sum;
+}
+
+// ----------------------------------------------------------------------------- kernels
+template <int TYPE, int LPR, int J>
+__global__ __launch_bounds__(RT) void route_kernel(RouteArgs p) {
+  using L = Logit<TYPE>;
+  constexpr int W = L::W, V = J * W, ROWS = RT / LPR, S = kRouteMaxK / LPR;
+  extern __shared__ uint64_t s_keys[];                         // [ROWS][E] where there are groups
+  __shared__ uint64_t s_group[ROWS][kRouteMaxGroups];
+  __shared__ int32_t s_sel[ROWS][kRouteMaxK];
+  const int lane = threadIdx.x % LPR, r = threadIdx.x / LPR;
+  const int64_t t = ((int64_t)blockIdx.x + (int64_t)blockIdx.y * p.row_blocks) * ROWS + r;
+  const bool in = t < p.T;                                     // the other rows run along, as rows of nothing
+  const typename L::T* row = static_cast<const typename L::T*>(p.logits) + (in ? t : 0) * p.ld;
+  float l[V];
+  load_row<TYPE, LPR, J>(row, in ? p.E : 0, lane, l);
+  const float top = row_top<LPR, V>(l);
+  const float inv_sum = p.sigmoid || p.renormalize ? 0.0f : row_inv_sum<LPR, V>(l, top);
+  select_exact<LPR, J, W>(p, l, top, lane, s_keys + (int64_t)r * p.E, s_group[r], s_sel[r]);
+  int32_t e[S];
+  float x[S], w[S];
+  bool live[S];
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    const int j = i * LPR + lane;
+    e[i] = j < p.k ? s_sel[r][j] : -1;
+    live[i] = e[i] >= 0;
+    x[i] = live[i] ? L::up(row[e[i]]) : 0.0f;
+  }
+  slot_weights<LPR, S>(p, x, live, top, inv_sum, w);
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    const int j = i * LPR + lane;
+    if (in && j < p.k) {
+      p.experts[t * p.k + j] = e[i];
+      p.probs[t * p.k + j] = live[i] ? w[i] * p.scale : 0.0f;
+    }
+  }
+}
+
+// dlogits of a row, all of it: with g_j = scale dprobs_j and w_j the weights before the scale
+//   softmax                 p_e (sum of g_j at e - sum_j g_j w_j)
+//   softmax, renormalized   w_j (g_j - sum g w) at the chosen, 0 elsewhere
+//   sigmoid                 g_j s_j (1 - s_j) at the chosen
+//   sigmoid, renormalized   w_j (g_j - sum g w) (1 - s_j) at the chosen
+// The slots' parts are added to the row in LDS one slot after the other, so that an expert named twice has the
+// sum, in a fixed order.
+template <int TYPE, int LPR, int J>
+__global__ __launch_bounds__(RT) void route_backward_kernel(RouteArgs p) {
+  using L = Logit<TYPE>;
+  constexpr int W = L::W, V = J * W, ROWS = RT / LPR, S = kRouteMaxK / LPR;
+  __shared__ float s_row[ROWS][V * LPR];
+  const int lane = threadIdx.x % LPR, r = threadIdx.x / LPR;
+  const int64_t t = ((int64_t)blockIdx.x + (int64_t)blockIdx.y * p.row_blocks) * ROWS + r;
+  const bool in = t < p.T;
+  const typename L::T* row = static_cast<const typename L::T*>(p.logits) + (in ? t : 0) * p.ld;
+  const bool dense = !p.sigmoid && !p.renormalize;
+  float l[V];
+  float top = 0.0f, inv_sum = 0.0f;
+  if (dense) {
+    load_row<TYPE, LPR, J>(row, in ? p.E : 0, lane, l);
+    top = row_top<LPR, V>(l);
+    inv_sum = row_inv_sum<LPR, V>(l, top);
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int i = 0; i < W; ++i) s_row[r][(j * LPR + lane) * W + i] = 0.0f;
+  int32_t e[S];
+  float x[S], w[S], g[S];
+  bool live[S];
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    const int j = i * LPR + lane;
+    e[i] = in && j < p.k ? p.experts[t * p.k + j] : -1;
+    live[i] = (uint32_t)e[i] < (uint32_t)p.E;
+    x[i] = live[i] ? L::up(row[e[i]]) : 0.0f;
+    live[i] = live[i] && x[i] != kMasked;
+    g[i] = live[i] ? p.scale * p.dprobs[t * p.k + j] : 0.0f;
+  }
+  slot_weights<LPR, S>(p, x, live, top, inv_sum, w);
+  float dot = 0.0f;
+#pragma unroll
+  for (int i = 0; i < S; ++i) dot += live[i] ? g[i] * w[i] : 0.0f;
+  dot = lanes_sum<LPR>(dot);
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    if (p.renormalize) g[i] = w[i] * (g[i] - dot);
+    else if (p.sigmoid) g[i] = g[i] * w[i];
+    if (p.sigmoid) g[i] = g[i] / (1.0f + expf(x[i]));
+  }
+  wave_fence();
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+    for (int j = 0; j < LPR && i * LPR + j < p.k; ++j) {
+      if (lane == j && live[i]) s_row[r][e[i]] += g[i];
+      wave_fence();
+    }
+  if (!in) return;
+  typename L::T* out = static_cast<typename L::T*>(p.dlogits) + t * p.ld_dlogits;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e0 = (j * LPR + lane) * W;
+    if (e0 >= p.E) continue;
+    typename L::T y[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      float d = s_row[r][e0 + i];
+      if (dense) d = l[j * W + i] == kMasked ? 0.0f : expf(l[j * W + i] - top) * inv_sum * (d - dot);
+      y[i] = L::down(d);
+    }
+    if (e0 + W <= p.E) {
+      __builtin_memcpy(out + e0, y, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (e0 + i < p.E) out[e0 + i] = y[i];
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------- launches
+template <int TYPE, int LPR, int J>
+static hipError_t run_route(RouteArgs p, bool backward, hipStream_t s) {
+  constexpr int ROWS = RT / LPR;
+  const FoldedGrid g = fold_grid((p.T + ROWS - 1) / ROWS, RT);
+  p.row_blocks = g.x;
+  if (backward)
+    hipLaunchKernelGGL((route_backward_kernel<TYPE, LPR, J>), dim3(g.x, g.y), dim3(RT), 0, s, p);
+  else
+    hipLaunchKernelGGL((route_kernel<TYPE, LPR, J>), dim3(g.x, g.y), dim3(RT), p.groups > 1 ? sizeof(uint64_t) * ROWS * p.E : 0, s, p);
+  return hipGetLastError();
+}
+// The fewest lanes and loads that hold the row.
+template <int TYPE>
+static hipError_t run_route(const RouteArgs& p, bool backward, hipStream_t s) {
+  constexpr int W = Logit<TYPE>::W;
+  if (p.E <= 16 * W) return run_route<TYPE, 16, 1>(p, backward, s);
+  if (p.E <= 32 * W) return run_route<TYPE, 16, 2>(p, backward, s);
+  if constexpr (W == 4) {
+    if (p.E <= 64 * W) return run_route<TYPE, 16, 4>(p, backward, s);
+    if (p.E <= 128 * W) return run_route<TYPE, 64, 2>(p, backward, s);
+    return run_route<TYPE, 64, 4>(p, backward, s);
+  } else {
+    if (p.E <= 64 * W) return run_route<TYPE, 64, 1>(p, backward, s);
+    return run_route<TYPE, 64, 2>(p, backward, s);
+  }
+}
+static hipError_t run_route(const RouteArgs& p, bool backward, hipStream_t s) {
+  if (p.type == ROUTE_BF16) return run_route<ROUTE_BF16>(p, backward, s);
+  if (p.type == ROUTE_FP16) return run_route<ROUTE_FP16>(p, backward, s);
+  return run_route<ROUTE_FP32>(p, backward, s);
+}
+hipError_t launch_route(const RouteArgs& p, hipStream_t s) { return run_route(p, false, s); }
+hipError_t launch_route_backward(const RouteArgs& p, hipStream_t s) { return run_route(p, true, s); }
+
+}  // namespace gmlp

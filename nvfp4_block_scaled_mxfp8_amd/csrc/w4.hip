@@ -1,0 +1,200 @@
+// Grouped products of few rows with weights of 4 bits: y[r] = x[r] w[g]^T.  Bound by the read of the weights
+// (half a byte an element and the scales), so a weight is read once, decoded in registers and multiplied on the
+// matrix cores.
+//
+// A workgroup has 16 MT rows of one group and 16 NT columns; its waves take chunks of 128 along K in turn
+// and join their sums in LDS.  Of a chunk a lane loads 16 bytes of a column's codes, 32 elements of one
+// row of w: the operand of a product 16 x 16 x 32 holds 8 consecutive elements of a column per lane, the 16
+// columns in the lanes of a row of 16, so each of the four words is one product's operand.  Which elements of K
+// a product takes together is free as long as x's operand has the same:
+//   without scales outside (NVFP4) or with one scale for the chunk: product i has elements 32 q + 8 i + (0..7)
+//     of the chunk in lanes 16 q..16 q + 15, as they were loaded;
+//   groups of 32 and 64: a product may hold one group only, so the four words of the lanes l, l + 16,
+//     l + 32, l + 48 are transposed (four exchanges), and product i has the elements 32 i + 8 q + (0..7).
+// Exactness: NVFP4 weights E2M1 x E4M3 have at most 6 significant bits, and integers q - zero at most 5, exact in
+// both types; an integer group's sum is taken in fp32 before its scale multiplies it.
+#include "block_ops.h"
+#include "block_sizes.h"
+#include "mm_common.h"
+
+namespace gmlp {
+
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
+constexpr int kW4Chunk = sizes::kW4Chunk;
+
+// The four words of lanes l, l + 16, l + 32, l + 48 transposed.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
+  v2u a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+  v2u b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+  const v2u c = __builtin_amdgcn_permlane16_swap(a.x, b.x, false, false);
+  const v2u d = __builtin_amdgcn_permlane16_swap(a.y, b.y, false, false);
+  w[0] = c.x;
+  w[1] = c.y;
+  w[2] = d.x;
+  w[3] = d.y;
+}
+
+// Sums of bf16 rows are kept 2^-12 as large as they are until the end, so that those of the largest rows with
+// integers up to 15 stay in fp32 (fp16 rows are far from its end).
+template <int TYPE>
+constexpr float kDown = TYPE == MM_BF16 ? 0x1p-12f : 1.0f;
+// Eight codes -> eight integers q - zero, times kDown, exact in 16 bits (zero: times -kDown).
+template <int TYPE>
+__device__ __forceinline__ v4i decode_int(uint32_t w, float zero) {
+  const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+  auto pair = [&](int at) {
+    return (int)Elem<TYPE>::down2(fmaf((float)((even >> at) & 255u), kDown<TYPE>, zero), fmaf((float)((odd >> at) & 255u), kDown<TYPE>, zero));
+  };
+  return v4i{pair(0), pair(8), pair(16), pair(24)};
+}
+// Eight E2M1 codes times an E4M3 block scale, exact in 16 bits.
+template <int TYPE, int I>
+__device__ __forceinline__ int decode_fp4x2(uint32_t w, float sc) {
+  const v2f v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, I);
+  return (int)Elem<TYPE>::down2(v.x * sc, v.y * sc);
+}
+template <int TYPE>
+__device__ __forceinline__ v4i decode_fp4(uint32_t w, float sc) {
+  return v4i{decode_fp4x2<TYPE, 0>(w, sc), decode_fp4x2<TYPE, 1>(w, sc), decode_fp4x2<TYPE, 2>(w, sc), decode_fp4x2<TYPE, 3>(w, sc)};
+}
+
+template <int TYPE, int KIND, int GROUP, int MT, int NT>
+__global__ __launch_bounds__(512) void w4_kernel(W4Args p, uint32_t ntn, int64_t blocks) {
+  using E = Elem<TYPE>;
+  constexpr bool INT = KIND == W4_INT, TRANS = INT && GROUP < 128;
+  constexpr int PER = INT ? kW4Chunk / GROUP : 2;              // scales a lane has in a chunk
+  constexpr int SLOTS = MT * NT * 4;
+  extern __shared__ float s_sum[];                             // [waves][SLOTS][64]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int64_t block = (int64_t)blockIdx.x + (int64_t)blockIdx.y * p.row_blocks;
+  if (block >= blocks) return;
+  const RowTile tile = find_row_tile(p.m_splits, p.G, (uint32_t)p.M, 16 * MT, ntn, p.zero_rest, (uint32_t)block, lane);
+  if (tile.g < 0) return;
+  const uint32_t r0 = tile.t / ntn * (16 * MT);
+  const int n0 = (int)(tile.t % ntn) * (16 * NT);
+  const int rows = (int)min(tile.m - r0, 16u * MT);
+  uint16_t* y = static_cast<uint16_t*>(p.y) + (int64_t)(tile.row0 + r0) * p.ldy;
+  if (tile.g == p.G) {
+    for (int i = threadIdx.x; i < rows * 16 * NT; i += blockDim.x)
+      if (n0 + i % (16 * NT) < p.N) y[(int64_t)(i / (16 * NT)) * p.ldy + n0 + i % (16 * NT)] = 0;
+    return;
+  }
+  const int col = lane & 15, q = lane >> 4, N = p.N, K = p.K;
+  const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)(tile.row0 + r0 + col) * p.ldx;
+  const uint8_t* codes[NT];
+  int64_t meta[NT];                                            // the column's first scale
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int64_t n = (int64_t)tile.g * N + min(n0 + 16 * j + col, N - 1);
+    codes[j] = p.codes + n * (K / 2) + 16 * q;
+    meta[j] = n * (K / GROUP);
+  }
+  // NVFP4, bf16 rows: the largest power of two up to 1 / S goes into the block scales, so that products are
+  // no larger than those of the weights themselves (above 2^-60: below it they would leave the exact values)
+  const float global = INT ? 1.0f : nvfp4_global_scale(p.amax[tile.g]);
+  const int down = INT || TYPE != MM_BF16 ? 0 : min(ilogbf(global) + 1, 60);
+  v4f acc[MT][NT] = {};
+  const int chunks = (K + kW4Chunk - 1) / kW4Chunk;
+  for (int c = wave; c < chunks; c += waves) {
+    const int k0 = c * kW4Chunk;
+    const bool have = k0 + 32 * q < K;
+    v4i raw[NT];
+    float sc[NT][PER], zero[NT][PER];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      raw[j] = v4i{0, 0, 0, 0};
+      if (have) raw[j] = *reinterpret_cast<const v4i*>(codes[j] + k0 / 2);
+#pragma unroll
+      for (int s = 0; s < PER; ++s) {
+        const int k = INT ? k0 + s * GROUP : k0 + 32 * q + 16 * s;
+        sc[j][s] = 0.0f;
+        zero[j][s] = -8.0f * kDown<TYPE>;
+        if (k >= K) continue;
+        if (INT) {
+          sc[j][s] = E::up(static_cast<const uint16_t*>(p.scales)[meta[j] + k / GROUP]);
+          if (p.zeros) zero[j][s] = -kDown<TYPE> * (float)p.zeros[meta[j] + k / GROUP];
+        } else {
+          sc[j][s] = ldexpf(__builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(p.scales)[meta[j] + k / GROUP], 0), -down);
+        }
+      }
+    }
+    v4i a[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = k0 + (TRANS ? 32 * i + 8 * q : 32 * q + 8 * i);
+        a[m][i] = v4i{0, 0, 0, 0};
+        if (16 * m + col < rows && k < K) __builtin_memcpy(&a[m][i], x + (int64_t)(16 * m) * p.ldx + k, 16);
+      }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      uint32_t w[4] = {(uint32_t)raw[j].x, (uint32_t)raw[j].y, (uint32_t)raw[j].z, (uint32_t)raw[j].w};
+      if (TRANS) transpose4(w);
+      v4f part[MT] = {};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int s = INT ? i * 32 / GROUP : i / 2;
+        const v4i b = INT ? decode_int<TYPE>(w[i], zero[j][s]) : decode_fp4<TYPE>(w[i], sc[j][s]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (!INT) {
+            acc[m][j] = E::mma16(a[m][i], b, acc[m][j]);
+          } else {
+            part[m] = E::mma16(a[m][i], b, part[m]);
+            if ((i + 1) * 32 % GROUP == 0) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[m][j][r] = fmaf(sc[j][s], part[m][r], acc[m][j][r]);
+              part[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+          }
+        }
+      }
+    }
+  }
+  // the waves' sums, joined in order
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s_sum[(wave * SLOTS + (m * NT + j) * 4 + r) * 64 + lane] = acc[m][j][r];
+  __syncthreads();
+  const float rest = ldexpf(global, -down);
+  for (int s = wave; s < SLOTS; s += waves) {
+    float v = s_sum[s * 64 + lane];
+    for (int o = 1; o < waves; ++o) v += s_sum[(o * SLOTS + s) * 64 + lane];
+    v = INT ? v * (1.0f / kDown<TYPE>) : __fdiv_rn(v, rest);
+    const int m = s / 4 / NT * 16 + 4 * q + s % 4, n = n0 + s / 4 % NT * 16 + col;
+    if (m < rows && n < N) y[(int64_t)m * p.ldy + n] = E::down(v);
+  }
+}
+
+// ----------------------------------------------------------------------------- launches
+template <int TYPE, int KIND, int GROUP, int MT, int NT>
+static hipError_t run_w4(W4Args p, hipStream_t s) {
+  const int waves = 4;
+  const int64_t ntn = (p.N + 16 * NT - 1) / (16 * NT), blocks = sizes::row_tiles_bound(p.M, p.G, 16 * MT) * ntn;
+  const FoldedGrid g = fold_grid(blocks, 64 * waves);
+  p.row_blocks = g.x;
+  hipLaunchKernelGGL((w4_kernel<TYPE, KIND, GROUP, MT, NT>), dim3(g.x, g.y), dim3(64 * waves), (size_t)waves * MT * NT * 4 * 64 * sizeof(float),
+                     s, p, (uint32_t)ntn, blocks);
+  return hipGetLastError();
+}
+template <int TYPE, int KIND, int GROUP>
+static hipError_t run_w4(const W4Args& p, hipStream_t s) {
+  return run_w4<TYPE, KIND, GROUP, 1, 4>(p, s);
+}
+template <int TYPE>
+static hipError_t run_w4(const W4Args& p, hipStream_t s) {
+  if (p.kind == W4_NVFP4) return run_w4<TYPE, W4_NVFP4, 16>(p, s);
+  if (p.group == 32) return run_w4<TYPE, W4_INT, 32>(p, s);
+  if (p.group == 64) return run_w4<TYPE, W4_INT, 64>(p, s);
+  return run_w4<TYPE, W4_INT, 128>(p, s);
+}
+hipError_t launch_w4(const W4Args& p, hipStream_t s) {
+  return p.type == MM_BF16 ? run_w4<MM_BF16>(p, s) : run_w4<MM_FP16>(p, s);
+}
+
+}  // namespace gmlp

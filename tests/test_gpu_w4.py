@@ -1,0 +1,304 @@
+"""grouped_matmul_w4 against products in 64 bits with the weights that the codes stand for."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_block_scaled_mxfp8_amd as g
+from block_util import int4_values, nvfp4_values
+from mm_util import DTYPES, assert_close, randn, spans
+
+pytestmark = pytest.mark.gpu
+
+
+def _int4(G, N, K, group, dtype, seed, zeros=True):
+    gen = torch.Generator().manual_seed(seed)
+    codes = torch.randint(0, 256, (G, N, K // 2), dtype=torch.uint8, generator=gen)
+    scales = ((0.5 + torch.rand((G, N, K // group), generator=gen)) / math.sqrt(K)).to(dtype)
+    z = torch.randint(0, 16, (G, N, K // group), dtype=torch.uint8, generator=gen) if zeros else None
+    return codes, scales, z
+
+
+def _nvfp4(G, N, K, seed):
+    gen = torch.Generator().manual_seed(seed)
+    codes = torch.randint(0, 256, (G, N, K // 2), dtype=torch.uint8, generator=gen)
+    scales = torch.randint(0, 0x7F, (G, N, K // 16), dtype=torch.uint8, generator=gen)
+    amax = (0.01 + torch.rand(G, generator=gen))
+    return codes, scales, amax
+
+
+def _handle(w, kind):
+    dev = [t.cuda() if t is not None else None for t in w]
+    if kind == "nvfp4":
+        return g.QTensor(g.NVFP4_RHT, {"row_data": dev[0].reshape(-1), "row_scale": dev[1].reshape(-1), "amax_pre": dev[2]})
+    return g.Int4Weights(*dev)
+
+
+def _values(w, kind):
+    return nvfp4_values(*w) if kind == "nvfp4" else int4_values(*w)
+
+
+def _make(kind, G, N, K, dtype, seed=1):
+    if kind == "nvfp4":
+        return _nvfp4(G, N, K, seed)
+    return _int4(G, N, K, int(kind), dtype, seed, zeros=seed % 2 == 1)
+
+
+def _check(x, w, kind, splits, what="y", dev_x=None):
+    M, K = x.shape
+    values = _values(w, kind)
+    y = g.grouped_matmul_w4(dev_x if dev_x is not None else x.cuda(), _handle(w, kind), torch.tensor(splits, dtype=torch.int32, device="cuda"))
+    want = torch.zeros((M, values.shape[1]), dtype=torch.float64)
+    mag = torch.zeros_like(want)
+    ranges, used = spans(splits, M)
+    for i, (a, b) in enumerate(ranges):
+        want[a:b] = x[a:b].double() @ values[i].t()
+        mag[a:b] = x[a:b].double().abs() @ values[i].abs().t()
+    # K exact products, a scale for each group of them (NVFP4: the division at the end)
+    assert_close(y, want, mag, 2 * K, what)
+    assert not y[used:].any()
+    return y
+
+
+KINDS = ["32", "64", "128", "nvfp4"]
+
+
+def _k(kind, K):
+    step = 32 if kind == "nvfp4" else int(kind)
+    return max(step, K // step * step)
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("splits,M,N,K", [([1], 1, 1, 32), ([1], 1, 64, 128), ([3, 0, 2], 5, 17, 96), ([1, 16, 17], 34, 65, 160), ([0, 0], 4, 33, 256),
+                                          ([40, 1, 0, 70], 115, 130, 544), ([9], 9, 200, 4096), ([2, 2, 2], 9, 48, 1056), ([64, 65], 129, 96, 384),
+                                          ([5, -3, 900], 12, 40, 640), ([200], 200, 80, 288)])
+def test_products(splits, M, N, K, kind, dt):
+    K = _k(kind, K)
+    print(f"w4 splits={splits} M={M} N={N} K={K} {kind} {dt}", flush=True)
+    dtype = DTYPES[dt]
+    for seed in (1, 2):
+        w = _make(kind, len(splits), N, K, dtype, seed)
+        _check(randn((M, K), dtype, 3), w, kind, splits)
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("kind", KINDS)
+def test_every_element_is_at_its_place(kind, dt):
+    """Rows of the identity read every weight back: exact, one element at a time."""
+    dtype = DTYPES[dt]
+    K = 256
+    w = _make(kind, 1, 50, K, dtype)
+    y = g.grouped_matmul_w4(torch.eye(K, dtype=dtype).cuda(), _handle(w, kind), torch.tensor([K], dtype=torch.int32, device="cuda"))
+    want = _values(w, kind)[0].t()
+    if kind == "nvfp4":
+        # one fp32 division, then the rounding
+        assert_close(y, want, want.abs(), 0, "values")
+    else:
+        assert torch.equal(y.cpu().double(), want.to(dtype).double())
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_every_code_under_every_scale(dt):
+    """All sixteen codes with all zeros, and with all E4M3 scales that are numbers."""
+    dtype = DTYPES[dt]
+    codes = torch.tensor([i | (i << 4) for i in range(16)], dtype=torch.uint8)[None, :, None].expand(16, 16, 16).contiguous()
+    zeros = torch.arange(16, dtype=torch.uint8)[:, None, None].expand(16, 16, 1).contiguous()
+    w = (codes, torch.full((16, 16, 1), 0.5, dtype=dtype), zeros)
+    x = torch.zeros((16, 32), dtype=dtype)
+    x[:, 7] = 2.0
+    y = g.grouped_matmul_w4(x.cuda(), _handle(w, "32"), torch.ones(16, dtype=torch.int32, device="cuda"))
+    assert torch.equal(y.cpu().double(), (torch.arange(16)[None, :] - torch.arange(16)[:, None]).double())
+    codes = torch.tensor([i | (i << 4) for i in range(16)], dtype=torch.uint8)[None, :, None].expand(127, 16, 16).contiguous()
+    scales = torch.arange(127, dtype=torch.uint8)[:, None, None].expand(127, 16, 2).contiguous()
+    w = (codes, scales, torch.full((127,), 2688.0))                   # S = 1
+    x = torch.zeros((127, 32), dtype=dtype)
+    x[:, 19] = 1.0
+    y = g.grouped_matmul_w4(x.cuda(), _handle(w, "nvfp4"), torch.ones(127, dtype=torch.int32, device="cuda"))
+    assert torch.equal(y.cpu().double(), nvfp4_values(*w)[:, :, 19])
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_quantized_weights_of_the_library(dt):
+    """What weight_quantize makes with the NVFP4 recipe, stacked, as it stands."""
+    if dt == "fp16":
+        w16 = randn((3, 128, 256), torch.bfloat16, 5, 0.02)
+    else:
+        w16 = randn((3, 256, 384), torch.bfloat16, 5, 0.02)
+    q = g.weight_quantize(w16.cuda(), g.recipe("nvfp4", 0x1234))
+    E, N, K = w16.shape
+    x = randn((7, K), DTYPES[dt], 6)
+    y = g.grouped_matmul_w4(x.cuda(), q, torch.tensor([2, 4, 1], dtype=torch.int32, device="cuda"))
+    values = nvfp4_values(q.bufs["row_data"].cpu().view(E, N, K // 2), q.bufs["row_scale"].cpu().view(E, N, K // 16), q.bufs["amax_pre"].cpu())
+    # the values are the weights within the format's step: half of 2/6 of the block's largest at most, and 2^-4 of its scale
+    assert float((values - w16.double()).abs().max()) <= 0.25 * float(w16.abs().max())
+    at = torch.tensor([0, 0, 1, 1, 1, 1, 2])
+    want = torch.stack([x[i].double() @ values[at[i]].t() for i in range(7)])
+    mag = torch.stack([x[i].double().abs() @ values[at[i]].abs().t() for i in range(7)])
+    assert_close(y, want, mag, 2 * K, "y")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_strided_rows_and_a_given_output(kind):
+    K = _k(kind, 384)
+    splits, M, N = [3, 20], 30, 70
+    w = _make(kind, 2, N, K, torch.bfloat16)
+    x = randn((M, K), torch.bfloat16, 3)
+    ref = _check(x, w, kind, splits)
+    m = torch.tensor(splits, dtype=torch.int32, device="cuda")
+    for pad, off in ((8, 0), (3, 1), (24, 8)):
+        big = torch.full((M, K + pad), math.nan, dtype=torch.bfloat16, device="cuda")
+        big[:, off:off + K] = x.cuda()
+        out = torch.full((M, N + pad), 7.0, dtype=torch.bfloat16, device="cuda")
+        y = g.grouped_matmul_w4(big[:, off:off + K], _handle(w, kind), m, out=out[:, off:off + N])
+        assert torch.equal(y[:23], ref[:23])
+        rest = out.clone()
+        rest[:23, off:off + N] = 7.0
+        assert bool((rest == 7.0).all())                              # rows behind the groups, columns beside: as they were
+    assert torch.equal(g.grouped_matmul_w4(x.cuda().t().contiguous().t(), _handle(w, kind), m), ref)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_rows_that_are_not_finite_or_large_stay_alone(kind, dt):
+    K = _k(kind, 256)
+    dtype = DTYPES[dt]
+    w = _make(kind, 1, 40, K, dtype)
+    x = randn((20, K), dtype, 3)
+    ref = _check(x, w, kind, [20])
+    x[4, 9] = math.nan
+    x[11, 100] = math.inf
+    y = g.grouped_matmul_w4(x.cuda(), _handle(w, kind), torch.tensor([20], dtype=torch.int32, device="cuda"))
+    rows = torch.tensor([i for i in range(20) if i not in (4, 11)])
+    assert torch.equal(y[rows], ref[rows]) and bool(torch.isnan(y[4]).all())
+    v = _values(w, kind)[0, :, 100]
+    want = torch.where(v == 0, math.nan, torch.sign(v) * math.inf)
+    got = y[11].cpu().double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got[v != 0], want[v != 0])
+    # one large element beside zeros: within range as long as the result is
+    big = torch.zeros((1, K), dtype=dtype)
+    big[0, 33] = torch.finfo(dtype).max / 64
+    _check(big, w, kind, [1])
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_the_largest_rows(dt):
+    """Products of the largest rows with the largest integers pass the type's range before the scale brings them back."""
+    dtype = DTYPES[dt]
+    big = torch.zeros((2, 256), dtype=dtype)
+    big[0, 33] = big[1, 200] = torch.finfo(dtype).max
+    codes = torch.full((1, 16, 128), 0xFF, dtype=torch.uint8)
+    codes[:, ::2] = 0
+    zeros = torch.zeros((1, 16, 8), dtype=torch.uint8)
+    zeros[:, ::2] = 15
+    _check(big, (codes, torch.full((1, 16, 8), 2.0 ** -6, dtype=dtype), zeros), "32", [2])
+    scales = torch.full((1, 16, 16), 0x7E, dtype=torch.uint8)         # 448: the weights are +-0.5
+    codes[:, ::4] = 0x77
+    _check(big, (codes, scales, torch.full((1,), 0.5)), "nvfp4", [2])
+    # weights as large and as small as bf16 has them
+    x = randn((3, 256), dtype, 4)
+    for amax in (1e38, 1e-30, 0.0) if dt == "bf16" else (1e3, 1e-3, 0.0):
+        _check(x * (1e-3 if amax > 1 or amax == 0 else 1), (codes, scales, torch.full((1,), amax)), "nvfp4", [3])
+
+
+def test_scales_that_are_not_finite_reach_their_column_only():
+    codes, scales, zeros = _int4(1, 20, 128, 32, torch.bfloat16, 1)
+    x = randn((3, 128), torch.bfloat16, 2)
+    ref = _check(x, (codes, scales, zeros), "32", [3])
+    scales[0, 6, 2] = math.nan
+    y = g.grouped_matmul_w4(x.cuda(), _handle((codes, scales, zeros), "32"), torch.tensor([3], dtype=torch.int32, device="cuda"))
+    cols = torch.tensor([i for i in range(20) if i != 6])
+    assert torch.equal(y[:, cols], ref[:, cols]) and bool(torch.isnan(y[:, 6]).all())
+
+
+def test_many_groups_and_random_splits():
+    r = np.random.RandomState(3)
+    for G, M in ((128, 64), (300, 500), (64, 509)):
+        splits = r.multinomial(M - 3, np.full(G, 1.0 / G)).tolist()
+        for kind, dtype in (("64", torch.bfloat16), ("nvfp4", torch.float16)):
+            print(f"w4 groups G={G} M={M} {kind}", flush=True)
+            w = _make(kind, G, 72, 192, dtype)
+            _check(randn((M, 192), dtype, 4), w, kind, splits)
+
+
+def test_no_rows_and_determinism():
+    w = _handle(_make("32", 2, 24, 64, torch.bfloat16), "32")
+    m = torch.zeros(2, dtype=torch.int32, device="cuda")
+    assert g.grouped_matmul_w4(torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), w, m).shape == (0, 24)
+    w = _handle(_make("nvfp4", 4, 1000, 2048, torch.bfloat16), "nvfp4")
+    x, m = randn((50, 2048), torch.bfloat16, 1).cuda(), torch.tensor([9, 1, 30, 10], dtype=torch.int32, device="cuda")
+    ref = g.grouped_matmul_w4(x, w, m)
+    for _ in range(5):
+        assert torch.equal(ref, g.grouped_matmul_w4(x, w, m))
+
+
+def test_graph_replays_and_two_streams():
+    a, b = (_make("64", 6, 300, 1024, torch.bfloat16, s) for s in (1, 3))
+    x = randn((33, 1024), torch.bfloat16, 5).cuda()
+    live = [t.cuda() for t in a]
+    m1, m2 = (torch.tensor(s, dtype=torch.int32, device="cuda") for s in ([3, 0, 20, 1, 9, 0], [33, 0, 0, 0, 0, 0]))
+    m = m1.clone()
+
+    def step():
+        return g.grouped_matmul_w4(x, g.Int4Weights(*live), m)
+    refs = []
+    for w, s in ((a, m1), (b, m2)):
+        for t, v in zip(live, w):
+            t.copy_(v)
+        m.copy_(s)
+        refs.append(step().clone())
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for s in (s1, s2):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append(step())
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], refs[1]) and torch.equal(got[1], refs[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for r in range(4):
+        for t, v in zip(live, a if r % 2 == 0 else b):
+            t.copy_(v)
+        m.copy_(m1 if r % 2 == 0 else m2)
+        out.fill_(5)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, refs[r % 2]), r
+    del graph
+
+
+def test_codes_past_four_gigabytes():
+    """The last group's codes and scales lie behind 2^32 bytes."""
+    G, N, K = 20, 16384, 32768                                        # 5.4 GB of codes
+    free, _ = torch.cuda.mem_get_info()
+    if free < 16 << 30:
+        pytest.skip("needs 16 GB")
+    codes = torch.zeros((G, N, K // 2), dtype=torch.uint8, device="cuda").fill_(0x88)
+    codes[-1] = 0x9B
+    scales = torch.ones((G, N, K // 128), dtype=torch.bfloat16, device="cuda")
+    scales[-1, -5:] = 2.0
+    x = torch.zeros((3, K), dtype=torch.bfloat16, device="cuda")
+    x[:, -2:] = torch.tensor([[1.0, 0.0], [0.0, 1.0], [1.0, 1.0]])
+    splits = [0] * G
+    splits[-1] = 3
+    y = g.grouped_matmul_w4(x, g.Int4Weights(codes, scales), torch.tensor(splits, dtype=torch.int32, device="cuda"))
+    want = torch.tensor([3.0, 1.0, 4.0], dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(y[:, :-5], want[:, None].expand(3, N - 5)) and torch.equal(y[:, -5:], 2 * want[:, None].expand(3, 5))
+
+
+def test_more_tiles_than_one_grid_row_holds():
+    """Past 2^24 workgroups the grid is folded: 16-row tiles of 2^18 x 16 rows, 65 column tiles."""
+    M, N, K = (1 << 22) + 5, 4100, 32
+    free, _ = torch.cuda.mem_get_info()
+    if free < 90 << 30:
+        pytest.skip("needs 90 GB")
+    codes = torch.full((1, N, K // 2), 0x99, dtype=torch.uint8, device="cuda")
+    scales = torch.ones((1, N, 1), dtype=torch.float16, device="cuda")
+    x = torch.zeros((M, K), dtype=torch.float16, device="cuda")
+    x[:, 3] = (torch.arange(M, device="cuda") % 97).to(torch.float16)
+    y = g.grouped_matmul_w4(x, g.Int4Weights(codes, scales), torch.tensor([M], dtype=torch.int32, device="cuda"))
+    assert torch.equal(y.amin(1), x[:, 3]) and torch.equal(y.amax(1), x[:, 3])
