@@ -608,7 +608,7 @@ typedef struct {
   int32_t G;
   int64_t M, N, K;
 } gmlp_w4_args;
-gmlp_status gmlp_grouped_matmul_w4(const gmlp_w4_args* args, hipStream_t stream);
+gmlp_status gmlp_grouped_matmul_four_bit(const gmlp_w4_args* args, hipStream_t stream);
 
 #ifdef __cplusplus
 }

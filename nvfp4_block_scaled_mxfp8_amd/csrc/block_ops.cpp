@@ -231,7 +231,7 @@ extern "C" gmlp_status gmlp_residual_norm_backward(const gmlp_norm_bwd_args* p, 
 }
 
 // ----------------------------------------------------------------------------- products with 4-bit weights
-extern "C" gmlp_status gmlp_grouped_matmul_w4(const gmlp_w4_args* p, hipStream_t stream) {
+extern "C" gmlp_status gmlp_grouped_matmul_four_bit(const gmlp_w4_args* p, hipStream_t stream) {
   if (!p) return null_arg();
   gmlp_status st = check_dtype(p->dtype);
   if (st != GMLP_OK) return st;

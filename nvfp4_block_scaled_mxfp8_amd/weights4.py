@@ -26,7 +26,7 @@ class W4Args(ctypes.Structure):
                 ("K", ctypes.c_int64)]
 
 
-_SIGS.update({"gmlp_grouped_matmul_w4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p])})      # W4Args*
+_SIGS.update({"gmlp_grouped_matmul_four_bit": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p])})      # W4Args*
 _pack = _packer(W4Args)
 
 
@@ -114,5 +114,5 @@ def grouped_matmul_w4(x, w, m_splits, out=None):
     args = _pack(_DTYPES[x.dtype], kind, group, out is None, x.data_ptr(), _ld(x), codes.data_ptr(), scales.data_ptr(),
                  zeros.data_ptr() if zeros is not None else 0, amax.data_ptr() if amax is not None else 0, y.data_ptr(), _ld(y),
                  m_splits.data_ptr(), G, M, N, K)
-    _run(lib().gmlp_grouped_matmul_w4, args, dev)
+    _run(lib().gmlp_grouped_matmul_four_bit, args, dev)
     return y if out is None else _written(out)

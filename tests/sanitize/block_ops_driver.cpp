@@ -114,7 +114,7 @@ static void w4(int64_t M, int64_t N, int64_t K, int kind, int group) {
   a.M = M;
   a.N = a.ldy = N;
   a.K = a.ldx = K;
-  expect("w4", gmlp_grouped_matmul_w4(&a, nullptr), GMLP_OK);
+  expect("w4", gmlp_grouped_matmul_four_bit(&a, nullptr), GMLP_OK);
 }
 
 // A row's threads cover it in eights, with less than a wave of them to spare, and fit a workgroup.

@@ -239,7 +239,7 @@ def _w4():
 
 
 def test_w4_abi():
-    name = "gmlp_grouped_matmul_w4"
+    name = "gmlp_grouped_matmul_four_bit"
     assert _call(name, None) == 1
     for change, status, text in (({"dtype": 2}, 2, "dtype"), ({"kind": 2}, 1, "kind"), ({"group": 16}, 2, "group"), ({"group": 256}, 2, "group"),
                                  ({"kind": 1}, 2, "group"), ({"M": -1}, 2, "M = "), ({"M": (1 << 30) + 1}, 2, "M = "), ({"G": 0}, 2, "groups"),
