@@ -39,30 +39,59 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
 // integers up to 15 stay in fp32 (fp16 rows are far from its end).
 template <int TYPE>
 constexpr float kDown = TYPE == MM_BF16 ? 0x1p-12f : 1.0f;
-// Eight codes -> eight integers q - zero, times kDown, exact in 16 bits (zero: times -kDown).
+// Eight codes -> eight integers q - zero, times kDown, exact in 16 bits (zero: times -kDown; fp16: the pair
+// of -(1024 + zero)).  fp16 takes the pairs k, k + 4 that a mask leaves in one word: 1024 + q is a number whose last
+// bits are q, so a mask, an or and one addition of pairs do; x's operand is then in that order too (pairs_apart).
 template <int TYPE>
-__device__ __forceinline__ v4i decode_int(uint32_t w, float zero) {
+__device__ __forceinline__ v4i decode_int(uint32_t w, float zero, uint32_t zero2) {
+  if constexpr (TYPE == MM_FP16) {
+    v4i o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const v2h q = __builtin_bit_cast(v2h, ((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u);
+      o[i] = __builtin_bit_cast(int, q + __builtin_bit_cast(v2h, zero2));
+    }
+    return o;
+  }
   const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
   auto pair = [&](int at) {
     return (int)Elem<TYPE>::down2(fmaf((float)((even >> at) & 255u), kDown<TYPE>, zero), fmaf((float)((odd >> at) & 255u), kDown<TYPE>, zero));
   };
   return v4i{pair(0), pair(8), pair(16), pair(24)};
 }
-// Eight E2M1 codes times an E4M3 block scale, exact in 16 bits.
-template <int TYPE, int I>
-__device__ __forceinline__ int decode_fp4x2(uint32_t w, float sc) {
-  const v2f v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, I);
-  return (int)Elem<TYPE>::down2(v.x * sc, v.y * sc);
+// Eight values (0 1)(2 3)(4 5)(6 7) -> (0 4)(1 5)(2 6)(3 7).
+__device__ __forceinline__ v4i pairs_apart(v4i v) {
+  const uint32_t a = (uint32_t)v.x, b = (uint32_t)v.y, c = (uint32_t)v.z, d = (uint32_t)v.w;
+  return v4i{(int)__builtin_amdgcn_perm(c, a, 0x05040100u), (int)__builtin_amdgcn_perm(c, a, 0x07060302u),
+             (int)__builtin_amdgcn_perm(d, b, 0x05040100u), (int)__builtin_amdgcn_perm(d, b, 0x07060302u)};
 }
+// Eight E2M1 codes times an E4M3 block scale, exact in 16 bits.
 template <int TYPE>
 __device__ __forceinline__ v4i decode_fp4(uint32_t w, float sc) {
-  return v4i{decode_fp4x2<TYPE, 0>(w, sc), decode_fp4x2<TYPE, 1>(w, sc), decode_fp4x2<TYPE, 2>(w, sc), decode_fp4x2<TYPE, 3>(w, sc)};
+  if constexpr (TYPE == MM_BF16)
+    return v4i{(int)e2m1x2_scaled_bf16<0>(w, sc), (int)e2m1x2_scaled_bf16<1>(w, sc), (int)e2m1x2_scaled_bf16<2>(w, sc),
+               (int)e2m1x2_scaled_bf16<3>(w, sc)};
+  const v2h s{(_Float16)sc, (_Float16)sc};
+  return v4i{__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * s),
+             __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * s),
+             __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * s),
+             __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * s)};
 }
+
+// What a wave has in registers of a chunk: a column's codes, scales and zeros (packed as they lie) per lane and,
+// with one row tile, x's operands.
+template <int MT, int NT>
+struct W4Loads {
+  v4i w[NT];
+  uint64_t s[NT];
+  uint32_t z[NT];
+  v4i a[MT][4];
+};
 
 template <int TYPE, int KIND, int GROUP, int MT, int NT>
 __global__ __launch_bounds__(512) void w4_kernel(W4Args p, uint32_t ntn, int64_t blocks) {
   using E = Elem<TYPE>;
-  constexpr bool INT = KIND == W4_INT, TRANS = INT && GROUP < 128;
+  constexpr bool INT = KIND == W4_INT, TRANS = INT && GROUP < 128, APART = INT && TYPE == MM_FP16;
   constexpr int PER = INT ? kW4Chunk / GROUP : 2;              // scales a lane has in a chunk
   constexpr int SLOTS = MT * NT * 4;
   extern __shared__ float s_sum[];                             // [waves][SLOTS][64]
@@ -71,8 +100,10 @@ __global__ __launch_bounds__(512) void w4_kernel(W4Args p, uint32_t ntn, int64_t
   if (block >= blocks) return;
   const RowTile tile = find_row_tile(p.m_splits, p.G, (uint32_t)p.M, 16 * MT, ntn, p.zero_rest, (uint32_t)block, lane);
   if (tile.g < 0) return;
-  const uint32_t r0 = tile.t / ntn * (16 * MT);
-  const int n0 = (int)(tile.t % ntn) * (16 * NT);
+  // a column tile's row tiles follow each other: they read the same weights
+  const uint32_t nrt = (tile.m + 16 * MT - 1) / (16 * MT);
+  const uint32_t r0 = tile.t % nrt * (16 * MT);
+  const int n0 = (int)(tile.t / nrt) * (16 * NT);
   const int rows = (int)min(tile.m - r0, 16u * MT);
   uint16_t* y = static_cast<uint16_t*>(p.y) + (int64_t)(tile.row0 + r0) * p.ldy;
   if (tile.g == p.G) {
@@ -81,77 +112,139 @@ __global__ __launch_bounds__(512) void w4_kernel(W4Args p, uint32_t ntn, int64_t
     return;
   }
   const int col = lane & 15, q = lane >> 4, N = p.N, K = p.K;
-  const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)(tile.row0 + r0 + col) * p.ldx;
+  // rows and columns behind the last read the last one's values: a product's row or column reaches its own results only
+  const uint16_t* x[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) x[m] = static_cast<const uint16_t*>(p.x) + ((int64_t)(tile.row0 + r0) + min(16 * m + col, rows - 1)) * p.ldx;
   const uint8_t* codes[NT];
   int64_t meta[NT];                                            // the column's first scale
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int64_t n = (int64_t)tile.g * N + min(n0 + 16 * j + col, N - 1);
-    codes[j] = p.codes + n * (K / 2) + 16 * q;
+    codes[j] = p.codes + n * (K / 2);
     meta[j] = n * (K / GROUP);
   }
   // NVFP4, bf16 rows: the largest power of two up to 1 / S goes into the block scales, so that products are
   // no larger than those of the weights themselves (above 2^-60: below it they would leave the exact values)
   const float global = INT ? 1.0f : nvfp4_global_scale(p.amax[tile.g]);
   const int down = INT || TYPE != MM_BF16 ? 0 : min(ilogbf(global) + 1, 60);
+  const float downf = ldexpf(1.0f, -down);
   v4f acc[MT][NT] = {};
   const int chunks = (K + kW4Chunk - 1) / kW4Chunk;
-  for (int c = wave; c < chunks; c += waves) {
+  auto load_x = [&](int c, v4i (&a)[MT][4]) {
     const int k0 = c * kW4Chunk;
-    const bool have = k0 + 32 * q < K;
-    v4i raw[NT];
-    float sc[NT][PER], zero[NT][PER];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      raw[j] = v4i{0, 0, 0, 0};
-      if (have) raw[j] = *reinterpret_cast<const v4i*>(codes[j] + k0 / 2);
-#pragma unroll
-      for (int s = 0; s < PER; ++s) {
-        const int k = INT ? k0 + s * GROUP : k0 + 32 * q + 16 * s;
-        sc[j][s] = 0.0f;
-        zero[j][s] = -8.0f * kDown<TYPE>;
-        if (k >= K) continue;
-        if (INT) {
-          sc[j][s] = E::up(static_cast<const uint16_t*>(p.scales)[meta[j] + k / GROUP]);
-          if (p.zeros) zero[j][s] = -kDown<TYPE> * (float)p.zeros[meta[j] + k / GROUP];
-        } else {
-          sc[j][s] = ldexpf(__builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(p.scales)[meta[j] + k / GROUP], 0), -down);
-        }
-      }
-    }
-    v4i a[MT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = k0 + (TRANS ? 32 * i + 8 * q : 32 * q + 8 * i);
-        a[m][i] = v4i{0, 0, 0, 0};
-        if (16 * m + col < rows && k < K) __builtin_memcpy(&a[m][i], x + (int64_t)(16 * m) * p.ldx + k, 16);
-      }
+      for (int i = 0; i < 4; ++i)
+        __builtin_memcpy(&a[m][i], x[m] + min(k0 + (TRANS ? 32 * i + 8 * q : 32 * q + 8 * i), K - 8), 16);
+  };
+  auto load = [&](int c, W4Loads<MT, NT>& l) {
+    const int k0 = c * kW4Chunk;
+    if (MT == 1) load_x(c, l.a);
+    const bool whole = k0 + kW4Chunk <= K;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      uint32_t w[4] = {(uint32_t)raw[j].x, (uint32_t)raw[j].y, (uint32_t)raw[j].z, (uint32_t)raw[j].w};
+      l.w[j] = *reinterpret_cast<const v4i*>(codes[j] + min(k0 / 2 + 16 * q, K / 2 - 16));
+      const int64_t at = meta[j] + k0 / GROUP;
+      if (!INT) {
+        uint16_t s;
+        __builtin_memcpy(&s, static_cast<const uint8_t*>(p.scales) + meta[j] + min(k0 / 16 + 2 * q, K / 16 - 2), 2);
+        l.s[j] = s;
+      } else if (PER == 1 || whole) {
+        const uint16_t* s = static_cast<const uint16_t*>(p.scales) + at;
+        if (PER == 4) __builtin_memcpy(&l.s[j], s, 8);
+        if (PER == 2) {
+          uint32_t v;
+          __builtin_memcpy(&v, s, 4);
+          l.s[j] = v;
+        }
+        if (PER == 1) l.s[j] = *s;
+        if (p.zeros) {
+          const uint8_t* z = p.zeros + at;
+          if (PER == 4) __builtin_memcpy(&l.z[j], z, 4);
+          if (PER == 2) {
+            uint16_t v;
+            __builtin_memcpy(&v, z, 2);
+            l.z[j] = v;
+          }
+          if (PER == 1) l.z[j] = *z;
+        }
+      } else {                                                 // the groups that there are, at least one
+        l.s[j] = 0;
+        l.z[j] = 0;
+        for (int s = 0; k0 + s * GROUP < K; ++s) {
+          l.s[j] |= (uint64_t)static_cast<const uint16_t*>(p.scales)[at + s] << (16 * s);
+          if (p.zeros) l.z[j] |= (uint32_t)p.zeros[at + s] << (8 * s);
+        }
+      }
+    }
+  };
+  auto multiply = [&](int c, W4Loads<MT, NT>& l) {
+    const int k0 = c * kW4Chunk;
+    const bool whole = k0 + kW4Chunk <= K, have = k0 + 32 * q < K;
+    if (!TRANS && !whole)                                      // lanes behind K's end: zeros
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l.a[m][i] = have ? l.a[m][i] : v4i{0, 0, 0, 0};
+    if (APART)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l.a[m][i] = pairs_apart(l.a[m][i]);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      uint32_t w[4] = {(uint32_t)l.w[j].x, (uint32_t)l.w[j].y, (uint32_t)l.w[j].z, (uint32_t)l.w[j].w};
       if (TRANS) transpose4(w);
+      float sc[PER], zero[PER];
+      uint32_t zero2[PER];
+#pragma unroll
+      for (int s = 0; s < PER; ++s) {
+        if (INT) {
+          sc[s] = E::up((uint16_t)(l.s[j] >> (16 * s)));
+          const float z = p.zeros ? (float)((l.z[j] >> (8 * s)) & 255u) : 8.0f;
+          zero[s] = -kDown<TYPE> * z;
+          zero2[s] = APART ? E::down2(-1024.0f - z, -1024.0f - z) : 0;
+        } else {
+          sc[s] = downf * (s == 0 ? __builtin_amdgcn_cvt_f32_fp8((int)l.s[j], 0) : __builtin_amdgcn_cvt_f32_fp8((int)l.s[j], 1));
+          if (!whole && !have) sc[s] = 0.0f;
+        }
+      }
       v4f part[MT] = {};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        if (TRANS && !whole && k0 + 32 * i >= K) break;
         const int s = INT ? i * 32 / GROUP : i / 2;
-        const v4i b = INT ? decode_int<TYPE>(w[i], zero[j][s]) : decode_fp4<TYPE>(w[i], sc[j][s]);
+        const v4i b = INT ? decode_int<TYPE>(w[i], zero[s], zero2[s]) : decode_fp4<TYPE>(w[i], sc[s]);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           if (!INT) {
-            acc[m][j] = E::mma16(a[m][i], b, acc[m][j]);
+            acc[m][j] = E::mma16(l.a[m][i], b, acc[m][j]);
           } else {
-            part[m] = E::mma16(a[m][i], b, part[m]);
+            part[m] = E::mma16(l.a[m][i], b, part[m]);
             if ((i + 1) * 32 % GROUP == 0) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r) acc[m][j][r] = fmaf(sc[j][s], part[m][r], acc[m][j][r]);
+              for (int r = 0; r < 4; ++r) acc[m][j][r] = fmaf(sc[s], part[m][r], acc[m][j][r]);
               part[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
             }
           }
         }
       }
     }
+  };
+  // the next chunk's loads in flight
+  W4Loads<MT, NT> l0, l1;
+  int c = wave;
+  if (c < chunks) load(c, l0);
+  for (; c < chunks; c += 2 * waves) {
+    if (MT > 1) load_x(c, l0.a);
+    if (c + waves < chunks) load(c + waves, l1);
+    multiply(c, l0);
+    if (c + waves >= chunks) break;
+    if (MT > 1) load_x(c + waves, l1.a);
+    if (c + 2 * waves < chunks) load(c + 2 * waves, l0);
+    multiply(c + waves, l1);
   }
   // the waves' sums, joined in order
 #pragma unroll
@@ -174,8 +267,8 @@ __global__ __launch_bounds__(512) void w4_kernel(W4Args p, uint32_t ntn, int64_t
 // ----------------------------------------------------------------------------- launches
 template <int TYPE, int KIND, int GROUP, int MT, int NT>
 static hipError_t run_w4(W4Args p, hipStream_t s) {
-  const int waves = 4;
   const int64_t ntn = (p.N + 16 * NT - 1) / (16 * NT), blocks = sizes::row_tiles_bound(p.M, p.G, 16 * MT) * ntn;
+  const int waves = sizes::w4_waves(blocks, p.K);
   const FoldedGrid g = fold_grid(blocks, 64 * waves);
   p.row_blocks = g.x;
   hipLaunchKernelGGL((w4_kernel<TYPE, KIND, GROUP, MT, NT>), dim3(g.x, g.y), dim3(64 * waves), (size_t)waves * MT * NT * 4 * 64 * sizeof(float),
@@ -184,7 +277,10 @@ static hipError_t run_w4(W4Args p, hipStream_t s) {
 }
 template <int TYPE, int KIND, int GROUP>
 static hipError_t run_w4(const W4Args& p, hipStream_t s) {
-  return run_w4<TYPE, KIND, GROUP, 1, 4>(p, s);
+  const int64_t tiles = sizes::row_tiles_bound(p.M, p.G, 16) * ((p.N + 63) / 64);
+  if (p.M / p.G > 32) return run_w4<TYPE, KIND, GROUP, 4, 2>(p, s);
+  if (tiles >= 1024) return run_w4<TYPE, KIND, GROUP, 1, 4>(p, s);
+  return run_w4<TYPE, KIND, GROUP, 1, 1>(p, s);
 }
 template <int TYPE>
 static hipError_t run_w4(const W4Args& p, hipStream_t s) {
