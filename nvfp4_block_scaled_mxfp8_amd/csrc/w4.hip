@@ -16,6 +16,9 @@
 #include "block_ops.h"
 #include "block_sizes.h"
 #include "mm_common.h"
+#include "wave_ops.h"
+
+#include <type_traits>
 
 namespace gmlp {
 
@@ -41,15 +44,21 @@ template <int TYPE>
 constexpr float kDown = TYPE == MM_BF16 ? 0x1p-12f : 1.0f;
 // Eight codes -> eight integers q - zero, times kDown, exact in 16 bits (zero: times -kDown; fp16: the pair
 // of -(1024 + zero)).  fp16 takes the pairs k, k + 4 that a mask leaves in one word: 1024 + q is a number whose last
-// bits are q, so a mask, an or and one addition of pairs do; x's operand is then in that order too (pairs_apart).
+// bits are q, and 1024 + 16 q the same four bits higher, so a mask, an or and one addition (or one product with
+// 1/16 and addition) of pairs do; x's operand is then in that order too (pairs_apart).
 template <int TYPE>
 __device__ __forceinline__ v4i decode_int(uint32_t w, float zero, uint32_t zero2) {
   if constexpr (TYPE == MM_FP16) {
+    const v2h low = __builtin_bit_cast(v2h, zero2);
+    const v2h high = low + v2h{(_Float16)960, (_Float16)960};             // -(64 + zero)
+    const v2h sixteenth{(_Float16)0.0625f, (_Float16)0.0625f};
     v4i o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const v2h q = __builtin_bit_cast(v2h, ((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u);
-      o[i] = __builtin_bit_cast(int, q + __builtin_bit_cast(v2h, zero2));
+    for (int i = 0; i < 4; i += 2) {
+      const uint32_t v = w >> (4 * i);
+      const v2h a = __builtin_bit_cast(v2h, (v & 0x000F000Fu) | 0x64006400u), b = __builtin_bit_cast(v2h, (v & 0x00F000F0u) | 0x64006400u);
+      o[i] = __builtin_bit_cast(int, a + low);
+      o[i + 1] = __builtin_bit_cast(int, __builtin_elementwise_fma(b, sixteenth, high));
     }
     return o;
   }
@@ -80,10 +89,11 @@ __device__ __forceinline__ v4i decode_fp4(uint32_t w, float sc) {
 
 // What a wave has in registers of a chunk: a column's codes, scales and zeros (packed as they lie) per lane and,
 // with one row tile, x's operands.
-template <int MT, int NT>
+template <int KIND, int PER, int MT, int NT>
 struct W4Loads {
+  using Scales = std::conditional_t<KIND == W4_INT && PER == 4, uint64_t, uint32_t>;
   v4i w[NT];
-  uint64_t s[NT];
+  Scales s[NT];
   uint32_t z[NT];
   v4i a[MT][4];
 };
@@ -139,7 +149,7 @@ __global__ __launch_bounds__(512) void w4_kernel(W4Args p, uint32_t ntn, int64_t
       for (int i = 0; i < 4; ++i)
         __builtin_memcpy(&a[m][i], x[m] + min(k0 + (TRANS ? 32 * i + 8 * q : 32 * q + 8 * i), K - 8), 16);
   };
-  auto load = [&](int c, W4Loads<MT, NT>& l) {
+  auto load = [&](int c, W4Loads<KIND, PER, MT, NT>& l) {
     const int k0 = c * kW4Chunk;
     if (MT == 1) load_x(c, l.a);
     const bool whole = k0 + kW4Chunk <= K;
@@ -174,13 +184,13 @@ __global__ __launch_bounds__(512) void w4_kernel(W4Args p, uint32_t ntn, int64_t
         l.s[j] = 0;
         l.z[j] = 0;
         for (int s = 0; k0 + s * GROUP < K; ++s) {
-          l.s[j] |= (uint64_t)static_cast<const uint16_t*>(p.scales)[at + s] << (16 * s);
+          l.s[j] |= (typename W4Loads<KIND, PER, MT, NT>::Scales)static_cast<const uint16_t*>(p.scales)[at + s] << (16 * s);
           if (p.zeros) l.z[j] |= (uint32_t)p.zeros[at + s] << (8 * s);
         }
       }
     }
   };
-  auto multiply = [&](int c, W4Loads<MT, NT>& l) {
+  auto multiply = [&](int c, W4Loads<KIND, PER, MT, NT>& l) {
     const int k0 = c * kW4Chunk;
     const bool whole = k0 + kW4Chunk <= K, have = k0 + 32 * q < K;
     if (!TRANS && !whole)                                      // lanes behind K's end: zeros
@@ -234,7 +244,7 @@ __global__ __launch_bounds__(512) void w4_kernel(W4Args p, uint32_t ntn, int64_t
     }
   };
   // the next chunk's loads in flight
-  W4Loads<MT, NT> l0, l1;
+  W4Loads<KIND, PER, MT, NT> l0, l1;
   int c = wave;
   if (c < chunks) load(c, l0);
   for (; c < chunks; c += 2 * waves) {
@@ -264,9 +274,251 @@ __global__ __launch_bounds__(512) void w4_kernel(W4Args p, uint32_t ntn, int64_t
   }
 }
 
+// ----------------------------------------------------------------------------- many tiles
+// Where the tiles alone fill the device: a workgroup has 16 MT rows of one group and 128 columns, 16 a wave, and walks K in
+// spans of SPAN chunks: a wave's loads of the next span (512 or 1024 elements of each of its columns) are all in
+// flight while it multiplies this one, and x's part of a span lies in LDS for all waves.  What is left of K
+// behind the last whole span goes chunk by chunk.
+// bf16 rows of a single tile become fp16 on their way into LDS, times a power of two by row and span that brings the span's largest to
+// [2^14, 2^15): the same 8 bits down to 2^-28 of it, and no more than 2^-40 of it is lost below that, far under
+// what fp32 sums keep.  So both types decode by the packed operations that fp16 has and bf16 lacks (11 instead of
+// 22 operations a product of integers, 8 instead of 20 with NVFP4; a product's 512 weights take 85 ns at 6 TB/s and a
+// CU's share, four products side by side, 2 ns an operation).
+// Loads alone, 16 rows of 64 bytes each, reach 6.0 TB/s where eight are in flight per wave, 3.5 to 4 with one or two.
+template <int KIND, int GROUP, int SPAN>
+struct W4Span {
+  static constexpr bool INT = KIND == W4_INT;
+  static constexpr int NS = INT ? SPAN * kW4Chunk / GROUP : SPAN * 2;      // 16-bit words of scales a lane has
+  v4i w[SPAN];
+  uint32_t s[NS / 2];        // integers: the column's, in order; NVFP4: of each four chunks, the one q's eight bytes
+  uint32_t z[INT ? NS / 4 : 1];
+};
+// Scale bytes of four chunks, chunk q in lane row q -> the pairs of blocks 2 q, 2 q + 1 of every chunk.
+__device__ __forceinline__ void scales_by_lane(uint32_t& d0, uint32_t& d1) {
+  const v2u a = __builtin_amdgcn_permlane32_swap(d0, d1, false, false);
+  const v2u b = __builtin_amdgcn_permlane16_swap(a.x, a.y, false, false);
+  const uint32_t lo = __builtin_amdgcn_perm(b.y, b.x, 0x05040100u), hi = __builtin_amdgcn_perm(b.y, b.x, 0x07060302u);
+  const v2u c = __builtin_amdgcn_permlane16_swap(lo, hi, false, false);
+  d0 = c.x;
+  d1 = c.y;
+}
+
+template <int TYPE, int KIND, int GROUP, int MT, int SPAN, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void w4_wide_kernel(W4Args p, uint32_t ntn, int64_t blocks) {
+  using E = Elem<TYPE>;
+  using F = Elem<MM_FP16>;
+  constexpr bool SCALED = TYPE == MM_BF16 && MT == 1;          // rows become fp16 times a power of two
+  constexpr int T = SCALED ? MM_FP16 : TYPE;
+  constexpr bool INT = KIND == W4_INT, TRANS = INT && GROUP < 128, APART = INT && T == MM_FP16;
+  constexpr int SK = SPAN * kW4Chunk, XLD = SK + 8, PIECES = SK / 8, ROWS = 16 * MT;
+  constexpr int NTH = 64 * WAVES, STAGE = ROWS * PIECES / NTH;                   // 16-byte pieces of x a thread stages at most
+  using Span = W4Span<KIND, GROUP, SPAN>;
+  static_assert(PIECES % 64 == 0, "a wave stages pieces of one row");
+  extern __shared__ __align__(16) uint16_t s_x[];              // [2][ROWS][XLD]: rows 16 bytes apart in the banks
+  __shared__ __align__(16) float s_factor[2][PIECES / 64][ROWS];            // what brings a row's sums over a span back
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t block = (int64_t)blockIdx.x + (int64_t)blockIdx.y * p.row_blocks;
+  if (block >= blocks) return;
+  const RowTile tile = find_row_tile(p.m_splits, p.G, (uint32_t)p.M, ROWS, ntn, p.zero_rest, (uint32_t)block, lane);
+  if (tile.g < 0) return;
+  const uint32_t nrt = (tile.m + ROWS - 1) / ROWS;
+  const uint32_t r0 = tile.t % nrt * ROWS;
+  const int n0 = (int)(tile.t / nrt) * (16 * WAVES) + 16 * wave;
+  const int rows = (int)min(tile.m - r0, (uint32_t)ROWS);
+  const int col = lane & 15, q = lane >> 4, N = p.N, K = p.K;
+  uint16_t* y = static_cast<uint16_t*>(p.y) + (int64_t)(tile.row0 + r0) * p.ldy + n0 + col;
+  if (tile.g == p.G) {
+    if (n0 + col < N)
+      for (int m = q; m < rows; m += 4) y[(int64_t)m * p.ldy] = 0;
+    return;
+  }
+  const uint16_t* x0 = static_cast<const uint16_t*>(p.x) + (int64_t)(tile.row0 + r0) * p.ldx;
+  const int64_t n = (int64_t)tile.g * N + min(n0 + col, N - 1);
+  const uint8_t* codes = p.codes + n * (K / 2);
+  const int64_t meta = n * (K / GROUP);
+  const float global = INT ? 1.0f : nvfp4_global_scale(p.amax[tile.g]);
+  const int down = INT || TYPE != MM_BF16 ? 0 : min(ilogbf(global) + 1, 60);
+  const float downf = ldexpf(1.0f, -down);
+  const int spans = K / SK, chunks = (K + kW4Chunk - 1) / kW4Chunk;
+
+  auto load = [&](int s, Span& l) {
+#pragma unroll
+    for (int c = 0; c < SPAN; ++c) l.w[c] = *reinterpret_cast<const v4i*>(codes + s * (SK / 2) + c * 64 + 16 * q);
+    if (INT) {
+      __builtin_memcpy(l.s, static_cast<const uint16_t*>(p.scales) + meta + s * Span::NS, 2 * Span::NS);
+      if (p.zeros) __builtin_memcpy(l.z, p.zeros + meta + s * Span::NS, Span::NS);
+    } else {
+#pragma unroll
+      for (int h = 0; h < SPAN / 4; ++h) __builtin_memcpy(&l.s[2 * h], static_cast<const uint8_t*>(p.scales) + meta + (s * SPAN + 4 * h + q) * 8, 8);
+    }
+  };
+  v4i xr[STAGE];
+  auto load_x = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < STAGE; ++i) {
+      const int at = tid + NTH * i;
+      if (at / PIECES < rows) __builtin_memcpy(&xr[i], x0 + (int64_t)(at / PIECES) * p.ldx + s * SK + at % PIECES * 8, 16);
+    }
+  };
+  auto store_x = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < STAGE; ++i) {
+      const int at = tid + NTH * i, row = at / PIECES;
+      if (row >= rows) continue;
+      v4i v = xr[i];
+      if constexpr (SCALED) {
+        int most = 0;                                          // the largest finite magnitude's bits
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int u = (int)(((uint32_t)v[j / 2] >> (16 * (j & 1))) & 0x7FFFu);
+          most = max(most, u < 0x7F80 ? u : 0);
+          f[j] = E::up((uint16_t)((uint32_t)v[j / 2] >> (16 * (j & 1))));
+        }
+        most = lanes_reduce<64>((uint32_t)most, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+        const int e = min(141 - (most >> 7), 126);
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = (int)F::down2(f[2 * j] * up, f[2 * j + 1] * up);
+        if (lane == 0) s_factor[s & 1][at % PIECES / 64][row] = ldexpf(INT ? kDown<TYPE> : downf, -e);
+      }
+      *reinterpret_cast<v4i*>(s_x + ((s & 1) * ROWS + row) * XLD + at % PIECES * 8) = APART ? pairs_apart(v) : v;
+    }
+  };
+  v4f acc[MT] = {}, sum[MT];
+  // one chunk into `to`: a(m, i) gives x's operand, w the codes, sc and zero the scales of the chunk's groups
+  // (NVFP4: of the lane's two blocks); products of k >= K are left out (live of the four)
+  auto multiply = [&](auto type, v4f (&to)[MT], auto a, v4i codes4, const float* sc, const float* zero, const uint32_t* zero2, int live) {
+    constexpr int U = decltype(type)::value;
+    uint32_t w[4] = {(uint32_t)codes4.x, (uint32_t)codes4.y, (uint32_t)codes4.z, (uint32_t)codes4.w};
+    if (TRANS) transpose4(w);
+    v4f part[MT] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= live) break;
+      const int s = INT ? i * 32 / GROUP : i / 2;
+      const v4i b = INT ? decode_int<U>(w[i], zero[s], zero2[s]) : decode_fp4<U>(w[i], sc[s]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if (!INT) {
+          to[m] = Elem<U>::mma16(a(m, i), b, to[m]);
+        } else {
+          part[m] = Elem<U>::mma16(a(m, i), b, part[m]);
+          if ((i + 1) * 32 % GROUP == 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) to[m][r] = fmaf(sc[s], part[m][r], to[m][r]);
+            part[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+          }
+        }
+      }
+    }
+  };
+  constexpr int PER = INT ? kW4Chunk / GROUP : 2;
+  auto int_scales = [&](uint32_t s16, uint32_t z8, float& sc, float& zero, uint32_t& zero2) {
+    sc = E::up((uint16_t)s16);
+    const uint32_t z = p.zeros ? z8 & 255u : 8u;
+    zero = -kDown<TYPE> * (float)z;
+    zero2 = 0xE400E400u + z * 0x00010001u;                     // fp16 -(1024 + z), z < 16
+  };
+  int row_at[MT];                                              // rows behind the last read the last one's
+#pragma unroll
+  for (int m = 0; m < MT; ++m) row_at[m] = min(16 * m + col, rows - 1) * XLD;
+  auto span = [&](int s, Span& l) {
+    const uint16_t* xs = s_x + (s & 1) * ROWS * XLD;
+    if (!INT)
+#pragma unroll
+      for (int h = 0; h < SPAN / 4; ++h) scales_by_lane(l.s[2 * h], l.s[2 * h + 1]);
+#pragma unroll
+    for (int c = 0; c < SPAN; ++c) {
+      if (SCALED && c % 4 == 0)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) sum[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      float sc[PER], zero[PER];
+      uint32_t zero2[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int at = c * PER + i;
+        if (INT) int_scales(l.s[at / 2] >> (16 * (at & 1)), l.z[INT ? at / 4 : 0] >> (8 * (at & 3)), sc[i], zero[i], zero2[i]);
+        else sc[i] = (SCALED ? 1.0f : downf) * __builtin_amdgcn_cvt_f32_fp8((int)((l.s[c / 2] >> (16 * (c & 1))) >> (8 * i)), 0);
+      }
+      multiply(std::integral_constant<int, T>{}, SCALED ? sum : acc, [&](int m, int i) { return *reinterpret_cast<const v4i*>(xs + row_at[m] + c * kW4Chunk + (TRANS ? 32 * i + 8 * q : 32 * q + 8 * i)); },
+               l.w[c], sc, zero, zero2, 4);
+      if (SCALED && c % 4 == 3)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const v4f f = *reinterpret_cast<const v4f*>(&s_factor[s & 1][c / 4][16 * m + 4 * q]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[m][r] = fmaf(f[r], sum[m][r], acc[m][r]);
+        }
+      __builtin_amdgcn_sched_barrier(0);                       // a chunk's values only are live at once
+    }
+  };
+  Span l0, l1;
+  load_x(0);
+  load(0, l0);
+  store_x(0);
+  __syncthreads();
+  for (int s = 0; s < spans; s += 2) {
+    const bool more = s + 1 < spans;
+    if (more) {
+      load_x(s + 1);
+      load(s + 1, l1);
+    }
+    span(s, l0);
+    if (!more) break;
+    store_x(s + 1);
+    __syncthreads();
+    const bool yet = s + 2 < spans;
+    if (yet) {
+      load_x(s + 2);
+      load(s + 2, l0);
+    }
+    span(s + 1, l1);
+    if (!yet) break;
+    store_x(s + 2);
+    __syncthreads();
+  }
+  for (int c = spans * SPAN; c < chunks; ++c) {                // the rest of K
+    const int k0 = c * kW4Chunk, live = min((K - k0) / 32, 4);
+    const v4i w = *reinterpret_cast<const v4i*>(codes + min(k0 / 2 + 16 * q, K / 2 - 16));
+    v4i a[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = k0 + (TRANS ? 32 * i + 8 * q : 32 * q + 8 * i);
+        v4i v;
+        __builtin_memcpy(&v, x0 + (int64_t)min(16 * m + col, rows - 1) * p.ldx + min(k, K - 8), 16);
+        if (!TRANS) v = k < K ? v : v4i{0, 0, 0, 0};
+        a[m][i] = APART && TYPE == MM_FP16 ? pairs_apart(v) : v;
+      }
+    float sc[PER], zero[PER];
+    uint32_t zero2[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (INT) {
+        const int64_t at = meta + min((k0 + i * GROUP) / GROUP, K / GROUP - 1);
+        int_scales(static_cast<const uint16_t*>(p.scales)[at], p.zeros ? p.zeros[at] : 0, sc[i], zero[i], zero2[i]);
+      } else {
+        const int k = k0 + 32 * q + 16 * i;
+        sc[i] = k < K ? downf * __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(p.scales)[meta + k / 16], 0) : 0.0f;
+      }
+    }
+    multiply(std::integral_constant<int, TYPE>{}, acc, [&](int m, int i) { return a[m][i]; }, w, sc, zero, zero2, TRANS ? live : 4);
+  }
+  const float rest = ldexpf(global, -down);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float v = INT ? acc[m][r] * (1.0f / kDown<TYPE>) : __fdiv_rn(acc[m][r], rest);
+      if (16 * m + 4 * q + r < rows && n0 + col < N) y[(int64_t)(16 * m + 4 * q + r) * p.ldy] = E::down(v);
+    }
+}
+
 // ----------------------------------------------------------------------------- launches
 template <int TYPE, int KIND, int GROUP, int MT, int NT>
-static hipError_t run_w4(W4Args p, hipStream_t s) {
+static hipError_t run_split(W4Args p, hipStream_t s) {
   const int64_t ntn = (p.N + 16 * NT - 1) / (16 * NT), blocks = sizes::row_tiles_bound(p.M, p.G, 16 * MT) * ntn;
   const int waves = sizes::w4_waves(blocks, p.K);
   const FoldedGrid g = fold_grid(blocks, 64 * waves);
@@ -275,12 +527,22 @@ static hipError_t run_w4(W4Args p, hipStream_t s) {
                      s, p, (uint32_t)ntn, blocks);
   return hipGetLastError();
 }
+template <int TYPE, int KIND, int GROUP, int MT, int SPAN, int WAVES>
+static hipError_t run_wide(W4Args p, hipStream_t s) {
+  const int64_t ntn = (p.N + 16 * WAVES - 1) / (16 * WAVES), blocks = sizes::row_tiles_bound(p.M, p.G, 16 * MT) * ntn;
+  const FoldedGrid g = fold_grid(blocks, 64 * WAVES);
+  p.row_blocks = g.x;
+  hipLaunchKernelGGL((w4_wide_kernel<TYPE, KIND, GROUP, MT, SPAN, WAVES>), dim3(g.x, g.y), dim3(64 * WAVES), 2 * 16 * MT * (SPAN * kW4Chunk + 8) * sizeof(uint16_t),
+                     s, p, (uint32_t)ntn, blocks);
+  return hipGetLastError();
+}
 template <int TYPE, int KIND, int GROUP>
 static hipError_t run_w4(const W4Args& p, hipStream_t s) {
-  const int64_t tiles = sizes::row_tiles_bound(p.M, p.G, 16) * ((p.N + 63) / 64);
-  if (p.M / p.G > 32) return run_w4<TYPE, KIND, GROUP, 4, 2>(p, s);
-  if (tiles >= 1024) return run_w4<TYPE, KIND, GROUP, 1, 4>(p, s);
-  return run_w4<TYPE, KIND, GROUP, 1, 1>(p, s);
+  constexpr int SPAN = 4;
+  const int64_t waves = sizes::row_tiles_bound(p.M, p.G, 16) * ((p.N + 15) / 16);
+  if (waves < 2048 || p.K < SPAN * kW4Chunk) return run_split<TYPE, KIND, GROUP, 1, 1>(p, s);
+  if (p.M / p.G <= 16) return run_wide<TYPE, KIND, GROUP, 1, SPAN, 4>(p, s);
+  return run_wide<TYPE, KIND, GROUP, 4, SPAN, 8>(p, s);
 }
 template <int TYPE>
 static hipError_t run_w4(const W4Args& p, hipStream_t s) {
