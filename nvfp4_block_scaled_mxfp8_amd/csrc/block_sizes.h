@@ -21,11 +21,8 @@ inline int64_t norm_part_floats(int64_t T, int64_t H) { return 3 * (int64_t)norm
 
 // ----------------------------------------------------------------------------- products with 4-bit weights
 constexpr int kW4Chunk = 128;        // elements along K that a wave takes at once
-// Waves that share a tile's chunks: eight where the tiles alone leave the device empty.
-inline int w4_waves(int64_t blocks, int64_t K) {
-  const int64_t chunks = (K + kW4Chunk - 1) / kW4Chunk;
-  return (int)std::min<int64_t>(blocks < 1024 ? 8 : 4, chunks);
-}
+// Waves that share a tile's chunks where the tiles alone leave the device empty.
+inline int w4_waves(int64_t K) { return (int)std::min<int64_t>(8, (K + kW4Chunk - 1) / kW4Chunk); }
 // Workgroups with the smallest tile, 16 rows x 16 columns: what every launch stays below.
 inline int64_t w4_tiles_bound(int64_t M, int64_t G, int64_t N) { return row_tiles_bound(M, (int)G, 16) * ((N + 15) / 16); }
 

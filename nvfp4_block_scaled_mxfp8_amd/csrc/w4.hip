@@ -2,8 +2,7 @@
 // (half a byte an element and the scales), so a weight is read once, decoded in registers and multiplied on the
 // matrix cores.
 //
-// A workgroup has 16 MT rows of one group and 16 NT columns; its waves take chunks of 128 along K in turn
-// and join their sums in LDS.  Of a chunk a lane loads 16 bytes of a column's codes, 32 elements of one
+// K is taken in chunks of 128.  Of a chunk a lane loads 16 bytes of a column's codes, 32 elements of one
 // row of w: the operand of a product 16 x 16 x 32 holds 8 consecutive elements of a column per lane, the 16
 // columns in the lanes of a row of 16, so each of the four words is one product's operand.  Which elements of K
 // a product takes together is free as long as x's operand has the same:
@@ -87,189 +86,191 @@ __device__ __forceinline__ v4i decode_fp4(uint32_t w, float sc) {
              __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * s)};
 }
 
-// What a wave has in registers of a chunk: a column's codes, scales and zeros (packed as they lie) per lane and,
-// with one row tile, x's operands.
-template <int KIND, int PER, int MT, int NT>
-struct W4Loads {
-  using Scales = std::conditional_t<KIND == W4_INT && PER == 4, uint64_t, uint32_t>;
-  v4i w[NT];
-  Scales s[NT];
-  uint32_t z[NT];
-  v4i a[MT][4];
+// ----------------------------------------------------------------------------- few tiles
+// A workgroup has 16 rows of one group and 16 NT columns; its waves take a part of K each, a batch of chunks' loads in
+// flight at once, and join their sums in LDS.  Of one group with up to 16 rows, a single token's layer, all loads
+// are on their way before the split size that says how many rows there are.
+// What bounds it is the number of requests, 64 bytes of a row each: one token, 7168 x 4096, groups of 64 (us): no loads 3.1,
+// codes 5.2, scales and zeros chunk by chunk 8.8, x 10.5, products 11.4.  So a batch's scales come in one load (10.5 in
+// all), and where tiles have many rows, whose part of x is four requests a row and chunk, four column tiles share it
+// (32 rows: 29.8 -> 18.9).
+template <int KIND, int GROUP, int NT>
+struct W4Batch {
+  static constexpr bool INT = KIND == W4_INT;
+  static constexpr int B = 2;                                  // chunks (four leave one workgroup on a CU: 12.3 us for 10.5)
+  static constexpr int NS = INT ? B * kW4Chunk / GROUP : B;    // 16-bit words of scales
+  v4i w[B][NT];
+  uint32_t s[NT][NS / 2];    // integers: the column's scales in order; NVFP4: the lane's two blocks of each chunk
+  uint32_t z[NT][(NS + 3) / 4];
+  v4i a[B][4];
 };
-
-template <int TYPE, int KIND, int GROUP, int MT, int NT>
-__global__ __launch_bounds__(512) void w4_kernel(W4Args p, uint32_t ntn, int64_t blocks) {
+template <int TYPE, int KIND, int GROUP, int NT>
+__global__ __launch_bounds__(512) void w4_split_kernel(W4Args p, uint32_t ntn, int64_t blocks) {
   using E = Elem<TYPE>;
   constexpr bool INT = KIND == W4_INT, TRANS = INT && GROUP < 128, APART = INT && TYPE == MM_FP16;
   constexpr int PER = INT ? kW4Chunk / GROUP : 2;              // scales a lane has in a chunk
-  constexpr int SLOTS = MT * NT * 4;
+  using Batch = W4Batch<KIND, GROUP, NT>;
+  constexpr int B = Batch::B, NS = Batch::NS, SLOTS = 4 * NT;
   extern __shared__ float s_sum[];                             // [waves][SLOTS][64]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int64_t block = (int64_t)blockIdx.x + (int64_t)blockIdx.y * p.row_blocks;
   if (block >= blocks) return;
-  const RowTile tile = find_row_tile(p.m_splits, p.G, (uint32_t)p.M, 16 * MT, ntn, p.zero_rest, (uint32_t)block, lane);
-  if (tile.g < 0) return;
-  // a column tile's row tiles follow each other: they read the same weights
-  const uint32_t nrt = (tile.m + 16 * MT - 1) / (16 * MT);
-  const uint32_t r0 = tile.t % nrt * (16 * MT);
-  const int n0 = (int)(tile.t / nrt) * (16 * NT);
-  const int rows = (int)min(tile.m - r0, 16u * MT);
-  uint16_t* y = static_cast<uint16_t*>(p.y) + (int64_t)(tile.row0 + r0) * p.ldy;
-  if (tile.g == p.G) {
-    for (int i = threadIdx.x; i < rows * 16 * NT; i += blockDim.x)
-      if (n0 + i % (16 * NT) < p.N) y[(int64_t)(i / (16 * NT)) * p.ldy + n0 + i % (16 * NT)] = 0;
-    return;
-  }
   const int col = lane & 15, q = lane >> 4, N = p.N, K = p.K;
-  // rows and columns behind the last read the last one's values: a product's row or column reaches its own results only
-  const uint16_t* x[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) x[m] = static_cast<const uint16_t*>(p.x) + ((int64_t)(tile.row0 + r0) + min(16 * m + col, rows - 1)) * p.ldx;
+  const int chunks = (K + kW4Chunk - 1) / kW4Chunk;
+  const int first = chunks * wave / waves, last = chunks * (wave + 1) / waves;      // waves <= chunks: at least one
+  const uint16_t* x;
   const uint8_t* codes[NT];
   int64_t meta[NT];                                            // the column's first scale
+  // rows and columns behind the last read the last one's values: a product's row or column reaches its own results only
+  auto operands = [&](int g, int64_t row0, int last_row, int n0) {
+    x = static_cast<const uint16_t*>(p.x) + (row0 + min(col, last_row)) * p.ldx;
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t n = (int64_t)tile.g * N + min(n0 + 16 * j + col, N - 1);
-    codes[j] = p.codes + n * (K / 2);
-    meta[j] = n * (K / GROUP);
+    for (int j = 0; j < NT; ++j) {
+      const int64_t n = (int64_t)g * N + min(n0 + 16 * j + col, N - 1);
+      codes[j] = p.codes + n * (K / 2);
+      meta[j] = n * (K / GROUP);
+    }
+  };
+  Batch l;
+  auto load = [&](int from) {
+    const bool whole = (from + B) * kW4Chunk <= K;
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        l.w[b][j] = *reinterpret_cast<const v4i*>(codes[j] + min((from + b) * (kW4Chunk / 2) + 16 * q, K / 2 - 16));
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      if (!INT) {
+        const uint8_t* s = static_cast<const uint8_t*>(p.scales) + meta[j];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          uint16_t v;
+          __builtin_memcpy(&v, s + min((from + b) * 8 + 2 * q, K / 16 - 2), 2);
+          l.s[j][b / 2] = b % 2 ? l.s[j][b / 2] | (uint32_t)v << 16 : v;
+        }
+      } else {
+        const int at = from * PER;
+        const uint16_t* s = static_cast<const uint16_t*>(p.scales) + meta[j] + at;
+        if (whole) {
+          __builtin_memcpy(l.s[j], s, 2 * NS);
+          if (p.zeros) __builtin_memcpy(l.z[j], p.zeros + meta[j] + at, NS);
+        } else {                                               // up to K's end, the last one's again behind it
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            const int e = min(i, K / GROUP - 1 - at);
+            const uint32_t v = s[e], z = p.zeros ? p.zeros[meta[j] + at + e] : 0;
+            l.s[j][i / 2] = i % 2 ? l.s[j][i / 2] | v << 16 : v;
+            l.z[j][i / 4] = i % 4 ? l.z[j][i / 4] | z << (8 * (i % 4)) : z;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        __builtin_memcpy(&l.a[b][i], x + min((from + b) * kW4Chunk + (TRANS ? 32 * i + 8 * q : 32 * q + 8 * i), K - 8), 16);
+  };
+  const bool early = p.G == 1 && p.M <= 16 && block < ntn;
+  RowTile tile;
+  int n0, rows;
+  if (early) {
+    n0 = (int)block * (16 * NT);
+    operands(0, 0, (int)p.M - 1, n0);
+    load(first);
+    tile = RowTile{0, 0, (uint32_t)min((int64_t)max(p.m_splits[0], 0), p.M), 0};
+    rows = (int)tile.m;
+  } else {
+    tile = find_row_tile(p.m_splits, p.G, (uint32_t)p.M, 16, ntn, p.zero_rest, (uint32_t)block, lane);
+    if (tile.g < 0) return;
+    // a column tile's row tiles follow each other: they read the same weights
+    const uint32_t nrt = (tile.m + 15) / 16, r0 = tile.t % nrt * 16;
+    n0 = (int)(tile.t / nrt) * (16 * NT);
+    rows = (int)min(tile.m - r0, 16u);
+    tile.row0 += r0;
+  }
+  uint16_t* y = static_cast<uint16_t*>(p.y) + (int64_t)tile.row0 * p.ldy;
+  if (tile.g == p.G || rows == 0) {                            // rows behind the groups; all of them where the one group has none
+    const int n = n0 + (int)threadIdx.x % (16 * NT);
+    if (n < N && p.zero_rest)
+      for (int m = threadIdx.x / (16 * NT); m < (early ? (int)p.M : rows); m += blockDim.x / (16 * NT)) y[(int64_t)m * p.ldy + n] = 0;
+    return;
+  }
+  if (!early) {
+    operands(tile.g, tile.row0, rows - 1, n0);
+    load(first);
   }
   // NVFP4, bf16 rows: the largest power of two up to 1 / S goes into the block scales, so that products are
   // no larger than those of the weights themselves (above 2^-60: below it they would leave the exact values)
   const float global = INT ? 1.0f : nvfp4_global_scale(p.amax[tile.g]);
   const int down = INT || TYPE != MM_BF16 ? 0 : min(ilogbf(global) + 1, 60);
   const float downf = ldexpf(1.0f, -down);
-  v4f acc[MT][NT] = {};
-  const int chunks = (K + kW4Chunk - 1) / kW4Chunk;
-  auto load_x = [&](int c, v4i (&a)[MT][4]) {
-    const int k0 = c * kW4Chunk;
+  v4f acc[NT] = {};
+  for (int from = first; from < last; from += B) {
+    if (from > first) load(from);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int b = 0; b < B; ++b) {
+      const int k0 = (from + b) * kW4Chunk;
+      if (from + b >= last) break;
+      const bool whole = k0 + kW4Chunk <= K, have = k0 + 32 * q < K;
+      if (!TRANS && !whole)                                    // lanes behind K's end: zeros
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        __builtin_memcpy(&a[m][i], x[m] + min(k0 + (TRANS ? 32 * i + 8 * q : 32 * q + 8 * i), K - 8), 16);
-  };
-  auto load = [&](int c, W4Loads<KIND, PER, MT, NT>& l) {
-    const int k0 = c * kW4Chunk;
-    if (MT == 1) load_x(c, l.a);
-    const bool whole = k0 + kW4Chunk <= K;
+        for (int i = 0; i < 4; ++i) l.a[b][i] = have ? l.a[b][i] : v4i{0, 0, 0, 0};
+      if (APART)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      l.w[j] = *reinterpret_cast<const v4i*>(codes[j] + min(k0 / 2 + 16 * q, K / 2 - 16));
-      const int64_t at = meta[j] + k0 / GROUP;
-      if (!INT) {
-        uint16_t s;
-        __builtin_memcpy(&s, static_cast<const uint8_t*>(p.scales) + meta[j] + min(k0 / 16 + 2 * q, K / 16 - 2), 2);
-        l.s[j] = s;
-      } else if (PER == 1 || whole) {
-        const uint16_t* s = static_cast<const uint16_t*>(p.scales) + at;
-        if (PER == 4) __builtin_memcpy(&l.s[j], s, 8);
-        if (PER == 2) {
-          uint32_t v;
-          __builtin_memcpy(&v, s, 4);
-          l.s[j] = v;
-        }
-        if (PER == 1) l.s[j] = *s;
-        if (p.zeros) {
-          const uint8_t* z = p.zeros + at;
-          if (PER == 4) __builtin_memcpy(&l.z[j], z, 4);
-          if (PER == 2) {
-            uint16_t v;
-            __builtin_memcpy(&v, z, 2);
-            l.z[j] = v;
-          }
-          if (PER == 1) l.z[j] = *z;
-        }
-      } else {                                                 // the groups that there are, at least one
-        l.s[j] = 0;
-        l.z[j] = 0;
-        for (int s = 0; k0 + s * GROUP < K; ++s) {
-          l.s[j] |= (typename W4Loads<KIND, PER, MT, NT>::Scales)static_cast<const uint16_t*>(p.scales)[at + s] << (16 * s);
-          if (p.zeros) l.z[j] |= (uint32_t)p.zeros[at + s] << (8 * s);
-        }
-      }
-    }
-  };
-  auto multiply = [&](int c, W4Loads<KIND, PER, MT, NT>& l) {
-    const int k0 = c * kW4Chunk;
-    const bool whole = k0 + kW4Chunk <= K, have = k0 + 32 * q < K;
-    if (!TRANS && !whole)                                      // lanes behind K's end: zeros
+        for (int i = 0; i < 4; ++i) l.a[b][i] = pairs_apart(l.a[b][i]);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int j = 0; j < NT; ++j) {
+        const v4i v = l.w[b][j];
+        uint32_t w[4] = {(uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w};
+        if (TRANS) transpose4(w);
+        float sc[PER], zero[PER];
+        uint32_t zero2[PER];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) l.a[m][i] = have ? l.a[m][i] : v4i{0, 0, 0, 0};
-    if (APART)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) l.a[m][i] = pairs_apart(l.a[m][i]);
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      uint32_t w[4] = {(uint32_t)l.w[j].x, (uint32_t)l.w[j].y, (uint32_t)l.w[j].z, (uint32_t)l.w[j].w};
-      if (TRANS) transpose4(w);
-      float sc[PER], zero[PER];
-      uint32_t zero2[PER];
-#pragma unroll
-      for (int s = 0; s < PER; ++s) {
-        if (INT) {
-          sc[s] = E::up((uint16_t)(l.s[j] >> (16 * s)));
-          const float z = p.zeros ? (float)((l.z[j] >> (8 * s)) & 255u) : 8.0f;
-          zero[s] = -kDown<TYPE> * z;
-          zero2[s] = APART ? E::down2(-1024.0f - z, -1024.0f - z) : 0;
-        } else {
-          sc[s] = downf * (s == 0 ? __builtin_amdgcn_cvt_f32_fp8((int)l.s[j], 0) : __builtin_amdgcn_cvt_f32_fp8((int)l.s[j], 1));
-          if (!whole && !have) sc[s] = 0.0f;
-        }
-      }
-      v4f part[MT] = {};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (TRANS && !whole && k0 + 32 * i >= K) break;
-        const int s = INT ? i * 32 / GROUP : i / 2;
-        const v4i b = INT ? decode_int<TYPE>(w[i], zero[s], zero2[s]) : decode_fp4<TYPE>(w[i], sc[s]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if (!INT) {
-            acc[m][j] = E::mma16(l.a[m][i], b, acc[m][j]);
+        for (int s = 0; s < PER; ++s) {
+          const int at = b * PER + s;
+          if (INT) {
+            sc[s] = E::up((uint16_t)(l.s[j][at / 2] >> (16 * (at & 1))));
+            const uint32_t z = p.zeros ? (l.z[j][at / 4] >> (8 * (at & 3))) & 255u : 8u;
+            zero[s] = -kDown<TYPE> * (float)z;
+            zero2[s] = 0xE400E400u + z * 0x00010001u;          // fp16 -(1024 + z), z < 16
           } else {
-            part[m] = E::mma16(l.a[m][i], b, part[m]);
+            sc[s] = downf * __builtin_amdgcn_cvt_f32_fp8((int)(l.s[j][b / 2] >> (16 * (b & 1) + 8 * s)), 0);
+            if (!whole && !have) sc[s] = 0.0f;
+          }
+        }
+        v4f part = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (TRANS && !whole && k0 + 32 * i >= K) break;
+          const int s = INT ? i * 32 / GROUP : i / 2;
+          if (!INT) {
+            acc[j] = E::mma16(l.a[b][i], decode_fp4<TYPE>(w[i], sc[s]), acc[j]);
+          } else {
+            part = E::mma16(l.a[b][i], decode_int<TYPE>(w[i], zero[s], zero2[s]), part);
             if ((i + 1) * 32 % GROUP == 0) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r) acc[m][j][r] = fmaf(sc[s], part[m][r], acc[m][j][r]);
-              part[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+              for (int r = 0; r < 4; ++r) acc[j][r] = fmaf(sc[s], part[r], acc[j][r]);
+              part = v4f{0.0f, 0.0f, 0.0f, 0.0f};
             }
           }
         }
       }
     }
-  };
-  // the next chunk's loads in flight
-  W4Loads<KIND, PER, MT, NT> l0, l1;
-  int c = wave;
-  if (c < chunks) load(c, l0);
-  for (; c < chunks; c += 2 * waves) {
-    if (MT > 1) load_x(c, l0.a);
-    if (c + waves < chunks) load(c + waves, l1);
-    multiply(c, l0);
-    if (c + waves >= chunks) break;
-    if (MT > 1) load_x(c + waves, l1.a);
-    if (c + 2 * waves < chunks) load(c + 2 * waves, l0);
-    multiply(c + waves, l1);
   }
   // the waves' sums, joined in order
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) s_sum[(wave * SLOTS + (m * NT + j) * 4 + r) * 64 + lane] = acc[m][j][r];
+    for (int r = 0; r < 4; ++r) s_sum[(wave * SLOTS + 4 * j + r) * 64 + lane] = acc[j][r];
   __syncthreads();
   const float rest = ldexpf(global, -down);
   for (int s = wave; s < SLOTS; s += waves) {
     float v = s_sum[s * 64 + lane];
     for (int o = 1; o < waves; ++o) v += s_sum[(o * SLOTS + s) * 64 + lane];
     v = INT ? v * (1.0f / kDown<TYPE>) : __fdiv_rn(v, rest);
-    const int m = s / 4 / NT * 16 + 4 * q + s % 4, n = n0 + s / 4 % NT * 16 + col;
+    const int m = 4 * q + s % 4, n = n0 + s / 4 * 16 + col;
     if (m < rows && n < N) y[(int64_t)m * p.ldy + n] = E::down(v);
   }
 }
@@ -517,14 +518,14 @@ __global__ __launch_bounds__(64 * WAVES) void w4_wide_kernel(W4Args p, uint32_t 
 }
 
 // ----------------------------------------------------------------------------- launches
-template <int TYPE, int KIND, int GROUP, int MT, int NT>
+template <int TYPE, int KIND, int GROUP, int NT>
 static hipError_t run_split(W4Args p, hipStream_t s) {
-  const int64_t ntn = (p.N + 16 * NT - 1) / (16 * NT), blocks = sizes::row_tiles_bound(p.M, p.G, 16 * MT) * ntn;
-  const int waves = sizes::w4_waves(blocks, p.K);
+  const int64_t ntn = (p.N + 16 * NT - 1) / (16 * NT), blocks = sizes::row_tiles_bound(p.M, p.G, 16) * ntn;
+  const int waves = sizes::w4_waves(p.K);
   const FoldedGrid g = fold_grid(blocks, 64 * waves);
   p.row_blocks = g.x;
-  hipLaunchKernelGGL((w4_kernel<TYPE, KIND, GROUP, MT, NT>), dim3(g.x, g.y), dim3(64 * waves), (size_t)waves * MT * NT * 4 * 64 * sizeof(float),
-                     s, p, (uint32_t)ntn, blocks);
+  hipLaunchKernelGGL((w4_split_kernel<TYPE, KIND, GROUP, NT>), dim3(g.x, g.y), dim3(64 * waves), (size_t)waves * NT * 4 * 64 * sizeof(float), s, p,
+                     (uint32_t)ntn, blocks);
   return hipGetLastError();
 }
 template <int TYPE, int KIND, int GROUP, int MT, int SPAN, int WAVES>
@@ -539,10 +540,14 @@ static hipError_t run_wide(W4Args p, hipStream_t s) {
 template <int TYPE, int KIND, int GROUP>
 static hipError_t run_w4(const W4Args& p, hipStream_t s) {
   constexpr int SPAN = 4;
+  // 16 x 16 tiles: eight a CU, a wave each, fill the device (64 rows over 128 experts of 4096 x 7168, NVFP4: 165 us in spans, 232 as few tiles)
   const int64_t waves = sizes::row_tiles_bound(p.M, p.G, 16) * ((p.N + 15) / 16);
-  if (waves < 2048 || p.K < SPAN * kW4Chunk) return run_split<TYPE, KIND, GROUP, 1, 1>(p, s);
+  if (waves < 2048 || p.K < SPAN * kW4Chunk)
+    return p.M / p.G > 4 && waves >= 512 ? run_split<TYPE, KIND, GROUP, 4>(p, s) : run_split<TYPE, KIND, GROUP, 1>(p, s);
   if (p.M / p.G <= 16) return run_wide<TYPE, KIND, GROUP, 1, SPAN, 4>(p, s);
-  return run_wide<TYPE, KIND, GROUP, 4, SPAN, 8>(p, s);
+  // 512 rows in 8 groups of 4096 x 4096 by tiles of 64 / 32 rows: groups of 128 80 / 88 us; groups of 64 (whose larger tiles spill)
+  // 146 / 93, of 32 343 / 105
+  return run_wide<TYPE, KIND, GROUP, KIND == W4_INT && GROUP < 128 ? 2 : 4, SPAN, 8>(p, s);
 }
 template <int TYPE>
 static hipError_t run_w4(const W4Args& p, hipStream_t s) {

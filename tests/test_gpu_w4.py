@@ -233,6 +233,19 @@ def test_no_rows_and_determinism():
         assert torch.equal(ref, g.grouped_matmul_w4(x, w, m))
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_one_group_short_of_the_rows(kind):
+    """A dense layer's split size may say less than all rows, down to none."""
+    w = _make(kind, 1, 50, 256, torch.bfloat16)
+    x = randn((9, 256), torch.bfloat16, 3)
+    for m in (9, 4, 0, -2, 100):
+        _check(x, w, kind, [m])
+        out = torch.full((9, 50), 7.0, dtype=torch.bfloat16, device="cuda")
+        g.grouped_matmul_w4(x.cuda(), _handle(w, kind), torch.tensor([m], dtype=torch.int32, device="cuda"), out=out)
+        assert bool((out[max(m, 0):] == 7.0).all()) and (m <= 0 or not bool((out[:m] == 7.0).all()))
+    _check(randn((40, 256), torch.bfloat16, 3), w, kind, [17])
+
+
 def test_graph_replays_and_two_streams():
     a, b = (_make("64", 6, 300, 1024, torch.bfloat16, s) for s in (1, 3))
     x = randn((33, 1024), torch.bfloat16, 5).cuda()
