@@ -196,6 +196,56 @@ def test_strided_and_transposed_logits(dt):
     _check(logits[:1].expand(5, 50), 4, "sigmoid", dev_logits=logits[:1].cuda().expand(5, 50))
 
 
+def _sorted_choice(logits, k, score, bias, groups, top, best):
+    """The choice for many rows by stable sorts in 64 bits on the device (finite logits)."""
+    l = logits.double()
+    T, E = l.shape
+    s = torch.sigmoid(l) if score == "sigmoid" else torch.softmax(l, 1)
+    c = s + bias.double() if bias is not None else s
+    order = c if bias is not None else l
+    if groups > 1:
+        by = c if bias is not None or best > 1 else l
+        value = by.view(T, groups, -1).sort(dim=2, descending=True).values[:, :, :best].sum(2)
+        at = value.sort(dim=1, descending=True, stable=True).indices[:, :top]
+        keep = torch.zeros((T, groups), dtype=torch.bool, device=l.device).scatter_(1, at, True)
+        order = order.masked_fill(~keep.repeat_interleave(E // groups, 1), -math.inf)
+    return order.sort(dim=1, descending=True, stable=True).indices[:, :k].to(torch.int32)
+
+
+@pytest.mark.parametrize("spread", ["wide", "crowded", "equal"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,top,best", [(128, 8, 1, 1, 1), (256, 8, 1, 1, 1), (256, 8, 8, 4, 2), (64, 15, 1, 1, 1), (256, 6, 8, 3, 1),
+                                                 (512, 10, 1, 1, 1), (1024, 20, 16, 4, 2), (16, 1, 1, 1, 1), (16, 15, 1, 1, 1)])
+def test_many_rows_against_sorts_in_64_bits(E, k, groups, top, best, score, spread):
+    """wide: as routers give them; crowded: values within a few hundred roundings of each other, some equal; equal: few values."""
+    print(f"route many E={E} k={k} groups={groups} {score} {spread}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    T = 20000
+    r = torch.randn((T, E), generator=gen, device="cuda")
+    if spread == "crowded":
+        r = 1.0 + torch.randint(0, 300, (T, E), generator=gen, device="cuda") * 2.0 ** -23 + torch.randint(0, 3, (T, 1), generator=gen, device="cuda")
+    elif spread == "equal":
+        r = torch.randint(-2, 3, (T, E), generator=gen, device="cuda").float()
+    small = 0.2 * torch.randn(E, generator=gen, device="cuda")
+    # a softmax in torch and one here differ by 2^-50: sums that near each other are left to the tests of single rows
+    for bias in (None, small, small * 2.0 ** -20) if score == "sigmoid" or spread == "wide" else (None,):
+        if groups > 1 and best > 1 and spread != "wide" and score == "softmax":
+            continue
+        for dt in (torch.float32, torch.bfloat16):
+            l = r.to(dt)
+            got, _ = g.route_forward(l, k, score, bias=bias, groups=groups, top_groups=top, group_best=best)
+            want = _sorted_choice(l, k, score, bias, groups, top, best)
+            bad = (got != want).any(1)
+            if bool(bad.any()):
+                # 1 / (1 + exp) here and in torch may round differently in the last of 64 bits: only sums that near may differ
+                rows = bad.nonzero()[:, 0]
+                assert rows.numel() <= 3, (rows.numel(), rows[:4], got[rows[0]], want[rows[0]])
+                s = torch.sigmoid(l[rows].double()) if score == "sigmoid" else torch.softmax(l[rows].double(), 1)
+                c = s + (bias.double() if bias is not None else 0)
+                a, b = c.gather(1, got[rows].long()), c.gather(1, want[rows].long())
+                assert bool(((a - b).abs() <= 2.0 ** -50).all()), (got[rows[0]], want[rows[0]])
+
+
 def test_no_tokens():
     e, p = g.route_forward(torch.empty((0, 8), device="cuda"), 2)
     assert e.shape == (0, 2) and p.shape == (0, 2)
