@@ -17,8 +17,7 @@ import functools
 import torch
 
 from . import _SIGS, _check, _dev_ptr, lib
-from .matmul import (_CODES, _DTYPES, _check_rows_out, _dtype16, _ld, _no_overlap, _packer, _row_major, _run, _same, _written,
-                     once_differentiable)
+from .matmul import _CODES, _check_rows_out, _dtype16, _ld, _no_overlap, _packer, _row_major, _run, _written, once_differentiable
 
 _CODES.setdefault(ctypes.c_float, "f")
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
@@ -60,101 +59,97 @@ def _ws_bytes(T, H):
     return need.value
 
 
-def _ptr(t):
-    return t.data_ptr() if t is not None else 0
-
-
-def _ld0(t):
-    return _ld(t) if t is not None else 0
-
-
-def _is_fp32(t):
-    return t is not None and t.dtype == torch.float32
-
-
-def _param(t, x, name):
-    """A vector of H parameters, of x's type or fp32."""
+# A decode step's norm takes 4.5 us on the device, so the checks below ask each tensor for each property once.
+def _param(t, H, dt, dev, name):
+    """A vector of H parameters, of the rows' type or fp32: (the tensor to keep, its address, fp32 or not)."""
     if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or t.dtype not in (x.dtype, torch.float32):
-        raise TypeError(f"{name}: a {x.dtype} or fp32 tensor is required, got {getattr(t, 'dtype', type(t).__name__)}")
-    if t.dim() != 1 or t.shape[0] != x.shape[1]:
-        raise ValueError(f"{name}: {x.shape[1]} elements expected (rows of x), got {tuple(t.shape)}")
-    if t.device != x.device:
-        raise ValueError(f"{name}: on {t.device}, the other tensors are on {x.device}")
-    return t.contiguous()
+        return None, 0, 0
+    if not isinstance(t, torch.Tensor) or (t.dtype is not dt and t.dtype is not torch.float32):
+        raise TypeError(f"{name}: a {dt} or fp32 tensor is required, got {getattr(t, 'dtype', type(t).__name__)}")
+    if tuple(t.shape) != (H,):
+        raise ValueError(f"{name}: {H} elements expected (rows of x), got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, the other tensors are on {dev}")
+    if not t.is_contiguous():
+        t = t.contiguous()
+    return t, t.data_ptr(), t.dtype is torch.float32
 
 
-def _gate(gate, x):
-    """(kind, the gate as the kernels address it, its row stride)."""
+def _gate(gate, T, H, dt, dev):
+    """(kind, the gate as the kernels address it, its address, fp32 or not, its row stride)."""
     if gate is None:
-        return GATE_NONE, None, 0
+        return GATE_NONE, None, 0, 0, 0
     if isinstance(gate, torch.Tensor) and gate.dim() == 1:
-        return GATE_CHANNEL, _param(gate, x, "gate"), 0
-    T, H = x.shape
-    if not isinstance(gate, torch.Tensor) or gate.dtype not in (x.dtype, torch.float32):
-        raise TypeError(f"gate: a {x.dtype} or fp32 tensor is required, got {getattr(gate, 'dtype', type(gate).__name__)}")
-    if gate.device != x.device:
-        raise ValueError(f"gate: on {gate.device}, the other tensors are on {x.device}")
+        return (GATE_CHANNEL, *_param(gate, H, dt, dev, "gate"), 0)
+    if not isinstance(gate, torch.Tensor) or gate.dtype not in (dt, torch.float32):
+        raise TypeError(f"gate: a {dt} or fp32 tensor is required, got {getattr(gate, 'dtype', type(gate).__name__)}")
+    if gate.device != dev:
+        raise ValueError(f"gate: on {gate.device}, the other tensors are on {dev}")
     if tuple(gate.shape) == (T, 1):
         if T > 1 and gate.stride(0) < 1:
             gate = gate.contiguous()
-        return GATE_TOKEN, gate, gate.stride(0) if T > 1 else 1
+        return GATE_TOKEN, gate, gate.data_ptr(), gate.dtype is torch.float32, gate.stride(0) if T > 1 else 1
     if tuple(gate.shape) != (T, H):
         raise ValueError(f"gate: shape [{H}], [{T}, 1] or [{T}, {H}] expected, got {tuple(gate.shape)}")
     gate = _row_major(gate)
-    return GATE_FULL, gate, _ld(gate)
+    return GATE_FULL, gate, gate.data_ptr(), gate.dtype is torch.float32, _ld(gate)
 
 
-def _rows(t, x, name):
-    """Rows beside x's: of its type, device and shape."""
+def _rows(t, shape, dt, dev, name):
+    """Rows beside x's, of its type, device and shape: (the tensor to keep, its address, its row stride)."""
     if t is None:
-        return None
-    _same(t, x, 2, name)
-    if t.shape != x.shape:
-        raise ValueError(f"{name}: shape {tuple(x.shape)} expected, got {tuple(t.shape)}")
-    return _row_major(t)
+        return None, 0, 0
+    if not isinstance(t, torch.Tensor) or t.dtype is not dt:
+        raise TypeError(f"{name}: a {dt} tensor is required, got {getattr(t, 'dtype', type(t).__name__)}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, the other tensors are on {dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t, t.data_ptr(), shape[1]
+    t = _row_major(t)
+    return t, t.data_ptr(), _ld(t)
 
 
-class _Inputs:
-    """The checked inputs of a call, and their fields of NormInputs."""
-
-    def __init__(self, x, branch, weight, branch_weight, gate, scale, eps):
-        _dtype16(x, "x")
-        if x.dim() != 2:
-            raise ValueError(f"x: 2 dimensions expected, got {x.dim()}")
-        self.branch = _rows(branch, x, "branch")
-        self.weight = _param(weight, x, "weight")
-        self.branch_weight = _param(branch_weight, x, "branch_weight")
-        self.kind, self.gate, ldg = _gate(gate, x)
+def _inputs(x, branch, weight, branch_weight, gate, scale, eps):
+    """(the fields of NormInputs, the tensors that they address: x, branch, weight, branch_weight, gate, x's device and shape)."""
+    code = _dtype16(x, "x")
+    dt, dev, shape = x.dtype, x.device, x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x: 2 dimensions expected, got {len(shape)}")
+    T, H = shape
+    branch, pb, ldb = _rows(branch, shape, dt, dev, "branch")
+    weight, pw, w32 = _param(weight, H, dt, dev, "weight")
+    branch_weight, pbw, bw32 = _param(branch_weight, H, dt, dev, "branch_weight")
+    kind, gate, pg, g32, ldg = _gate(gate, T, H, dt, dev)
+    if dev.type != "cuda":
         _dev_ptr(x, "x")                                             # refuses host tensors
-        self.x = _row_major(x)
-        self.fields = (_DTYPES[x.dtype], self.kind, _is_fp32(self.weight), _is_fp32(self.branch_weight), _is_fp32(self.gate),
-                       eps, scale, x.shape[0], x.shape[1], self.x.data_ptr(), _ld(self.x), _ptr(self.branch),
-                       _ld0(self.branch), _ptr(self.weight), _ptr(self.branch_weight), _ptr(self.gate), ldg)
+    x, px, ldx = _rows(x, shape, dt, dev, "x")
+    return ((code, kind, w32, bw32, g32, eps, scale, T, H, px, ldx, pb, ldb, pw, pbw, pg, ldg),
+            (x, branch, weight, branch_weight, gate), dev, shape)
 
 
 def residual_norm_forward(x, branch, weight=None, branch_weight=None, gate=None, scale=1.0, eps=1e-6, out=None):
     """(y, h, stats): y and h [T, H] in x's dtype (h None without weight; y is x without branch), stats for
     residual_norm_backward.  out: y is written there; it may be x or branch itself (in place)."""
-    i = _Inputs(x, branch, weight, branch_weight, gate, scale, eps)
-    y = x
+    fields, kept, dev, shape = _inputs(x, branch, weight, branch_weight, gate, scale, eps)
+    T, H = shape
+    y, py, ldy = x, 0, H
     if out is not None:
-        _check_rows_out(out, x.shape, x, "out")
+        _check_rows_out(out, shape, x, "out")
         if branch is None:
             raise ValueError("out: without a branch, y is x")
         _no_overlap(out, "out", weight=weight, branch_weight=branch_weight, gate=gate,
-                    **{n: t for n, t in (("x", i.x), ("branch", i.branch))
+                    **{n: t for n, t in (("x", kept[0]), ("branch", kept[1]))
                        if t.data_ptr() != out.data_ptr() or _ld(t) != _ld(out)})
-        y = out
+        y, py, ldy = out, out.data_ptr(), _ld(out)
     elif branch is not None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    h = torch.empty(x.shape, dtype=x.dtype, device=x.device) if weight is not None else None
-    stats = torch.empty((2, x.shape[0]), dtype=torch.float32, device=x.device)
-    if x.shape[0] == 0:
-        return y, h, stats
-    args = _pack_fwd(*i.fields, y.data_ptr() if branch is not None else 0, _ld(y), _ptr(h), x.shape[1], stats.data_ptr())
-    _run(lib().gmlp_residual_norm, args, x.device)
+        y = torch.empty(shape, dtype=x.dtype, device=dev)
+        py = y.data_ptr()
+    h = torch.empty(shape, dtype=x.dtype, device=dev) if weight is not None else None
+    stats = torch.empty((2, T), dtype=torch.float32, device=dev)
+    if T > 0:
+        _run(lib().gmlp_residual_norm, _pack_fwd(*fields, py, ldy, h.data_ptr() if h is not None else 0, H, stats.data_ptr()), dev)
     return y if out is None else _written(out), h, stats
 
 
@@ -163,27 +158,26 @@ def residual_norm_backward(dy, dh, x, branch, stats, weight=None, branch_weight=
     """{"dx", "dbranch", "dweight", "dbranch_weight", "dgate"} (None where there is no such input or it is
     not needed) from the gradients of y (None: zeros) and h (None without weight) and a forward's inputs and
     stats.  The inputs must be as the forward had them: not after an in-place forward."""
-    i = _Inputs(x, branch, weight, branch_weight, gate, scale, eps)
-    T, H = x.shape
-    dev = x.device
-    dy, dh = _rows(dy, x, "dy"), _rows(dh, x, "dh")
+    fields, kept, dev, shape = _inputs(x, branch, weight, branch_weight, gate, scale, eps)
+    T, H = shape
+    dy, pdy, lddy = _rows(dy, shape, x.dtype, dev, "dy")
+    dh, pdh, lddh = _rows(dh, shape, x.dtype, dev, "dh")
     if (dh is None) != (weight is None):
         raise ValueError("dh: goes with a weight")
-    if not isinstance(stats, torch.Tensor) or stats.dtype != torch.float32 or tuple(stats.shape) != (2, T) \
+    if not isinstance(stats, torch.Tensor) or stats.dtype is not torch.float32 or tuple(stats.shape) != (2, T) \
             or not stats.is_contiguous() or stats.device != dev:
         raise ValueError(f"stats: the fp32 tensor [2, {T}] of a residual_norm_forward is required")
-
-    def like(t, need):
-        return torch.empty(t.shape, dtype=t.dtype, device=dev) if need and t is not None else None
-    dx, db = like(x, need_dx), like(branch, need_dbranch)
-    dw, dbw, dg = like(weight, need_dweight), like(branch_weight, need_dbranch_weight), like(gate, need_dgate)
-    res = {"dx": dx, "dbranch": db, "dweight": dw, "dbranch_weight": dbw, "dgate": dg}
+    res, ptrs = {}, {}
+    for name, t, wanted in (("dx", x, need_dx), ("dbranch", branch, need_dbranch), ("dweight", weight, need_dweight),
+                            ("dbranch_weight", branch_weight, need_dbranch_weight), ("dgate", gate, need_dgate)):
+        r = torch.empty(t.shape, dtype=t.dtype, device=dev) if wanted and t is not None else None
+        res[name], ptrs[name] = r, r.data_ptr() if r is not None else 0
     if T == 0:                                                       # sums over no rows
-        return {k: t.zero_() if t is not None else None for k, t in res.items()}
+        return {k: r.zero_() if r is not None else None for k, r in res.items()}
     need = _ws_bytes(T, H)
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    args = _pack_bwd(*i.fields, _ptr(dy), _ld0(dy), _ptr(dh), _ld0(dh), stats.data_ptr(), _ptr(dx), H, _ptr(db), H, _ptr(dg),
-                     _ptr(dw), _ptr(dbw), ws.data_ptr(), need)
+    args = _pack_bwd(*fields, pdy, lddy, pdh, lddh, stats.data_ptr(), ptrs["dx"], H, ptrs["dbranch"], H, ptrs["dgate"], ptrs["dweight"],
+                     ptrs["dbranch_weight"], ws.data_ptr(), need)
     _run(lib().gmlp_residual_norm_backward, args, dev)
     return res
 
