@@ -264,6 +264,9 @@ __global__ __launch_bounds__(MAXT) void norm_backward_kernel(NormArgs p) {
       yh[i] = fmaf(gt, GATE == BWD_GATE_NONE ? n[i] : g[i] * n[i], x[i]) * ry;
       u[i] = dh[i] * w[i];
     }
+    if (!p.weight)                       // what is not finite in y stays out of the gradients that do not have it
+#pragma unroll
+      for (int i = 0; i < 4; ++i) yh[i] = 0.0f;
   };
   const float inv_h = 1.0f / (float)H;
   int turn = 0;
@@ -301,8 +304,9 @@ __global__ __launch_bounds__(MAXT) void norm_backward_kernel(NormArgs p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float gn = GATE == BWD_GATE_NONE ? n[i] : g[i] * n[i];
-          s.uy = fmaf(u[i], yh[i], s.uy);
           s.ndy = fmaf(gn, dy[i], s.ndy);
+          if (!p.weight) continue;
+          s.uy = fmaf(u[i], yh[i], s.uy);
           s.nu = fmaf(gn, u[i], s.nu);
           s.ny = fmaf(gn, yh[i], s.ny);
         }
@@ -323,7 +327,7 @@ __global__ __launch_bounds__(MAXT) void norm_backward_kernel(NormArgs p) {
       s.ny += o.ny;
     }
     const float c1 = s.uy * inv_h;
-    const float gnd = s.ndy + ry * (s.nu - c1 * s.ny);         // sum of g n d
+    const float gnd = p.weight ? s.ndy + ry * (s.nu - c1 * s.ny) : s.ndy;      // sum of g n d
     const float c2 = post ? gt * gnd * inv_h : 0.0f;
     if (p.dgate && p.gate_kind == GATE_TOKEN && tid == 0) store1p<TYPE>(p.dgate, p.gate_fp32, t, p.scale * gnd);
 #pragma unroll
@@ -349,8 +353,10 @@ __global__ __launch_bounds__(MAXT) void norm_backward_kernel(NormArgs p) {
           if (GATE == BWD_GATE_CHANNEL) ag[c][4 * half + i] += n[i];
           d[i] = GATE == BWD_GATE_NONE ? q : q * g[i];
           ab[c][4 * half + i] = fmaf(d[i], bh[i], ab[c][4 * half + i]);
-          d[i] = rb * fmaf(-bh[i], c2, d[i] * wb[i]);
         }
+        if (post)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[i] = rb * fmaf(-bh[i], c2, d[i] * wb[i]);
         db[2 * half] = (int)Elem<TYPE>::down2(d[0], d[1]);
         db[2 * half + 1] = (int)Elem<TYPE>::down2(d[2], d[3]);
         if (GATE == BWD_GATE_FULL) {

@@ -37,18 +37,36 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
   w[3] = d.y;
 }
 
-// Sums of bf16 rows are kept 2^-12 as large as they are until the end, so that those of the largest rows with
-// integers up to 15 stay in fp32 (fp16 rows are far from its end).
-template <int TYPE>
-constexpr float kDown = TYPE == MM_BF16 ? 0x1p-12f : 1.0f;
-// Eight codes -> eight integers q - zero, times kDown, exact in 16 bits (zero: times -kDown; fp16: the pair
-// of -(1024 + zero)).  fp16 takes the pairs k, k + 4 that a mask leaves in one word: 1024 + q is a number whose last
-// bits are q, and 1024 + 16 q the same four bits higher, so a mask, an or and one addition (or one product with
-// 1/16 and addition) of pairs do; x's operand is then in that order too (pairs_apart).
-template <int TYPE>
-__device__ __forceinline__ v4i decode_int(uint32_t w, float zero, uint32_t zero2) {
-  if constexpr (TYPE == MM_FP16) {
-    const v2h low = __builtin_bit_cast(v2h, zero2);
+// What a group's codes and sums are multiplied by (s16: the scale's bits in the rows' type R).
+//   fp16 operands: zero2 = the pair of -(1024 + zero), sc the scale.
+//   bf16 operands: the scale's power of two goes into the integers (exact: they have 5 bits) and the rest, in [1, 2),
+//   multiplies their sum, so that sums of the largest and the smallest rows are as large as the result's parts are; the
+//   power stays within 2^-126 and 2^123, where 15 times it is a number.
+struct IntGroup {
+  float sc, pow, zero;
+  uint32_t zero2;
+};
+template <int R, int U>
+__device__ __forceinline__ IntGroup int_group(uint32_t s16, uint32_t z) {
+  IntGroup o{Elem<R>::up((uint16_t)s16), 1.0f, 0.0f, 0u};
+  if constexpr (U == MM_FP16) {
+    o.zero2 = 0xE400E400u + z * 0x00010001u;
+  } else {
+    const uint32_t e = min(max((s16 >> 7) & 255u, 1u), 250u);
+    o.pow = __uint_as_float(e << 23);
+    o.sc *= __uint_as_float((254u - e) << 23);
+    o.zero = -o.pow * (float)z;
+  }
+  return o;
+}
+// Eight codes -> eight integers q - zero (bf16: times the group's power of two), exact in 16 bits.  fp16 takes the pairs
+// k, k + 4 that a mask leaves in one word: 1024 + q is a number whose last bits are q, and 1024 + 16 q the same four
+// bits higher, so a mask, an or and one addition (or one product with 1/16 and addition) of pairs do; x's operand
+// is then in that order too (pairs_apart).
+template <int U>
+__device__ __forceinline__ v4i decode_int(uint32_t w, const IntGroup& g) {
+  if constexpr (U == MM_FP16) {
+    const v2h low = __builtin_bit_cast(v2h, g.zero2);
     const v2h high = low + v2h{(_Float16)960, (_Float16)960};             // -(64 + zero)
     const v2h sixteenth{(_Float16)0.0625f, (_Float16)0.0625f};
     v4i o;
@@ -63,7 +81,7 @@ __device__ __forceinline__ v4i decode_int(uint32_t w, float zero, uint32_t zero2
   }
   const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
   auto pair = [&](int at) {
-    return (int)Elem<TYPE>::down2(fmaf((float)((even >> at) & 255u), kDown<TYPE>, zero), fmaf((float)((odd >> at) & 255u), kDown<TYPE>, zero));
+    return (int)Elem<U>::down2(fmaf((float)((even >> at) & 255u), g.pow, g.zero), fmaf((float)((odd >> at) & 255u), g.pow, g.zero));
   };
   return v4i{pair(0), pair(8), pair(16), pair(24)};
 }
@@ -204,7 +222,7 @@ __global__ __launch_bounds__(512) void w4_split_kernel(W4Args p, uint32_t ntn, i
   // NVFP4, bf16 rows: the largest power of two up to 1 / S goes into the block scales, so that products are
   // no larger than those of the weights themselves (above 2^-60: below it they would leave the exact values)
   const float global = INT ? 1.0f : nvfp4_global_scale(p.amax[tile.g]);
-  const int down = INT || TYPE != MM_BF16 ? 0 : min(ilogbf(global) + 1, 60);
+  const int down = INT || TYPE != MM_BF16 ? 0 : min(max(ilogbf(global), -126), 59) + 1;
   const float downf = ldexpf(1.0f, -down);
   v4f acc[NT] = {};
   for (int from = first; from < last; from += B) {
@@ -225,16 +243,13 @@ __global__ __launch_bounds__(512) void w4_split_kernel(W4Args p, uint32_t ntn, i
         const v4i v = l.w[b][j];
         uint32_t w[4] = {(uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w};
         if (TRANS) transpose4(w);
-        float sc[PER], zero[PER];
-        uint32_t zero2[PER];
+        float sc[PER];
+        IntGroup grp[PER];
 #pragma unroll
         for (int s = 0; s < PER; ++s) {
           const int at = b * PER + s;
           if (INT) {
-            sc[s] = E::up((uint16_t)(l.s[j][at / 2] >> (16 * (at & 1))));
-            const uint32_t z = p.zeros ? (l.z[j][at / 4] >> (8 * (at & 3))) & 255u : 8u;
-            zero[s] = -kDown<TYPE> * (float)z;
-            zero2[s] = 0xE400E400u + z * 0x00010001u;          // fp16 -(1024 + z), z < 16
+            grp[s] = int_group<TYPE, TYPE>((l.s[j][at / 2] >> (16 * (at & 1))) & 0xFFFFu, p.zeros ? (l.z[j][at / 4] >> (8 * (at & 3))) & 255u : 8u);
           } else {
             sc[s] = downf * __builtin_amdgcn_cvt_f32_fp8((int)(l.s[j][b / 2] >> (16 * (b & 1) + 8 * s)), 0);
             if (!whole && !have) sc[s] = 0.0f;
@@ -248,10 +263,10 @@ __global__ __launch_bounds__(512) void w4_split_kernel(W4Args p, uint32_t ntn, i
           if (!INT) {
             acc[j] = E::mma16(l.a[b][i], decode_fp4<TYPE>(w[i], sc[s]), acc[j]);
           } else {
-            part = E::mma16(l.a[b][i], decode_int<TYPE>(w[i], zero[s], zero2[s]), part);
+            part = E::mma16(l.a[b][i], decode_int<TYPE>(w[i], grp[s]), part);
             if ((i + 1) * 32 % GROUP == 0) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r) acc[j][r] = fmaf(sc[s], part[r], acc[j][r]);
+              for (int r = 0; r < 4; ++r) acc[j][r] = fmaf(grp[s].sc, part[r], acc[j][r]);
               part = v4f{0.0f, 0.0f, 0.0f, 0.0f};
             }
           }
@@ -269,7 +284,7 @@ __global__ __launch_bounds__(512) void w4_split_kernel(W4Args p, uint32_t ntn, i
   for (int s = wave; s < SLOTS; s += waves) {
     float v = s_sum[s * 64 + lane];
     for (int o = 1; o < waves; ++o) v += s_sum[(o * SLOTS + s) * 64 + lane];
-    v = INT ? v * (1.0f / kDown<TYPE>) : __fdiv_rn(v, rest);
+    if (!INT) v = __fdiv_rn(v, rest);
     const int m = 4 * q + s % 4, n = n0 + s / 4 * 16 + col;
     if (m < rows && n < N) y[(int64_t)m * p.ldy + n] = E::down(v);
   }
@@ -338,7 +353,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_wide_kernel(W4Args p, uint32_t 
   const uint8_t* codes = p.codes + n * (K / 2);
   const int64_t meta = n * (K / GROUP);
   const float global = INT ? 1.0f : nvfp4_global_scale(p.amax[tile.g]);
-  const int down = INT || TYPE != MM_BF16 ? 0 : min(ilogbf(global) + 1, 60);
+  const int down = INT || TYPE != MM_BF16 ? 0 : min(max(ilogbf(global), -126), 59) + 1;
   const float downf = ldexpf(1.0f, -down);
   const int spans = K / SK, chunks = (K + kW4Chunk - 1) / kW4Chunk;
 
@@ -381,15 +396,15 @@ __global__ __launch_bounds__(64 * WAVES) void w4_wide_kernel(W4Args p, uint32_t 
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = (int)F::down2(f[2 * j] * up, f[2 * j + 1] * up);
-        if (lane == 0) s_factor[s & 1][at % PIECES / 64][row] = ldexpf(INT ? kDown<TYPE> : downf, -e);
+        if (lane == 0) s_factor[s & 1][at % PIECES / 64][row] = INT ? ldexpf(1.0f, -e) : ldexpf(downf, -e);
       }
       *reinterpret_cast<v4i*>(s_x + ((s & 1) * ROWS + row) * XLD + at % PIECES * 8) = APART ? pairs_apart(v) : v;
     }
   };
   v4f acc[MT] = {}, sum[MT];
-  // one chunk into `to`: a(m, i) gives x's operand, w the codes, sc and zero the scales of the chunk's groups
-  // (NVFP4: of the lane's two blocks); products of k >= K are left out (live of the four)
-  auto multiply = [&](auto type, v4f (&to)[MT], auto a, v4i codes4, const float* sc, const float* zero, const uint32_t* zero2, int live) {
+  // one chunk into `to`: a(m, i) gives x's operand, w the codes, grp the chunk's groups (NVFP4: sc the scales of the
+  // lane's two blocks); products of k >= K are left out (live of the four)
+  auto multiply = [&](auto type, v4f (&to)[MT], auto a, v4i codes4, const float* sc, const IntGroup* grp, int live) {
     constexpr int U = decltype(type)::value;
     uint32_t w[4] = {(uint32_t)codes4.x, (uint32_t)codes4.y, (uint32_t)codes4.z, (uint32_t)codes4.w};
     if (TRANS) transpose4(w);
@@ -398,7 +413,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_wide_kernel(W4Args p, uint32_t 
     for (int i = 0; i < 4; ++i) {
       if (i >= live) break;
       const int s = INT ? i * 32 / GROUP : i / 2;
-      const v4i b = INT ? decode_int<U>(w[i], zero[s], zero2[s]) : decode_fp4<U>(w[i], sc[s]);
+      const v4i b = INT ? decode_int<U>(w[i], grp[s]) : decode_fp4<U>(w[i], sc[s]);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (!INT) {
@@ -407,7 +422,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_wide_kernel(W4Args p, uint32_t 
           part[m] = Elem<U>::mma16(a(m, i), b, part[m]);
           if ((i + 1) * 32 % GROUP == 0) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) to[m][r] = fmaf(sc[s], part[m][r], to[m][r]);
+            for (int r = 0; r < 4; ++r) to[m][r] = fmaf(grp[s].sc, part[m][r], to[m][r]);
             part[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
           }
         }
@@ -415,12 +430,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_wide_kernel(W4Args p, uint32_t 
     }
   };
   constexpr int PER = INT ? kW4Chunk / GROUP : 2;
-  auto int_scales = [&](uint32_t s16, uint32_t z8, float& sc, float& zero, uint32_t& zero2) {
-    sc = E::up((uint16_t)s16);
-    const uint32_t z = p.zeros ? z8 & 255u : 8u;
-    zero = -kDown<TYPE> * (float)z;
-    zero2 = 0xE400E400u + z * 0x00010001u;                     // fp16 -(1024 + z), z < 16
-  };
+  auto zero_of = [&](uint32_t z8) { return p.zeros ? z8 & 255u : 8u; };
   int row_at[MT];                                              // rows behind the last read the last one's
 #pragma unroll
   for (int m = 0; m < MT; ++m) row_at[m] = min(16 * m + col, rows - 1) * XLD;
@@ -434,16 +444,16 @@ __global__ __launch_bounds__(64 * WAVES) void w4_wide_kernel(W4Args p, uint32_t 
       if (SCALED && c % 4 == 0)
 #pragma unroll
         for (int m = 0; m < MT; ++m) sum[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      float sc[PER], zero[PER];
-      uint32_t zero2[PER];
+      float sc[PER];
+      IntGroup grp[PER];
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int at = c * PER + i;
-        if (INT) int_scales(l.s[at / 2] >> (16 * (at & 1)), l.z[INT ? at / 4 : 0] >> (8 * (at & 3)), sc[i], zero[i], zero2[i]);
+        if (INT) grp[i] = int_group<TYPE, T>((l.s[at / 2] >> (16 * (at & 1))) & 0xFFFFu, zero_of(l.z[INT ? at / 4 : 0] >> (8 * (at & 3))));
         else sc[i] = (SCALED ? 1.0f : downf) * __builtin_amdgcn_cvt_f32_fp8((int)((l.s[c / 2] >> (16 * (c & 1))) >> (8 * i)), 0);
       }
       multiply(std::integral_constant<int, T>{}, SCALED ? sum : acc, [&](int m, int i) { return *reinterpret_cast<const v4i*>(xs + row_at[m] + c * kW4Chunk + (TRANS ? 32 * i + 8 * q : 32 * q + 8 * i)); },
-               l.w[c], sc, zero, zero2, 4);
+               l.w[c], sc, grp, 4);
       if (SCALED && c % 4 == 3)
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -493,26 +503,26 @@ __global__ __launch_bounds__(64 * WAVES) void w4_wide_kernel(W4Args p, uint32_t 
         if (!TRANS) v = k < K ? v : v4i{0, 0, 0, 0};
         a[m][i] = APART && TYPE == MM_FP16 ? pairs_apart(v) : v;
       }
-    float sc[PER], zero[PER];
-    uint32_t zero2[PER];
+    float sc[PER];
+    IntGroup grp[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       if (INT) {
         const int64_t at = meta + min((k0 + i * GROUP) / GROUP, K / GROUP - 1);
-        int_scales(static_cast<const uint16_t*>(p.scales)[at], p.zeros ? p.zeros[at] : 0, sc[i], zero[i], zero2[i]);
+        grp[i] = int_group<TYPE, TYPE>(static_cast<const uint16_t*>(p.scales)[at], zero_of(p.zeros ? p.zeros[at] : 0));
       } else {
         const int k = k0 + 32 * q + 16 * i;
         sc[i] = k < K ? downf * __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(p.scales)[meta + k / 16], 0) : 0.0f;
       }
     }
-    multiply(std::integral_constant<int, TYPE>{}, acc, [&](int m, int i) { return a[m][i]; }, w, sc, zero, zero2, TRANS ? live : 4);
+    multiply(std::integral_constant<int, TYPE>{}, acc, [&](int m, int i) { return a[m][i]; }, w, sc, grp, TRANS ? live : 4);
   }
   const float rest = ldexpf(global, -down);
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float v = INT ? acc[m][r] * (1.0f / kDown<TYPE>) : __fdiv_rn(acc[m][r], rest);
+      const float v = INT ? acc[m][r] : __fdiv_rn(acc[m][r], rest);
       if (16 * m + 4 * q + r < rows && n0 + col < N) y[(int64_t)(16 * m + 4 * q + r) * p.ldy] = E::down(v);
     }
 }
@@ -546,7 +556,7 @@ static hipError_t run_w4(const W4Args& p, hipStream_t s) {
     return p.M / p.G > 4 && waves >= 512 ? run_split<TYPE, KIND, GROUP, 4>(p, s) : run_split<TYPE, KIND, GROUP, 1>(p, s);
   if (p.M / p.G <= 16) return run_wide<TYPE, KIND, GROUP, 1, SPAN, 4>(p, s);
   // 512 rows in 8 groups of 4096 x 4096 by tiles of 64 / 32 rows: groups of 128 80 / 88 us; groups of 64 (whose larger tiles spill)
-  // 146 / 93, of 32 343 / 105
+  // 146 / 94, of 32 343 / 132
   return run_wide<TYPE, KIND, GROUP, KIND == W4_INT && GROUP < 128 ? 2 : 4, SPAN, 8>(p, s);
 }
 template <int TYPE>

@@ -177,6 +177,27 @@ def test_a_row_that_is_not_finite_stays_alone():
             assert torch.isnan(got["dx"][6].float()).any()
 
 
+@pytest.mark.parametrize("H", [72, 2304, 9000])
+@pytest.mark.parametrize("gate", ["none", "channel", "full"])
+def test_infinities_reach_no_gradient_that_has_not_their_formula(gate, H):
+    """Without norms dx is dy and dbranch = scale gate dy, whatever x and branch hold; with one of the norms the
+    other side's rows stay as finite as their formula."""
+    c = _make(4, H, "bf16", gate, False, False, False)
+    ref = _run(c, 0.5, 1e-6, c["branch"], None)
+    dy = c["branch"].clone()
+    c["x"][1, 3] = math.inf
+    c["branch"][2, 5] = -math.inf
+    c["branch"][0, 7] = math.nan
+    got = _run(c, 0.5, 1e-6, dy, None)
+    assert torch.equal(got["dx"].cpu(), dy) and torch.equal(got["dx"], ref["dx"]) and torch.equal(got["dbranch"], ref["dbranch"])
+    c = _make(4, H, "bf16", gate, False, True, False)
+    ref = _run(c, 0.5, 1e-6, dy, None)
+    c["x"][1, 3] = math.inf
+    got = _run(c, 0.5, 1e-6, dy, None)
+    for n in ("dx", "dbranch", "dbranch_weight", "dgate"):
+        assert got[n] is None or torch.equal(got[n], ref[n]), n
+
+
 def test_gradients_against_differences():
     """<grad, v> against central differences of the loss, taken in 64 bits on the CPU."""
     for gate in GATES:

@@ -83,6 +83,82 @@ def test_products(splits, M, N, K, kind, dt):
         _check(randn((M, K), dtype, 3), w, kind, splits)
 
 
+# what the launcher takes: four column tiles a workgroup (more than 4 rows a group, 512 tiles or more); spans with one
+# row tile (2048 tiles or more, K of 512 or more), with several (more than 16 rows a group); K whole spans, with whole
+# chunks behind them, with a part of one; rows of scales that begin at every alignment
+LARGE = {"columns": ([9, 0, 20], 31, 2005, 416), "columns_long": ([30], 30, 4999, 1100), "spans": ([5, 0, 16, 17], 40, 5001, 1024),
+         "spans_tail": ([1, 0, 2, 30, 1], 36, 5003, 1190), "spans_one": ([3, 3, 3, 3, 3, 3], 21, 5010, 512),
+         "rows": ([100, 3, 64], 170, 2901, 1190), "rows_whole": ([33, 200, 1], 240, 2900, 1024)}
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("case", list(LARGE))
+def test_products_of_many_tiles(case, kind, dt):
+    splits, M, N, K = LARGE[case]
+    K = _k(kind, K)
+    print(f"w4 large {case} splits={splits} M={M} N={N} K={K} {kind} {dt}", flush=True)
+    for seed in (1, 2):
+        w = _make(kind, len(splits), N, K, DTYPES[dt], seed)
+        _check(randn((M, K), DTYPES[dt], 3), w, kind, splits)
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows", [8, 60])
+def test_rows_of_every_size_in_spans(rows, kind, dt):
+    """Rows as large and as small as the type has them, large beside small within a span, subnormals, zeros; then
+    rows that are not finite, which stay alone."""
+    dtype = DTYPES[dt]
+    splits = [rows, 0, 1, 2] if rows < 16 else [rows, 20]
+    M, N, K = sum(splits), 6001 if rows < 16 else 4003, _k(kind, 1100)
+    # weights of about 2^-12, so that sums of the largest rows stay in the type
+    if kind == "nvfp4":
+        w = list(_make(kind, len(splits), N, K, dtype))
+        w[2] = w[2] * 2.0 ** -10
+    else:
+        w = list(_make(kind, len(splits), N, K, dtype))
+        w[1] = (w[1].float() * 2.0 ** -9).to(dtype)
+    x = randn((M, K), dtype, 3)
+    f = torch.finfo(dtype)
+    top = 2.0 ** 126 if dt == "bf16" else 2.0 ** 14
+    x[0] = (x[0].float().clamp(-1.9, 1.9) * top).to(dtype)
+    x[1] = (x[1].float() * f.tiny).to(dtype)
+    x[2] = (x[2].float() * f.tiny * f.eps * 4).to(dtype)                      # subnormals
+    x[3] = 0
+    x[4] = (x[4].float() * torch.pow(2.0, torch.arange(K) % 40 - 30.0)).to(dtype)
+    x[5, ::3] = top / 4
+    x[6, 600:] = 0
+    ref = _check(x, w, kind, splits)
+    bad = x.clone()
+    bad[4, 9], bad[5, 700], bad[6, 130] = math.nan, math.inf, -math.inf
+    y = g.grouped_matmul_w4(bad.cuda(), _handle(w, kind), torch.tensor(splits, dtype=torch.int32, device="cuda"))
+    keep = torch.tensor([i for i in range(M) if i not in (4, 5, 6)])
+    assert torch.equal(y[keep], ref[keep]) and bool(torch.isnan(y[4]).all())
+    for row, k, sign in ((5, 700, 1), (6, 130, -1)):
+        v = _values(w, kind)[0, :, k]
+        got = y[row].cpu().double()
+        assert bool(torch.isnan(got[v == 0]).all()) and torch.equal(got[v != 0], sign * torch.sign(v[v != 0]) * math.inf)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_strides_and_a_given_output_in_spans(kind):
+    for splits, M, N in (([3, 9, 1, 8], 30, 5009), ([60, 20], 90, 4005)):
+        K = _k(kind, 1100)
+        w = _make(kind, len(splits), N, K, torch.bfloat16)
+        x = randn((M, K), torch.bfloat16, 3)
+        ref = _check(x, w, kind, splits)
+        m, used = torch.tensor(splits, dtype=torch.int32, device="cuda"), sum(splits)
+        for pad, off in ((3, 1), (24, 8)):
+            big = torch.full((M, K + pad), math.nan, dtype=torch.bfloat16, device="cuda")
+            big[:, off:off + K] = x.cuda()
+            out = torch.full((M, N + pad), 7.0, dtype=torch.bfloat16, device="cuda")
+            g.grouped_matmul_w4(big[:, off:off + K], _handle(w, kind), m, out=out[:, off:off + N])
+            assert torch.equal(out[:used, off:off + N], ref[:used])
+            out[:used, off:off + N] = 7.0
+            assert bool((out == 7.0).all())
+
+
 @pytest.mark.parametrize("dt", list(DTYPES))
 @pytest.mark.parametrize("kind", KINDS)
 def test_every_element_is_at_its_place(kind, dt):
