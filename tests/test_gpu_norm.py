@@ -72,6 +72,15 @@ def test_every_combination(pre, post, gate, wide, dt):
     _check(_make(5, 2304, dt, gate, pre, post, wide), scale=1.0)
 
 
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("H", [3, 5000, 8001, 12000, 20001])
+def test_fp32_parameters_of_long_rows(H, gate, dt):
+    """Every kernel of the backward with fp32 parameters and gates, whole and ragged rows."""
+    print(f"norm long H={H} gate={gate} {dt}", flush=True)
+    _check(_make(3, H, dt, gate, True, True, True), scale=0.5)
+
+
 @pytest.mark.parametrize("T,H", [(1, 64), (700, 200), (1025, 72), (2500, 1001)])
 def test_column_sums_of_many_rows(T, H):
     print(f"norm columns T={T} H={H}", flush=True)
