@@ -2,7 +2,7 @@
 
     python -m nvfp4_block_scaled_mxfp8_amd.build
 
-Compiles every source under csrc/ with hipcc into one shared library next to
+Compiles every source under csrc/ with hipcc, side by side, and links one shared library next to
 this file.  Flags: -O3, gfx950 only, no fast-math (correctly rounded fp32
 division is relied on by the NVFP4 cast), fp contraction off (bit-reproducible
 epilogues), and packed-fp32 instructions disabled.
@@ -11,6 +11,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -37,18 +39,25 @@ def hipcc():
 
 def build(verbose=True, extra_flags=()):
     """Compile libgmlp.so; raises on a compiler error."""
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
     tmp = LIB + ".tmp"
-    cmd = [hipcc()] + HIPCC_FLAGS + list(extra_flags) + srcs + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    noise = "unknown target feature"           # host pass does not know the packed-fp32 feature
-    err = "\n".join(l for l in (res.stderr or "").splitlines() if noise not in l and "packed-fp32" not in l)
-    if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + err)
-    if verbose and err.strip():
-        print(err, file=sys.stderr)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        noise = "unknown target feature"       # host pass does not know the packed-fp32 feature
+        err = "\n".join(l for l in (res.stderr or "").splitlines() if noise not in l and "packed-fp32" not in l)
+        if res.returncode != 0:
+            raise RuntimeError("hipcc failed:\n" + err)
+        if verbose and err.strip():
+            print(err, file=sys.stderr)
+
+    with tempfile.TemporaryDirectory() as out:
+        objs = [os.path.join(out, s + ".o") for s in SOURCES]
+        flags = [f for f in HIPCC_FLAGS if f != "-shared"] + list(extra_flags)
+        with ThreadPoolExecutor(min(len(SOURCES), 8)) as pool:
+            list(pool.map(lambda so: run([hipcc()] + flags + ["-c", os.path.join(CSRC, so[0]), "-o", so[1]]), zip(SOURCES, objs)))
+        run([hipcc()] + [f for f in HIPCC_FLAGS if f in ("-shared", "-fPIC") or f.startswith("--offload-arch")] + objs + ["-o", tmp])
     os.replace(tmp, LIB)
     return LIB
 
