@@ -178,10 +178,12 @@ __device__ void select_exact(const RouteArgs& p, const float* l, float top, int 
 // 16-bit logits without a bias lose no bits and need no proof.
 // 65536 rows of 256 with a bias: 34 us, 81 us in 64 bits throughout; 2049 rows in 8 groups 12 us, 20 in 64 bits.
 __device__ __forceinline__ float key_value(uint32_t key) { return __uint_as_float((key >> 31) ? key & 0x7FFFFFFFu : ~key); }
-// Ordered bits of a number that is none of NaN; 0 for a masked one.
-__device__ __forceinline__ uint32_t quick_key(float f, bool masked) {
-  const uint32_t u = __float_as_uint(f + 0.0f);               // -0 as +0
-  return masked ? 0u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+// Ordered bits of a number that is none of NaN and not -0.  Those of -inf, a masked one, and what lies below (0: not
+// allowed) are at most kNone; every number's are above.
+constexpr uint32_t kNone = 0x007FFFFFu;
+__device__ __forceinline__ uint32_t quick_key(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 // The value of the lane above or below, within 16 or 64 lanes (the last one's, the first one's: some lane's).
 template <int LPR>
@@ -230,16 +232,16 @@ __device__ bool select_fast(const RouteArgs& p, const float* l, const typename L
       }
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        const float x = l[j * W + i], c = score(x) + b[i];
+        const float x = l[j * W + i], c = score(x) + b[i];     // a score is not -0, nor is its sum
         odd |= c != c;
-        key[j * W + i] = quick_key(c, x == kMasked || c == kMasked);
+        key[j * W + i] = quick_key(x == kMasked ? kMasked : c);
       }
     }
   } else {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       odd |= l[v] != l[v];
-      key[v] = quick_key(l[v], l[v] == kMasked);
+      key[v] = quick_key(l[v] + 0.0f);                         // -0 as +0
     }
   }
   if (p.groups > 1) {
@@ -247,7 +249,7 @@ __device__ bool select_fast(const RouteArgs& p, const float* l, const typename L
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int e = expert_of<LPR, W>(v, lane);
-      if (e < p.E) keys[e] = p.bias || !scored ? key[v] : quick_key(score(l[v]), l[v] == kMasked);
+      if (e < p.E) keys[e] = p.bias || !scored ? key[v] : quick_key(l[v] == kMasked ? kMasked : score(l[v]));
     }
     wave_fence();
     for (int g = lane; g < p.groups; g += LPR) {
@@ -265,8 +267,8 @@ __device__ bool select_fast(const RouteArgs& p, const float* l, const typename L
         for (int u = 0; u < 8; ++u) take(x[u]);
       }
       for (; i < per; ++i) take(keys[g * per + i]);
-      const bool two = p.group_best > 1 && b;
-      group_value[2 * g] = a == 0 ? -INFINITY : two ? key_value(a) + key_value(b) : key_value(a);
+      const bool two = p.group_best > 1 && b > kNone;
+      group_value[2 * g] = a <= kNone ? -INFINITY : two ? key_value(a) + key_value(b) : key_value(a);
       group_value[2 * g + 1] = fabsf(key_value(a)) + (two ? fabsf(key_value(b)) : 0.0f);      // what it may be off by
     }
     wave_fence();
@@ -297,7 +299,6 @@ __device__ bool select_fast(const RouteArgs& p, const float* l, const typename L
     }
     wave_fence();
   }
-  // a masked key becomes one of at most IM, below every other
 #pragma unroll
   for (int v = 0; v < V; ++v) key[v] = (key[v] & ~IM) | (IM - (uint32_t)expert_of<LPR, W>(v, lane));
   const int most = min(p.k + 3, LPR);
@@ -308,7 +309,7 @@ __device__ bool select_fast(const RouteArgs& p, const float* l, const typename L
     for (int v = 0; v < V; ++v) d = max(d, key[v] - last);
     d = lanes_reduce<LPR>(d, [](uint32_t a, uint32_t b) { return max(a, b); });
     const uint32_t next = last + d;
-    last = next <= IM || (j > 0 && next >= last) ? 0u : next;  // masked ones only, or nothing left
+    last = next <= kNone || (j > 0 && next >= last) ? 0u : next;      // masked ones only, or nothing left
     if (lane == j) mine = last;
     if (last == 0) break;                                      // of this row: its lanes' reductions are their own
   }

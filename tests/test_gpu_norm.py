@@ -160,6 +160,27 @@ def test_in_place():
         assert y2 is c[into] and torch.equal(y, y2) and torch.equal(h, h2) and c[into]._version == version + 1
 
 
+def test_outputs_over_what_is_read_are_refused():
+    big = torch.zeros((12, 64), dtype=torch.bfloat16, device="cuda")
+    x, other, w = big[:8], torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda"), torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    for branch, out in ((other, big[1:9]), (big[1:9], x), (other, big[4:])):
+        with pytest.raises(ValueError, match="overlaps"):
+            g.residual_norm_forward(x, branch, w, out=out)
+    wide = torch.zeros((8, 128), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="overlaps"):
+        g.residual_norm_forward(wide[:, :64], other, w, gate=wide[:, 64:], out=wide[:, 60:124])
+    with pytest.raises(ValueError, match="overlaps"):
+        g.residual_norm_forward(other, x, w, gate=wide[0, :64], out=wide[:, :64])
+    y, _, _ = g.residual_norm_forward(wide[:, :64], other, w, out=wide[:, 64:])      # beside each other
+    assert not y.any()
+    with pytest.raises(ValueError, match="out"):
+        g.residual_norm_forward(x, None, w, out=other)
+    with pytest.raises(ValueError, match="stats"):
+        g.residual_norm_backward(other, other, x, other, torch.zeros((2, 7), device="cuda"), w)
+    with pytest.raises(ValueError, match="dh"):
+        g.residual_norm_backward(other, None, x, other, torch.zeros((2, 8), device="cuda"), w)
+
+
 @pytest.mark.parametrize("std", [1e-20, 1e-12, 1e12, 1e18, 1e36])
 def test_small_and_large_rows(std):
     """Squares that leave fp32 at both ends, without eps: the norms are still the formula's."""

@@ -298,6 +298,26 @@ def test_many_groups_and_random_splits():
             _check(randn((M, 192), dtype, 4), w, kind, splits)
 
 
+def test_outputs_over_what_is_read_and_codes_off_their_alignment_are_refused():
+    codes, scales, zeros = (t.cuda() for t in _int4(2, 64, 64, 32, torch.bfloat16, 1))
+    m = torch.tensor([2, 2], dtype=torch.int32, device="cuda")
+    big = torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda")
+    w = g.Int4Weights(codes, scales, zeros)
+    with pytest.raises(ValueError, match="overlaps"):
+        g.grouped_matmul_w4(big[:4], w, m, out=big[2:6])
+    y = g.grouped_matmul_w4(big[:4], w, m, out=big[4:])
+    assert not y.any()
+    for off in (1, 8):
+        room = torch.zeros(codes.numel() + 16, dtype=torch.uint8, device="cuda")
+        shifted = room[off:off + codes.numel()].view(codes.shape)
+        with pytest.raises(g.GmlpError, match="aligned"):
+            g.grouped_matmul_w4(big[:4], g.Int4Weights(shifted, scales, zeros), m)
+    with pytest.raises(ValueError, match="no gradient"):
+        g.grouped_matmul_w4(big[:4].clone().requires_grad_(), w, m)
+    with torch.no_grad():
+        g.grouped_matmul_w4(big[:4].clone().requires_grad_(), w, m)
+
+
 def test_no_rows_and_determinism():
     w = _handle(_make("32", 2, 24, 64, torch.bfloat16), "32")
     m = torch.zeros(2, dtype=torch.int32, device="cuda")
