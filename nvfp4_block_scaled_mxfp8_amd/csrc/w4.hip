@@ -291,20 +291,23 @@ __global__ __launch_bounds__(512) void w4_split_kernel(W4Args p, uint32_t ntn, i
 }
 
 // ----------------------------------------------------------------------------- many tiles
-// Where the tiles alone fill the device: a workgroup has 16 MT rows of one group and 128 columns, 16 a wave, and walks K in
-// spans of SPAN chunks: a wave's loads of the next span (512 or 1024 elements of each of its columns) are all in
+// Where the tiles alone fill the device: a workgroup has 16 MT rows of one group and 16 columns a wave, and walks K in
+// spans of SPAN chunks: a wave's loads of the next span (512 elements of each of its columns) are all in
 // flight while it multiplies this one, and x's part of a span lies in LDS for all waves.  What is left of K
 // behind the last whole span goes chunk by chunk.
-// bf16 rows of a single tile become fp16 on their way into LDS, times a power of two by row and span that brings the span's largest to
-// [2^14, 2^15): the same 8 bits down to 2^-28 of it, and no more than 2^-40 of it is lost below that, far under
-// what fp32 sums keep.  So both types decode by the packed operations that fp16 has and bf16 lacks (11 instead of
-// 22 operations a product of integers, 8 instead of 20 with NVFP4; a product's 512 weights take 85 ns at 6 TB/s and a
-// CU's share, four products side by side, 2 ns an operation).
+// bf16 rows of a single tile become fp16 on their way into LDS, times a power of two by row and span that brings the
+// span's largest to [2^14, 2^15): the same 8 bits down to 2^-28 of it, and no more than 2^-40 of it is lost below that,
+// far under what fp32 sums keep.  So both types decode by the packed operations that fp16 has and bf16 lacks: 9 instead
+// of 23 operations a product of integers, 8 instead of 20 with NVFP4.  At 6 TB/s a SIMD has 44 ns for a product's 512
+// weights: 22 to 26 operations at 2.0 to 2.4 GHz.
 // Loads alone, 16 rows of 64 bytes each, reach 6.0 TB/s where eight are in flight per wave, 3.5 to 4 with one or two.
+// 64 bf16 rows that reach 50 of 128 experts of 4096 x 7168, NVFP4 (us, whole launches in a graph): one chunk ahead 234;
+// spans in workgroups of eight waves, bf16 decode 246, fp16 195; of four waves 175; loads through the caches, not past
+// them, 164 to 167 (5.0 TB/s of the 50 experts' weights).
 template <int KIND, int GROUP, int SPAN>
 struct W4Span {
   static constexpr bool INT = KIND == W4_INT;
-  static constexpr int NS = INT ? SPAN * kW4Chunk / GROUP : SPAN * 2;      // 16-bit words of scales a lane has
+  static constexpr int NS = INT ? SPAN * kW4Chunk / GROUP : SPAN;          // 16-bit words of scales a lane has
   v4i w[SPAN];
   uint32_t s[NS / 2];        // integers: the column's, in order; NVFP4: of each four chunks, the one q's eight bytes
   uint32_t z[INT ? NS / 4 : 1];

@@ -3,8 +3,9 @@
     y = grouped_matmul_w4(x, w, m_splits)       # y[r] = x[r] w[g]^T, g the group of row r by m_splits
 
 w is an Int4Weights (integers with a scale, and a zero if given, by group of 32, 64 or 128 along K) or
-what weight_quantize made with the NVFP4 recipe.  One group is a dense layer.  Products are exact, sums fp32,
-each result is rounded once.  The weights are constants: no gradient is computed.  Argument marshalling only.
+what weight_quantize made with the NVFP4 recipe.  One group is a dense layer.  Sums are fp32 over exact products
+(where tiles fill the device and rows are few, elements of bf16 x may lose up to 2^-40 of the largest of the row's 512 around them), each result is
+rounded once; scales of integers are below 2^96.  The weights are constants: no gradient is computed.  Argument marshalling only.
 """
 import ctypes
 from dataclasses import dataclass
