@@ -31,11 +31,11 @@ _SIGS.update({"gmlp_grouped_matmul_four_bit": (ctypes.c_int, [ctypes.c_void_p, c
 _pack = _packer(W4Args)
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class Int4Weights:
     """w[g, n, k] = (q - zero) scale.  codes uint8 [G, N, K / 2]: q of k even in the low four bits, odd in the
     high; scales bf16 or fp16 [G, N, K / group] (the rows' type), zeros uint8 of that shape with values 0 to 15 or
-    None (8)."""
+    None (8).  Checked once, so its tensors are not replaced afterwards."""
     codes: torch.Tensor
     scales: torch.Tensor
     zeros: Optional[torch.Tensor] = None

@@ -1,5 +1,6 @@
 """Refusals of the operators around the experts (CPU): bad arguments are errors before anything is launched, in the
 binding and in the C ABI; and the C ABI's host code under the sanitizers."""
+import dataclasses
 import ctypes
 import os
 import shutil
@@ -120,6 +121,9 @@ def test_w4_refuses():
     for bad in (_t(2, 8, 2), _t(2, 8, 1, dtype=torch.uint8)):
         with pytest.raises(TypeError, match="zeros"):
             g.Int4Weights(codes, scales, bad)
+    for name, bad in (("codes", codes[:1]), ("scales", scales[:1]), ("zeros", _t(1, 8, 2, dtype=torch.uint8))):
+        with pytest.raises(dataclasses.FrozenInstanceError):           # would be read past its end
+            setattr(w, name, bad)
     q = {"row_data": codes.reshape(-1), "row_scale": _t(2 * 8 * 4, dtype=torch.uint8), "amax_pre": _t(2, dtype=torch.float32)}
     with pytest.raises(ValueError, match="GPU tensor"):
         g.grouped_matmul_w4(x, g.QTensor(g.NVFP4_RHT, q), m)
