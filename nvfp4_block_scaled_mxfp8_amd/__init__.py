@@ -14,6 +14,7 @@ under torch.autograd.
 import ctypes
 import os
 from dataclasses import dataclass, field
+from typing import Optional
 
 import torch
 
@@ -224,9 +225,11 @@ def read_device_flags(ws):
 # ----------------------------------------------------------------------------- quantized tensors
 @dataclass
 class QTensor:
-    """Device buffers of a group-quantized tensor (layouts as in include/gmlp.h)."""
+    """Device buffers of a group-quantized tensor (layouts as in include/gmlp.h).  shape: (E, N, K) of a quantized
+    weight, whose buffers are flat."""
     kind: int
     bufs: dict = field(default_factory=dict)
+    shape: Optional[tuple] = None
 
     def struct(self):
         return GroupedQ(*[_dev_ptr(self.bufs.get(n), n) for n in _Q_FIELDS])
@@ -294,6 +297,7 @@ def group_quantize(x, m_splits, rec, want_row=True, want_col=True, out=None, ws=
     G = m_splits.numel()
     if out is not None:
         _check_q_sizes(out, _grouped_need(rec, M, K, G, want_row, want_col), "out")
+        out.shape = None                                     # no weight, whatever it held
     out = out or alloc_grouped_q(rec, M, K, G, want_row, want_col, x.device)
     ws = ws if ws is not None else quant_workspace(G, x.device)
     q = out.struct()
@@ -311,6 +315,7 @@ def group_quantize_noalloc(x, m_splits, rec, want_row=True, want_col=True, out=N
     G = m_splits.numel()
     if out is not None:
         _check_q_sizes(out, _grouped_need(rec, M, K, G, want_row, want_col), "out")
+        out.shape = None                                     # no weight, whatever it held
     out = out or alloc_grouped_q(rec, M, K, G, want_row, want_col, x.device)
     q = out.struct()
     _check(lib().gmlp_group_quantize_noalloc(_p(x), M, K, _p(m_splits), G, rec, int(want_row), int(want_col),
@@ -339,6 +344,7 @@ def group_quantize_with_amax(x, m_splits, rec, amax_pre, amax_post, want_row=Tru
     G = m_splits.numel()
     if out is not None:
         _check_q_sizes(out, _grouped_need(rec, M, K, G, want_row, want_col), "out")
+        out.shape = None                                     # no weight, whatever it held
     out = out or alloc_grouped_q(rec, M, K, G, want_row, want_col, x.device)
     out.bufs["amax_pre"] = amax_pre
     out.bufs["amax_post"] = amax_post
@@ -368,7 +374,7 @@ def alloc_weight_q(rec, E, N, K, device="cuda", bf16_panels=True):
         if bf16_panels:               # the operands the GEMMs read, expanded once here
             b["row_bf16"] = torch.empty(2 * E * N * K, **u8)
             b["col_bf16"] = torch.empty(2 * E * K * N, **u8)
-    return QTensor(rec.kind, b)
+    return QTensor(rec.kind, b, (E, N, K))
 
 
 def _grouped_need(rec, M, K, G, row=True, col=True):
@@ -439,6 +445,7 @@ def weight_quantize(w, rec, out=None):
     q = out.struct()
     _check(lib().gmlp_weight_quantize(base, ptrs, E, N, K, rec, ctypes.byref(q), _p(ws), ws.numel(),
                                       _stream(dev)))
+    out.shape = (E, N, K)
     return out
 
 

@@ -3,7 +3,8 @@
     y = grouped_matmul_w4(x, w, m_splits)       # y[r] = x[r] w[g]^T, g the group of row r by m_splits
 
 w is an Int4Weights (integers with a scale, and a zero if given, by group of 32, 64 or 128 along K) or
-what weight_quantize made with the NVFP4 recipe.  One group is a dense layer.  Sums are fp32 over exact products
+what weight_quantize made with the NVFP4 recipe (a QTensor put together by hand says how long its rows are by its shape or by
+a row_data or row_scale [G, N, ..]: where all are flat, rows are taken to be as long as x's).  One group is a dense layer.  Sums are fp32 over exact products
 (where tiles fill the device and rows are few, elements of bf16 x may lose up to 2^-40 of the largest of the row's 512 around them), each result is
 rounded once; scales of integers are below 2^96.  The weights are constants: no gradient is computed.  Argument marshalling only.
 """
@@ -72,7 +73,12 @@ def _nvfp4(w, G, K):
         raise ValueError("w: contiguous row_data, row_scale and amax_pre are required")
     if c.dtype != torch.uint8 or s.dtype != torch.uint8 or a.dtype != torch.float32:
         raise TypeError("w: uint8 row_data and row_scale and fp32 amax_pre are required")
-    N = 2 * c.numel() // (G * K)
+    if w.shape is not None and (len(w.shape) != 3 or w.shape[0] != G or w.shape[2] != K):
+        raise ValueError(f"w: [{G}, N, {K}] expected, got {list(w.shape)}")
+    for t, n in ((c, K // 2), (s, K // 16)):                         # flatter ones do not say how long a row is
+        if t.dim() > 2 and t.shape[-1] != n:
+            raise ValueError(f"w: rows of {K} elements expected, got row_data {tuple(c.shape)} and row_scale {tuple(s.shape)}")
+    N = w.shape[1] if w.shape is not None else 2 * c.numel() // max(G * K, 1)
     if N < 1 or 2 * c.numel() != G * N * K or s.numel() * 16 != G * N * K or a.numel() != G:
         raise ValueError(f"w: sizes do not fit {G} groups of rows of {K} elements")
     return c, s, a, N

@@ -137,6 +137,34 @@ def test_w4_refuses():
         g.grouped_matmul_w4(x, g.QTensor(g.NVFP4_RHT, {**q, "row_scale": _t(64)}), m)
 
 
+def test_w4_refuses_an_nvfp4_weight_of_another_width():
+    """The weight's own K is held against x's, not inferred from it: rows of 64 read as twice as many of 32 would be other
+    weights."""
+    codes, scales, amax = _t(2, 8, 32, dtype=torch.uint8), _t(2, 8, 4, dtype=torch.uint8), _t(2, dtype=torch.float32)
+    flat = {"row_data": codes.reshape(-1), "row_scale": scales.reshape(-1), "amax_pre": amax}
+    m = _i32(2, 2)
+    for bufs, shape in (({**flat, "row_data": codes}, None), ({**flat, "row_scale": scales}, None), (flat, (2, 8, 64))):
+        w = g.QTensor(g.NVFP4_RHT, bufs, shape)
+        with pytest.raises(ValueError, match="GPU tensor"):                   # the width that it has
+            g.grouped_matmul_w4(_t(4, 64), w, m)
+        for K in (32, 128):
+            with pytest.raises(ValueError, match="^w:"):
+                g.grouped_matmul_w4(_t(4, K), w, m)
+    with pytest.raises(ValueError, match="^w:"):                              # the number of weights too
+        g.grouped_matmul_w4(_t(4, 64), g.QTensor(g.NVFP4_RHT, flat, (1, 16, 64)), m)
+    with pytest.raises(ValueError, match="^w:"):
+        g.grouped_matmul_w4(_t(4, 64), g.QTensor(g.NVFP4_RHT, flat), _i32())
+    # what the library makes says what it is
+    rec = g.recipe("nvfp4", 0x1234)
+    w = g.alloc_weight_q(rec, 2, 128, 256, device="cpu")
+    assert w.shape == (2, 128, 256)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        g.grouped_matmul_w4(_t(4, 256), w, m)
+    with pytest.raises(ValueError, match="^w:"):
+        g.grouped_matmul_w4(_t(4, 128), w, m)
+    assert g.alloc_grouped_q(rec, 128, 256, 2, device="cpu").shape is None
+
+
 # ----------------------------------------------------------------------------- C ABI
 P = 1 << 20          # an address that is aligned to everything and never read: each call is refused, or has no rows
 
