@@ -109,6 +109,8 @@ def grouped_matmul_w4(x, w, m_splits, out=None):
         kind, group = W4_NVFP4, 16
     else:
         raise TypeError("w: an Int4Weights or a QTensor is required")
+    if (scales.requires_grad or (amax is not None and amax.requires_grad)) and torch.is_grad_enabled():
+        raise ValueError("w: no gradient is computed for the weights' scales")
     for t, name in ((codes, "w"), (scales, "w"), (zeros, "w"), (amax, "w"), (m_splits, "m_splits")):
         if t is not None and t.device != dev:
             raise ValueError(f"{name}: on {t.device}, the other tensors are on {dev}")

@@ -165,6 +165,19 @@ def test_w4_refuses_an_nvfp4_weight_of_another_width():
     assert g.alloc_grouped_q(rec, 128, 256, 2, device="cpu").shape is None
 
 
+def test_w4_refuses_scales_that_wait_for_a_gradient():
+    """They would get none; without autograd they are numbers like others."""
+    x, m = _t(4, 64), _i32(2, 2)
+    scales = _t(2, 8, 2).requires_grad_()
+    amax = _t(2, dtype=torch.float32).requires_grad_()
+    flat = {"row_data": _t(512, dtype=torch.uint8), "row_scale": _t(64, dtype=torch.uint8), "amax_pre": amax}
+    for w in (g.Int4Weights(_t(2, 8, 32, dtype=torch.uint8), scales), g.QTensor(g.NVFP4_RHT, flat)):
+        with pytest.raises(ValueError, match="^w: no gradient"):
+            g.grouped_matmul_w4(x, w, m)
+        with torch.no_grad(), pytest.raises(ValueError, match="GPU tensor"):
+            g.grouped_matmul_w4(x, w, m)
+
+
 # ----------------------------------------------------------------------------- C ABI
 P = 1 << 20          # an address that is aligned to everything and never read: each call is refused, or has no rows
 
