@@ -22,6 +22,8 @@
 namespace gmlp {
 
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint16_t v2us __attribute__((ext_vector_type(2)));
+typedef int16_t v2ss __attribute__((ext_vector_type(2)));
 
 constexpr int kW4Chunk = sizes::kW4Chunk;
 
@@ -296,10 +298,11 @@ __global__ __launch_bounds__(512) void w4_split_kernel(W4Args p, uint32_t ntn, i
 // flight while it multiplies this one, and x's part of a span lies in LDS for all waves.  What is left of K
 // behind the last whole span goes chunk by chunk.
 // bf16 rows of a single tile become fp16 on their way into LDS, times a power of two by row and span that brings the
-// span's largest to [2^14, 2^15): the same 8 bits down to 2^-28 of it, and no more than 2^-40 of it is lost below that,
-// far under what fp32 sums keep.  So both types decode by the packed operations that fp16 has and bf16 lacks: 9 instead
-// of 23 operations a product of integers, 8 instead of 20 with NVFP4.  At 6 TB/s a SIMD has 44 ns for a product's 512
-// weights: 22 to 26 operations at 2.0 to 2.4 GHz.
+// span's largest to [2^14, 2^15): the same value as long as the smallest is no less than 2^-31 of it.  So both types decode
+// by the packed operations that fp16 has and bf16 lacks: 9 instead of 23 operations a product of integers, 8 instead of 20
+// with NVFP4.  At 6 TB/s a SIMD has 44 ns for a product's 512 weights: 22 to 26 operations at 2.0 to 2.4 GHz.
+// A row's span that spreads further is left out, and done behind the others with bf16 operands, chunk by chunk: of normally
+// distributed elements one in 10^9 is that small; where every row has one in every span the launch below takes 553 us.
 // Loads alone, 16 rows of 64 bytes each, reach 6.0 TB/s where eight are in flight per wave, 3.5 to 4 with one or two.
 // 64 bf16 rows that reach 50 of 128 experts of 4096 x 7168, NVFP4 (us, whole launches in a graph): one chunk ahead 234;
 // spans in workgroups of eight waves, bf16 decode 246, fp16 195; of four waves 175; loads through the caches, not past
@@ -334,7 +337,8 @@ __global__ __launch_bounds__(64 * WAVES) void w4_wide_kernel(W4Args p, uint32_t 
   using Span = W4Span<KIND, GROUP, SPAN>;
   static_assert(PIECES % 64 == 0, "a wave stages pieces of one row");
   extern __shared__ __align__(16) uint16_t s_x[];              // [2][ROWS][XLD]: rows 16 bytes apart in the banks
-  __shared__ __align__(16) float s_factor[2][PIECES / 64][ROWS];            // what brings a row's sums over a span back
+  __shared__ __align__(16) float s_factor[2][PIECES / 64][ROWS];            // what brings a row's sums over a span back; 0: left out
+  __shared__ int s_left[WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t block = (int64_t)blockIdx.x + (int64_t)blockIdx.y * p.row_blocks;
   if (block >= blocks) return;
@@ -371,35 +375,42 @@ __global__ __launch_bounds__(64 * WAVES) void w4_wide_kernel(W4Args p, uint32_t 
       for (int h = 0; h < SPAN / 4; ++h) __builtin_memcpy(&l.s[2 * h], static_cast<const uint8_t*>(p.scales) + meta + (s * SPAN + 4 * h + q) * 8, 8);
     }
   };
-  v4i xr[STAGE];
-  auto load_x = [&](int s) {
+  bool left = false;                                           // of the wave's rows: spans left out
+  auto load_x = [&](int s, int tid, v4i (&xr)[STAGE]) {
 #pragma unroll
     for (int i = 0; i < STAGE; ++i) {
       const int at = tid + NTH * i;
       if (at / PIECES < rows) __builtin_memcpy(&xr[i], x0 + (int64_t)(at / PIECES) * p.ldx + s * SK + at % PIECES * 8, 16);
     }
   };
-  auto store_x = [&](int s) {
+  auto store_x = [&](int s, int tid, const v4i (&xr)[STAGE]) {
 #pragma unroll
     for (int i = 0; i < STAGE; ++i) {
       const int at = tid + NTH * i, row = at / PIECES;
       if (row >= rows) continue;
       v4i v = xr[i];
       if constexpr (SCALED) {
-        int most = 0;                                          // the largest finite magnitude's bits
+        v2ss most2{128, 128};                                  // the largest finite magnitude's bits + 128: infinities and NaN are negative
+        v2us least2{65535, 65535};                             // the smallest's that is not 0, less 1
         float f[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int u = (int)(((uint32_t)v[j / 2] >> (16 * (j & 1))) & 0x7FFFu);
-          most = max(most, u < 0x7F80 ? u : 0);
-          f[j] = E::up((uint16_t)((uint32_t)v[j / 2] >> (16 * (j & 1))));
+        for (int j = 0; j < 4; ++j) {
+          const v2us u = __builtin_bit_cast(v2us, v[j] & 0x7FFF7FFF);
+          most2 = __builtin_elementwise_max(most2, __builtin_bit_cast(v2ss, u + v2us{128, 128}));
+          least2 = __builtin_elementwise_min(least2, u - v2us{1, 1});
+          f[2 * j] = E::up((uint16_t)v[j]);
+          f[2 * j + 1] = E::up((uint16_t)((uint32_t)v[j] >> 16));
         }
-        most = lanes_reduce<64>((uint32_t)most, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+        const int most = (int)lanes_reduce<64>((uint32_t)max((int)most2.x, (int)most2.y), [](uint32_t a, uint32_t b) { return a > b ? a : b; }) - 128;
+        const uint32_t least = min((uint32_t)least2.x, (uint32_t)least2.y);
+        // fp16's step below 2^-14 is 2^-24: all 8 bits from 2^-17 on, 31 binades below the largest
+        const bool fits = !__any(least < (uint32_t)max(((most >> 7) - 31) * 128 - 1, 0));
+        left |= !fits;
         const int e = min(141 - (most >> 7), 126);
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = (int)F::down2(f[2 * j] * up, f[2 * j + 1] * up);
-        if (lane == 0) s_factor[s & 1][at % PIECES / 64][row] = INT ? ldexpf(1.0f, -e) : ldexpf(downf, -e);
+        if (lane == 0) s_factor[s & 1][at % PIECES / 64][row] = !fits ? 0.0f : INT ? ldexpf(1.0f, -e) : ldexpf(downf, -e);
       }
       *reinterpret_cast<v4i*>(s_x + ((s & 1) * ROWS + row) * XLD + at % PIECES * 8) = APART ? pairs_apart(v) : v;
     }
@@ -462,37 +473,66 @@ __global__ __launch_bounds__(64 * WAVES) void w4_wide_kernel(W4Args p, uint32_t 
         for (int m = 0; m < MT; ++m) {
           const v4f f = *reinterpret_cast<const v4f*>(&s_factor[s & 1][c / 4][16 * m + 4 * q]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[m][r] = fmaf(f[r], sum[m][r], acc[m][r]);
+          for (int r = 0; r < 4; ++r) acc[m][r] = f[r] != 0.0f ? fmaf(f[r], sum[m][r], acc[m][r]) : acc[m][r];
         }
       __builtin_amdgcn_sched_barrier(0);                       // a chunk's values only are live at once
     }
   };
   Span l0, l1;
-  load_x(0);
+  v4i xr[STAGE];
+  load_x(0, tid, xr);
   load(0, l0);
-  store_x(0);
+  store_x(0, tid, xr);
   __syncthreads();
   for (int s = 0; s < spans; s += 2) {
     const bool more = s + 1 < spans;
     if (more) {
-      load_x(s + 1);
+      load_x(s + 1, tid, xr);
       load(s + 1, l1);
     }
     span(s, l0);
     if (!more) break;
-    store_x(s + 1);
+    store_x(s + 1, tid, xr);
     __syncthreads();
     const bool yet = s + 2 < spans;
     if (yet) {
-      load_x(s + 2);
+      load_x(s + 2, tid, xr);
       load(s + 2, l0);
     }
     span(s + 1, l1);
     if (!yet) break;
-    store_x(s + 2);
+    store_x(s + 2, tid, xr);
     __syncthreads();
   }
-  for (int c = spans * SPAN; c < chunks; ++c) {                // the rest of K
+  int behind = spans * SPAN;                                   // chunks that were done
+  if constexpr (SCALED) {
+    if (lane == 0) s_left[wave] = left;
+    __syncthreads();
+    for (int i = 0; i < WAVES; ++i) behind = s_left[i] ? 0 : behind;
+  }
+  bool mine[4] = {true, true, true, true};                     // the lane's rows that take part
+  for (int c = behind; c < chunks; ++c) {                      // the rest of K, and before it the spans that were left out
+    if constexpr (SCALED) {
+      static_assert(PIECES == 64, "a span has one factor");
+      if (c <= spans * SPAN && c % SPAN == 0) {
+        v4f f{0.0f, 0.0f, 0.0f, 0.0f};
+        if (c < spans * SPAN) {
+          v4i again[STAGE] = {};
+          int t = tid;
+          asm("" : "+v"(t));                                   // addresses of its own: none kept from above in registers
+          load_x(c / SPAN, t, again);
+          store_x(c / SPAN, t, again);
+          __syncthreads();
+          f = *reinterpret_cast<const v4f*>(&s_factor[c / SPAN & 1][0][4 * q]);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) mine[r] = f[r] == 0.0f && 4 * q + r < rows;
+        if (!__any(mine[0] || mine[1] || mine[2] || mine[3])) {          // the same in every wave
+          c += SPAN - 1;
+          continue;
+        }
+      }
+    }
     const int k0 = c * kW4Chunk, live = min((K - k0) / 32, 4);
     const v4i w = *reinterpret_cast<const v4i*>(codes + min(k0 / 2 + 16 * q, K / 2 - 16));
     v4i a[MT][4];
@@ -518,7 +558,14 @@ __global__ __launch_bounds__(64 * WAVES) void w4_wide_kernel(W4Args p, uint32_t 
         sc[i] = k < K ? downf * __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(p.scales)[meta + k / 16], 0) : 0.0f;
       }
     }
-    multiply(std::integral_constant<int, TYPE>{}, acc, [&](int m, int i) { return a[m][i]; }, w, sc, grp, TRANS ? live : 4);
+    v4f to[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) to[m] = acc[m];
+    multiply(std::integral_constant<int, TYPE>{}, to, [&](int m, int i) { return a[m][i]; }, w, sc, grp, TRANS ? live : 4);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[m][r] = mine[r] ? to[m][r] : acc[m][r];
   }
   const float rest = ldexpf(global, -down);
 #pragma unroll

@@ -411,3 +411,40 @@ def test_more_tiles_than_one_grid_row_holds():
     x[:, 3] = (torch.arange(M, device="cuda") % 97).to(torch.float16)
     y = g.grouped_matmul_w4(x, g.Int4Weights(codes, scales), torch.tensor([M], dtype=torch.int32, device="cuda"))
     assert torch.equal(y.amin(1), x[:, 3]) and torch.equal(y.amax(1), x[:, 3])
+
+
+def _in_spans(kind, seed, K=1190, rows=16, N=16400):
+    """bf16 rows of one tile over columns enough to fill the device: x, weights that are 0 at every 64th element of K, K."""
+    K = _k(kind, K)
+    w = _make(kind, 1, N, K, torch.bfloat16, 2)                        # integers without zeros: 8 is 0
+    w[0].view(N, K // 2)[:, ::32] = 0x08 if kind != "nvfp4" else 0x00
+    w[0].view(N, K // 2)[:, ::32] |= 0x90
+    return randn((rows, K), torch.bfloat16, seed), w, K
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_elements_beside_far_larger_ones_keep_their_bits(kind):
+    """The row's largest elements meet weights of 0, so that every bit of the others is seen: from 2^-24 to 2^-84 of the
+    largest, within one span, in the last part of K, alone and among ordinary elements."""
+    x, w, K = _in_spans(kind, 3)
+    ordinary = x.clone()
+    for r in range(16):
+        small = torch.zeros(K) if r % 2 else x[r].float() * 2.0 ** -(24 + 4 * r)
+        small[130 + r] = (1 + 127 / 128) * 2.0 ** -(24 + 4 * r)
+        small[K - 3] = (1 + 3 / 128) * 2.0 ** -(24 + 4 * r)
+        if r != 6:
+            small[700 + r] = -(1 + 65 / 128) * 2.0 ** -(24 + 4 * r)
+        small[::64] = 0
+        if r != 6:
+            small[64::512] = 1.0
+        small[960 if kind == "128" else 1088] = -1.5
+        x[r] = small.to(torch.bfloat16)
+    print(f"w4 spread {kind}", flush=True)
+    _check(x, w, kind, [16])
+    # rows are by themselves: the same beside others
+    m = torch.tensor([16], dtype=torch.int32, device="cuda")
+    mixed = torch.where((torch.arange(16) % 3 == 0)[:, None], x, ordinary)
+    ref = [g.grouped_matmul_w4(t.cuda(), _handle(w, kind), m) for t in (x, ordinary)]
+    y = g.grouped_matmul_w4(mixed.cuda(), _handle(w, kind), m)
+    for r in range(16):
+        assert torch.equal(y[r], ref[0 if r % 3 == 0 else 1][r]), r
