@@ -448,3 +448,18 @@ def test_elements_beside_far_larger_ones_keep_their_bits(kind):
     y = g.grouped_matmul_w4(mixed.cuda(), _handle(w, kind), m)
     for r in range(16):
         assert torch.equal(y[r], ref[0 if r % 3 == 0 else 1][r]), r
+
+
+def test_quantized_weights_say_what_they_are():
+    rec = g.recipe("nvfp4", 0x1234)
+    w16 = randn((2, 128, 256), torch.bfloat16, 5, 0.02).cuda()
+    m = torch.tensor([2, 2], dtype=torch.int32, device="cuda")
+    for w in (w16, list(w16)):
+        q = g.weight_quantize(w, rec)
+        assert q.shape == (2, 128, 256) and g.weight_quantize(w, rec, out=q).shape == (2, 128, 256)
+        assert g.grouped_matmul_w4(randn((4, 256), torch.bfloat16, 6).cuda(), q, m).shape == (4, 128)
+        with pytest.raises(ValueError, match="^w:"):
+            g.grouped_matmul_w4(randn((4, 128), torch.bfloat16, 6).cuda(), q, m)
+    out = g.alloc_grouped_q(rec, 256, 256, 2)
+    out.shape = (2, 128, 256)
+    assert g.group_quantize(w16.view(256, 256), torch.tensor([128, 128], dtype=torch.int32, device="cuda"), rec, out=out).shape is None
