@@ -301,8 +301,9 @@ __global__ __launch_bounds__(512) void w4_split_kernel(W4Args p, uint32_t ntn, i
 // span's largest to [2^14, 2^15): the same value as long as the smallest is no less than 2^-31 of it.  So both types decode
 // by the packed operations that fp16 has and bf16 lacks: 9 instead of 23 operations a product of integers, 8 instead of 20
 // with NVFP4.  At 6 TB/s a SIMD has 44 ns for a product's 512 weights: 22 to 26 operations at 2.0 to 2.4 GHz.
-// A row's span that spreads further is left out, and done behind the others with bf16 operands, chunk by chunk: of normally
-// distributed elements one in 10^9 is that small; where every row has one in every span the launch below takes 553 us.
+// A row's span that spreads further, or whose power of two leaves fp32 together with NVFP4's global scale, is left out, and
+// done behind the others with bf16 operands, chunk by chunk: of normally distributed elements one in 10^9 is that small;
+// where every row has one in every span the launch below takes 553 us.
 // Loads alone, 16 rows of 64 bytes each, reach 6.0 TB/s where eight are in flight per wave, 3.5 to 4 with one or two.
 // 64 bf16 rows that reach 50 of 128 experts of 4096 x 7168, NVFP4 (us, whole launches in a graph): one chunk ahead 234;
 // spans in workgroups of eight waves, bf16 decode 246, fp16 195; of four waves 175; loads through the caches, not past
@@ -404,9 +405,10 @@ __global__ __launch_bounds__(64 * WAVES) void w4_wide_kernel(W4Args p, uint32_t 
         const int most = (int)lanes_reduce<64>((uint32_t)max((int)most2.x, (int)most2.y), [](uint32_t a, uint32_t b) { return a > b ? a : b; }) - 128;
         const uint32_t least = min((uint32_t)least2.x, (uint32_t)least2.y);
         // fp16's step below 2^-14 is 2^-24: all 8 bits from 2^-17 on, 31 binades below the largest
-        const bool fits = !__any(least < (uint32_t)max(((most >> 7) - 31) * 128 - 1, 0));
+        const int e = most ? min(141 - (most >> 7), 126) : 0;
+        // and the power of two that brings the sums back is a number
+        const bool fits = !__any(least < (uint32_t)max(((most >> 7) - 31) * 128 - 1, 0)) && (INT || (down + e <= 126 && down + e >= -127));
         left |= !fits;
-        const int e = min(141 - (most >> 7), 126);
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = (int)F::down2(f[2 * j] * up, f[2 * j + 1] * up);

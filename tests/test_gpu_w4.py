@@ -450,6 +450,25 @@ def test_elements_beside_far_larger_ones_keep_their_bits(kind):
         assert torch.equal(y[r], ref[0 if r % 3 == 0 else 1][r]), r
 
 
+def test_rows_and_nvfp4_weights_at_opposite_ends():
+    """Rows and global scales whose powers of two together leave fp32 while the result does not: tiny rows by tiny
+    weights, huge rows by huge weights that are 0, tiny rows by huge weights."""
+    x, w, K = _in_spans("nvfp4", 4)
+    for p in range(16):
+        x[p] = (x[p].float().clamp(-1.9, 1.9) * 2.0 ** -(64 + p)).to(torch.bfloat16)
+    x[13] = 0
+    _check(x, (w[0], w[1], torch.full((1,), 2.0 ** -48)), "nvfp4", [16])
+    huge = torch.full((1,), 3e38)
+    x, w, K = _in_spans("nvfp4", 5)
+    w[0][:, ::2] = 0                                                  # columns of zeros
+    for p in range(16):
+        x[p] = (x[p].float().clamp(-1.9, 1.9) * 2.0 ** -(17 + 7 * p)).to(torch.bfloat16)
+    _check(x, (w[0], w[1], huge), "nvfp4", [16])
+    x[3] = (x[3].float() * 2.0 ** 38 * 2.0 ** 100).to(torch.bfloat16)
+    y = g.grouped_matmul_w4(x.cuda(), _handle((w[0], w[1], huge), "nvfp4"), torch.tensor([16], dtype=torch.int32, device="cuda"))
+    assert not y[:, ::2].any()                                        # (the others are past the largest number)
+
+
 def test_quantized_weights_say_what_they_are():
     rec = g.recipe("nvfp4", 0x1234)
     w16 = randn((2, 128, 256), torch.bfloat16, 5, 0.02).cuda()
