@@ -542,7 +542,8 @@ gmlp_status gmlp_route_backward(const gmlp_route_bwd_args* args, hipStream_t str
  * [H], by token [T] (strides ld_gate) or of every element [T, H] (rows of ld_gate).  weight, branch_weight and
  * gate are of the rows' type, or fp32 where their *_fp32 is not 0.  y may be x or branch itself with the
  * same row stride; other overlaps of outputs with inputs are not allowed.  1 <= H <= 32768.
- * stats: fp32 [2 T], for the backward: the factors 1 / sqrt(..) of branch and of y (written where the norm exists).
+ * stats: fp32 [2 T], for the backward: the factors 1 / sqrt(..) of branch and of y (written where the norm exists);
+ * one above 2^127, which only eps 0 leaves, as -factor 2^-64.
  * Backward, from dy (gradient of y, NULL: zeros) and dh (of h, NULL without weight): dx, dbranch
  * (row strides), dgate (of the gate's type and layout, contiguous), dweight, dbranch_weight; NULL where not
  * needed.  Column sums are taken in fp32 in an order that the sizes fix and rounded once. */

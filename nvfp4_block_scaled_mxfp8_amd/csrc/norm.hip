@@ -82,7 +82,24 @@ __device__ __forceinline__ T row_sum(T v, T* lds, int waves) {
   for (int w = 1; w < waves; ++w) s += lds[w];
   return s;
 }
-__device__ __forceinline__ float inv_root(double sum, int H, float eps) { return (float)(1.0 / sqrt(sum / H + (double)eps)); }
+// The factor 1 / sqrt(mean + eps).  Without eps, that of a row below 2^-127 (but not of zeros, whose is infinite) has no
+// place in fp32: then the row is multiplied by kTinyRow, exactly, and the factor is for that; stats hold it with a minus.
+constexpr float kTinyRow = 0x1p64f;
+struct RowFactor {
+  float f, row;
+  __device__ __forceinline__ float stat() const { return row == 1.0f ? f : -f; }
+};
+__device__ __forceinline__ RowFactor inv_root(double sum, int H, float eps) {
+  const double f = 1.0 / sqrt(sum / H + (double)eps);
+  if (eps == 0.0f && f > 0x1p127 && f < (double)INFINITY) return {(float)(f * 0x1p-64), kTinyRow};
+  return {(float)f, 1.0f};
+}
+// Of a workgroup's row; TINY: it may be such a row.
+template <bool TINY>
+__device__ __forceinline__ RowFactor row_factor(float stat) {
+  if (!TINY) return {stat, 1.0f};
+  return {fabsf(stat), stat < 0.0f ? kTinyRow : 1.0f};
+}
 
 // ----------------------------------------------------------------------------- forward
 template <int TYPE, int C, bool WAVE, bool SHORT>
@@ -113,8 +130,14 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs p) {
       for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fma((double)b[c][i], (double)b[c][i], ss);
-      rb = inv_root(row_sum<WAVE>(ss, s_red[0], waves), H, p.eps);
-      if (p.stats && tid == 0) p.stats[t] = rb;
+      const RowFactor r = inv_root(row_sum<WAVE>(ss, s_red[0], waves), H, p.eps);
+      rb = r.f;
+      if (p.stats && tid == 0) p.stats[t] = r.stat();
+      if (r.row != 1.0f)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) b[c][i] *= r.row;
     }
     const float st = p.gate_kind == GATE_TOKEN ? p.scale * load1p<TYPE>(p.gate, p.gate_fp32, t * p.ld_gate) : p.scale;
 #pragma unroll
@@ -146,8 +169,14 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs p) {
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = fma((double)y[c][i], (double)y[c][i], ss);
-  const float ry = inv_root(row_sum<WAVE>(ss, s_red[1], waves), H, p.eps);
-  if (p.stats && tid == 0) p.stats[p.T + t] = ry;
+  const RowFactor r = inv_root(row_sum<WAVE>(ss, s_red[1], waves), H, p.eps);
+  const float ry = r.f;
+  if (p.stats && tid == 0) p.stats[p.T + t] = r.stat();
+  if (r.row != 1.0f)
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[c][i] *= r.row;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int at = (c * nt + tid) * 8;
@@ -194,7 +223,7 @@ __device__ __forceinline__ void store_raw(void* base, int64_t at, int valid, v4i
       if (i < valid) p[i] = (uint16_t)((uint32_t)v[i / 2] >> (16 * (i & 1)));
   }
 }
-template <int TYPE, int C, int MAXT, int GATE, bool SHORT>
+template <int TYPE, int C, int MAXT, int GATE, bool SHORT, bool TINY>
 __global__ __launch_bounds__(MAXT) void norm_backward_kernel(NormArgs p) {
   constexpr bool AHEAD = C <= 2;         // the next row in registers, the parameters in LDS
   extern __shared__ __align__(16) float s_param[];     // [3][P]: weight, branch_weight, gate by channel
@@ -242,7 +271,7 @@ __global__ __launch_bounds__(MAXT) void norm_backward_kernel(NormArgs p) {
     }
   };
   // bh, n, g n, yh, u = dh w of four columns from `at`, and the gate and wb
-  auto columns = [&](int64_t t, const RawRow<C>& r, int c, int half, float rb, float ry, float gt, float* bh, float* n, float* g, float* wb,
+  auto columns = [&](int64_t t, const RawRow<C>& r, int c, int half, RowFactor rb, RowFactor ry, float gt, float* bh, float* n, float* g, float* wb,
                      float* yh, float* u, float* dh) {
     const int at = (c * nt + tid) * 8 + 4 * half;
     float x[4], w[4];
@@ -259,9 +288,9 @@ __global__ __launch_bounds__(MAXT) void norm_backward_kernel(NormArgs p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (GATE == BWD_GATE_NONE) g[i] = 1.0f;
-      bh[i] *= rb;
+      bh[i] = bh[i] * rb.row * rb.f;
       n[i] = bh[i] * wb[i];
-      yh[i] = fmaf(gt, GATE == BWD_GATE_NONE ? n[i] : g[i] * n[i], x[i]) * ry;
+      yh[i] = fmaf(gt, GATE == BWD_GATE_NONE ? n[i] : g[i] * n[i], x[i]) * ry.row * ry.f;
       u[i] = dh[i] * w[i];
     }
     if (!p.weight)                       // what is not finite in y stays out of the gradients that do not have it
@@ -290,8 +319,8 @@ __global__ __launch_bounds__(MAXT) void norm_backward_kernel(NormArgs p) {
         r.dh[c] = shift8(r.dh[c], valid);
         if (GATE == BWD_GATE_FULL) r.g[c] = shift8(r.g[c], valid);
       }
-    const float rb = post ? p.stats[t] : 1.0f;
-    const float ry = p.weight ? p.stats[p.T + t] : 0.0f;
+    const RowFactor rb = row_factor<TINY>(post ? p.stats[t] : 1.0f);
+    const RowFactor ry = row_factor<TINY>(p.weight ? p.stats[p.T + t] : 0.0f);
     const float gt = p.scale * (p.gate_kind == GATE_TOKEN ? load1p<TYPE>(p.gate, p.gate_fp32, t * p.ld_gate) : 1.0f);
     RowSums s{};
 #pragma unroll
@@ -327,7 +356,7 @@ __global__ __launch_bounds__(MAXT) void norm_backward_kernel(NormArgs p) {
       s.ny += o.ny;
     }
     const float c1 = s.uy * inv_h;
-    const float gnd = p.weight ? s.ndy + ry * (s.nu - c1 * s.ny) : s.ndy;      // sum of g n d
+    const float gnd = p.weight ? s.ndy + ry.f * ((s.nu - c1 * s.ny) * ry.row) : s.ndy;      // sum of g n d
     const float c2 = post ? gt * gnd * inv_h : 0.0f;
     if (p.dgate && p.gate_kind == GATE_TOKEN && tid == 0) store1p<TYPE>(p.dgate, p.gate_fp32, t, p.scale * gnd);
 #pragma unroll
@@ -342,7 +371,7 @@ __global__ __launch_bounds__(MAXT) void norm_backward_kernel(NormArgs p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           aw[c][4 * half + i] = fmaf(dh[i], yh[i], aw[c][4 * half + i]);
-          d[i] = fmaf(ry, fmaf(-yh[i], c1, u[i]), d[i]);
+          d[i] = fmaf(ry.f, fmaf(-yh[i], c1, u[i]) * ry.row, d[i]);
         }
         dx[2 * half] = (int)Elem<TYPE>::down2(d[0], d[1]);
         dx[2 * half + 1] = (int)Elem<TYPE>::down2(d[2], d[3]);
@@ -356,7 +385,7 @@ __global__ __launch_bounds__(MAXT) void norm_backward_kernel(NormArgs p) {
         }
         if (post)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d[i] = rb * fmaf(-bh[i], c2, d[i] * wb[i]);
+          for (int i = 0; i < 4; ++i) d[i] = rb.f * (fmaf(-bh[i], c2, d[i] * wb[i]) * rb.row);
         db[2 * half] = (int)Elem<TYPE>::down2(d[0], d[1]);
         db[2 * half + 1] = (int)Elem<TYPE>::down2(d[2], d[3]);
         if (GATE == BWD_GATE_FULL) {
@@ -445,8 +474,12 @@ hipError_t launch_norm(const NormArgs& p, hipStream_t s) {
 template <int TYPE, int C, int MAXT, int GATE, bool SHORT>
 static hipError_t run_backward(const NormArgs& p, hipStream_t s) {
   const int blocks = sizes::norm_bwd_blocks(p.T, p.H), threads = sizes::norm_threads(p.H, C);
-  hipLaunchKernelGGL((norm_backward_kernel<TYPE, C, MAXT, GATE, SHORT>), dim3(blocks), dim3(threads),
-                     C <= 2 ? 3 * 8 * C * sizeof(float) * threads : 0, s, p);
+  const size_t lds = C <= 2 ? 3 * 8 * C * sizeof(float) * threads : 0;
+  // four more products a value for rows that only eps 0 can have: 8192 x 7168, a gate by channel 170 -> 181 us, by token 160 -> 192
+  if (p.eps == 0.0f)
+    hipLaunchKernelGGL((norm_backward_kernel<TYPE, C, MAXT, GATE, SHORT, true>), dim3(blocks), dim3(threads), lds, s, p);
+  else
+    hipLaunchKernelGGL((norm_backward_kernel<TYPE, C, MAXT, GATE, SHORT, false>), dim3(blocks), dim3(threads), lds, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (!p.dweight && !p.dbranch_weight && !(p.dgate && p.gate_kind == GATE_CHANNEL)) return e;

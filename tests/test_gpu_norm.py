@@ -339,3 +339,48 @@ def test_more_rows_than_one_grid_row_holds():
     dx, dw = g.rms_norm_backward(torch.ones_like(x), x, w, stats, 0.0)
     # the norm of one element is its sign: no slope but roundings of (1 - yh^2) / |x|, two steps of fp32 each
     assert float(dx.float().abs().max()) <= 2 * 2.0 ** -21 and float(dw.float().abs()) <= T
+
+
+TINY = 2.0 ** -133                                # the smallest bf16 number
+
+
+@pytest.mark.parametrize("H", [7, 300, 2304, 9000])
+def test_rows_of_subnormals_without_eps(H):
+    """Without eps a norm does not depend on its row's size, down to rows of the smallest numbers, whose factor has no
+    place in fp32: values and gradients, beside ordinary rows, rows at the border and one of zeros (0 / 0)."""
+    T = 9
+    k = torch.randint(-9, 10, (T, H), generator=torch.Generator().manual_seed(1)).float()
+    k[:, 0] = 5.0
+    # sizes 2^-133, around 2^-128 and 2^-126, ordinary; the largest that one element can bring among zeros
+    x = (k * torch.tensor([TINY, TINY, 2.0 ** -130, 2.0 ** -129, 2.0 ** -127, 2.0 ** -125, 1.0, 2.0 ** 100, 1.0])[:, None]).to(torch.bfloat16)
+    x[1, 1:] = 0
+    x[8] = 0
+    x[8, 2] = 2.0 ** -122
+    w = 1 + randn((H,), torch.float32, 2, 0.2)
+    # the gradient for x of a row of size s is of size dh / s
+    dh = (randn((T, H), torch.float32, 3) * 2.0 ** -20).to(torch.bfloat16)
+    zero = torch.cat([x, torch.zeros((1, H), dtype=torch.bfloat16)])
+    h, stats = g.rms_norm_forward(x.cuda(), w.cuda(), 0.0)
+    dx, dw = g.rms_norm_backward(dh.cuda(), x.cuda(), w.cuda(), stats, 0.0)
+    want = norm_forms(x, None, w, None, None, 1.0, 0.0, None, dh)
+    assert_norm(h, want["h"], 16, "h")
+    assert_norm(dx, want["dx"], H + 32, "dx")
+    assert_norm(dw, want["dweight"], T + 32, "dweight")
+    hz, _ = g.rms_norm_forward(zero.cuda(), w.cuda(), 0.0)
+    assert torch.equal(hz[:T], h) and bool(torch.isnan(hz[T]).all())
+    # the branch's own norm, around ordinary rows; the sum of two such rows
+    c = dict(x=randn((T, H), torch.bfloat16, 4), branch=x, weight=w, branch_weight=1 + randn((H,), torch.float32, 5, 0.2),
+             gate=1 + randn((T, H), torch.bfloat16, 6, 0.2))
+    for gate, kind in ((None, "none"), (c["gate"], "full"), (c["gate"][:, :1].contiguous(), "token"), (c["gate"][0].contiguous(), "channel")):
+        print(f"norm subnormal H={H} gate={kind}", flush=True)
+        c["gate"] = gate
+        dy = (randn((T, H), torch.float32, 7) * 2.0 ** -20).to(torch.bfloat16)
+        got = _run(c, 0.5, 0.0, dy, dh)
+        want = norm_forms(c["x"], x, w, c["branch_weight"], gate, 0.5, 0.0, dy, dh)
+        terms = {"y": 8, "h": 16, "dx": H + 32, "dweight": T + 32, "dgate": 2 * H + T + 64, "dbranch": 4 * H + 64, "dbranch_weight": T + H + 64}
+        for name, form in want.items():
+            assert_norm(got[name], form, terms[name], f"{name} {kind}")
+    c = dict(x=x, branch=(x.float().roll(1, 1) * 4).to(torch.bfloat16), weight=w, branch_weight=None, gate=None)
+    got = _run(c, 1.0, 0.0, None, dh)
+    for name, form in norm_forms(x, c["branch"], w, None, None, 1.0, 0.0, None, dh).items():
+        assert_norm(got[name], form, {"y": 8, "h": 16, "dx": H + 32, "dweight": T + 32, "dbranch": 4 * H + 64}[name], f"{name} sum")
