@@ -344,7 +344,7 @@ def test_more_rows_than_one_grid_row_holds():
 TINY = 2.0 ** -133                                # the smallest bf16 number
 
 
-@pytest.mark.parametrize("H", [7, 300, 2304, 9000])
+@pytest.mark.parametrize("H", [7, 300, 2304, 5000, 9000, 20001])
 def test_rows_of_subnormals_without_eps(H):
     """Without eps a norm does not depend on its row's size, down to rows of the smallest numbers, whose factor has no
     place in fp32: values and gradients, beside ordinary rows, rows at the border and one of zeros (0 / 0)."""
@@ -384,3 +384,13 @@ def test_rows_of_subnormals_without_eps(H):
     got = _run(c, 1.0, 0.0, None, dh)
     for name, form in norm_forms(x, c["branch"], w, None, None, 1.0, 0.0, None, dh).items():
         assert_norm(got[name], form, {"y": 8, "h": 16, "dx": H + 32, "dweight": T + 32, "dbranch": 4 * H + 64}[name], f"{name} sum")
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("H", [3, 264, 5000, 12000, 20001])
+def test_every_kernel_without_eps(H, gate, dt):
+    """Ordinary rows, parameters of both types."""
+    print(f"norm without eps H={H} gate={gate} {dt}", flush=True)
+    for wide in (False, True):
+        _check(_make(4, H, dt, gate, True, True, wide), scale=0.5, eps=0.0)

@@ -482,3 +482,33 @@ def test_quantized_weights_say_what_they_are():
     out = g.alloc_grouped_q(rec, 256, 256, 2)
     out.shape = (2, 128, 256)
     assert g.group_quantize(w16.view(256, 256), torch.tensor([128, 128], dtype=torch.int32, device="cuda"), rec, out=out).shape is None
+
+
+def _folds(blocks, threads):
+    """A launch's threads along x are counted in 32 bits, in whole rounds over eight XCDs."""
+    return blocks > (2 ** 32 - 1) // threads // 8 * 8
+
+
+@pytest.mark.parametrize("kernel", ["split", "spans"])
+def test_grids_of_more_than_2_32_threads(kernel):
+    """Both kernels with their grids folded.  Split K, four column tiles a workgroup (more than 4 rows, K of 480: four waves);
+    spans of two row tiles (more than 16 rows, groups of 32: eight waves).  The spans of one row tile share their code
+    for the block's number, and would fold only past 130 GB of weights."""
+    M, N, K, row_tile, columns, threads = {"split": ((1 << 22) + 5, 4100, 480, 16, 64, 256),
+                                           "spans": ((1 << 21) + 33, 16385, 512, 32, 128, 512)}[kernel]
+    assert _folds(-(-M // row_tile) * -(-N // columns), threads)
+    free, _ = torch.cuda.mem_get_info()
+    if free < 90 << 30:
+        pytest.skip("needs 90 GB")
+    print(f"w4 folded {kernel}", flush=True)
+    codes = torch.full((1, N, K // 2), 0x99, dtype=torch.uint8, device="cuda")
+    codes[0, N - 3] = 0xAA                                              # a column of twos
+    scales = torch.ones((1, N, K // 32), dtype=torch.float16, device="cuda")
+    x = torch.zeros((M, K), dtype=torch.float16, device="cuda")
+    x[:, 3] = (torch.arange(M, device="cuda") % 97).to(torch.float16)
+    x[:, K - 1] = (torch.arange(M, device="cuda") % 89).to(torch.float16)
+    y = g.grouped_matmul_w4(x, g.Int4Weights(codes, scales), torch.tensor([M], dtype=torch.int32, device="cuda"))
+    want = x[:, 3] + x[:, K - 1]
+    assert torch.equal(y[:, N - 3], 2 * want)
+    y[:, N - 3] = want
+    assert torch.equal(y.amin(1), want) and torch.equal(y.amax(1), want)
