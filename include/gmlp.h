@@ -590,8 +590,8 @@ gmlp_status gmlp_residual_norm_backward(const gmlp_norm_bwd_args* args, hipStrea
  *                   at most 15; NULL: 8); group 32, 64 or 128, K a multiple of it
  *   GMLP_W4_NVFP4   w = E2M1(q) E4M3(s) / S, blocks of 16 along K (group 16): codes and block scales as gmlp_weight_quantize
  *                   leaves them in row_data and row_scale, S = fp32(2688 / amax[g]) clipped to FLT_MAX (1 for amax 0); K a multiple of 32
- * Sums are fp32 on the matrix cores over exact products (a group's integers are summed before its scale; scales below 2^96
- * in magnitude: larger ones may overflow sums that are later small), rounded once.
+ * Sums are fp32 on the matrix cores over exact products (a group's integers are summed before its scale; scales of 0 or
+ * of 2^-100 to 2^96 in magnitude: larger ones may overflow sums that are later small, smaller ones may lose bits), rounded once.
  * For few rows, as decoding has them; any M runs.  Rows of y behind the last group are zeroed when zero_rest != 0, else left
  * as they are.  Splits are clamped on the device as everywhere.  y must not overlap what is read.  No workspace. */
 typedef enum { GMLP_W4_INT = 0, GMLP_W4_NVFP4 = 1 } gmlp_w4_kind;

@@ -2,7 +2,8 @@
 //   n = b rb wb, rb = (mean b^2 + eps)^-1/2;  y = x + s g n;  h = y ry w, ry = (mean y^2 + eps)^-1/2
 // Bound by memory: forward 8 bytes an element (x, branch, y, h), backward 12 (x, branch, dy, dh, dx, dbranch).
 //
-// 8192 rows of 7168 (bf16, fp32 parameters): forward 98 us (4.8 TB/s), backward 171 + 6 us (4.2 TB/s; a copy reaches 5.2).
+// 8192 rows of 7168 (bf16, fp32 parameters): forward 100 to 104 us (4.6 TB/s), backward 165 to 180 and 6 us of column sums (4.0 TB/s;
+// a copy reaches 4.9).
 //
 // A row belongs to one workgroup (rows of up to 2048 in the forward: to one wave), 8 C values a thread in registers, so
 // that each tensor is read once.  Squares are summed in 64 bits: a square of a 16-bit value is exact in them, and
@@ -199,6 +200,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs p) {
 // rows of 7168: loads by branches on the row's end 425 us; without branches but with selects for absent inputs and 1024
 // threads' 128 registers (spills wait for the row ahead) 464; 512 threads 308; no selects 220; values of four
 // columns live at once 171 (with 1024 threads 213).
+// Rows above 8192 have 32 values a thread: no row ahead, parameters by element, and registers spilled; 4096 x 12288 1100 us,
+// 4096 x 16384 1350, 2048 x 32768 2290.
 struct RowSums {
   float uy, ndy, nu, ny;
 };

@@ -602,13 +602,16 @@ static hipError_t run_wide(W4Args p, hipStream_t s) {
 template <int TYPE, int KIND, int GROUP>
 static hipError_t run_w4(const W4Args& p, hipStream_t s) {
   constexpr int SPAN = 4;
-  // 16 x 16 tiles: eight a CU, a wave each, fill the device (64 rows over 128 experts of 4096 x 7168, NVFP4: 165 us in spans, 232 as few tiles)
+  // Spans where there are 2048 tiles of 16 x 16, a wave each eight a CU; near where the two cross for the larger tiles too (us,
+  // split K / spans): 64 rows over 128 experts of 4096 x 7168, NVFP4 305 / 161; 4, 8 and 16 rows over 16 experts of 2048 x 2048,
+  // NVFP4 (512, 1024 and 2048 tiles) 7.2 / 9.3, 12.8 / 9.6, 16.8 / 11.9; dense 7168 x 4096, groups of 128, 48, 64 and 96 rows (1792,
+  // 2240 and 3136) 28.5 / 35.0, 28.8 / 36.7, 41.7 / 37.2, 64 rows NVFP4 34.0 / 34.1, groups of 64 34.2 / 31.5, of 32 37.6 / 43.4
   const int64_t waves = sizes::row_tiles_bound(p.M, p.G, 16) * ((p.N + 15) / 16);
   if (waves < 2048 || p.K < SPAN * kW4Chunk)
     return p.M / p.G > 4 && waves >= 512 ? run_split<TYPE, KIND, GROUP, 4>(p, s) : run_split<TYPE, KIND, GROUP, 1>(p, s);
   if (p.M / p.G <= 16) return run_wide<TYPE, KIND, GROUP, 1, SPAN, 4>(p, s);
-  // 512 rows in 8 groups of 4096 x 4096 by tiles of 64 / 32 rows: groups of 128 80 / 88 us; groups of 64 (whose larger tiles spill)
-  // 146 / 94, of 32 343 / 132
+  // 512 rows in 8 groups of 4096 x 4096, their sizes drawn, by tiles of 64 / 32 rows: groups of 128 80 / 88 us; groups of 64 (whose
+  // larger tiles spill) 146 / 94, of 32 343 / 132
   return run_wide<TYPE, KIND, GROUP, KIND == W4_INT && GROUP < 128 ? 2 : 4, SPAN, 8>(p, s);
 }
 template <int TYPE>

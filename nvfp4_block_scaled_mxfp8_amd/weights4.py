@@ -2,10 +2,11 @@
 
     y = grouped_matmul_w4(x, w, m_splits)       # y[r] = x[r] w[g]^T, g the group of row r by m_splits
 
-w is an Int4Weights (integers with a scale, and a zero if given, by group of 32, 64 or 128 along K) or
-what weight_quantize made with the NVFP4 recipe (a QTensor put together by hand says how long its rows are by its shape or by
-a row_data or row_scale [G, N, ..]: where all are flat, rows are taken to be as long as x's).  One group is a dense layer.  Sums are fp32 over exact products,
-each result is rounded once; scales of integers are below 2^96.  The weights are constants: no gradient is computed.  Argument marshalling only.
+w is an Int4Weights (integers with a scale, and a zero if given, by group of 32, 64 or 128 along K) or what
+weight_quantize made with the NVFP4 recipe (a QTensor put together by hand says how long its rows are by its shape
+or by a row_data or row_scale [G, N, ..]: where all are flat, rows are taken to be as long as x's).  One group is a
+dense layer.  Sums are fp32 over exact products, each result is rounded once; scales of integers are 0 or 2^-100 to
+2^96 in magnitude.  The weights are constants: no gradient is computed.  Argument marshalling only.
 """
 import ctypes
 from dataclasses import dataclass
