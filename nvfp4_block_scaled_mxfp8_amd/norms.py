@@ -157,7 +157,7 @@ def residual_norm_backward(dy, dh, x, branch, stats, weight=None, branch_weight=
                            need_dx=True, need_dbranch=True, need_dweight=True, need_dbranch_weight=True, need_dgate=True):
     """{"dx", "dbranch", "dweight", "dbranch_weight", "dgate"} (None where there is no such input or it is
     not needed) from the gradients of y (None: zeros) and h (None without weight) and a forward's inputs and
-    stats.  The inputs must be as the forward had them: not after an in-place forward."""
+    stats.  The inputs, scale and eps must be as the forward had them: not after an in-place forward."""
     fields, kept, dev, shape = _inputs(x, branch, weight, branch_weight, gate, scale, eps)
     T, H = shape
     dy, pdy, lddy = _rows(dy, shape, x.dtype, dev, "dy")
