@@ -220,7 +220,8 @@ __device__ bool select_fast(const RouteArgs& p, const float* l, const typename L
     return p.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-x)) : __expf(x - top) * inv_sum;
   };
   uint32_t key[V];
-  bool odd = false;                                            // NaN, which only 64 bits put in order, or no certainty
+  // NaN, which only 64 bits put in order (an infinite logit makes all of a softmax NaN), or no certainty
+  bool odd = scored && !p.sigmoid && inv_sum != inv_sum;
   if (p.bias) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {

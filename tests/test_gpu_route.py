@@ -343,3 +343,24 @@ def test_more_rows_than_one_grid_row_holds():
         if bool(at.any()):
             p = max(math.exp(a), math.exp(b)) / (math.exp(a) + math.exp(b))
             assert bool(((probs[:, 0][at].double() - p).abs() <= route_tol(2, 2) * p).all())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("E,groups,top,k", [(8, 2, 2, 7), (32, 4, 2, 8), (64, 4, 3, 7), (256, 8, 1, 9), (512, 4, 2, 20)])
+@pytest.mark.parametrize("dt", list(TYPES))
+def test_infinities_and_nan_in_groups(E, groups, top, k, best, score, dt):
+    """A row with an infinite logit has no softmax that is a number: its experts are chosen all the same, NaN first."""
+    logits = _logits(9, E, TYPES[dt], 41, masked=0.2)
+    logits[1, 3] = logits[2, E - 1] = logits[3, E // 2] = logits[3, 0] = math.inf
+    logits[4, 1] = logits[5, E - 2] = math.nan
+    logits[5, 2] = logits[6, E // 2 - 1] = math.inf
+    logits[6] = torch.where(logits[6] == math.inf, logits[6], torch.full_like(logits[6], -math.inf))
+    some = _bias(E, 42)
+    high = some.clone()
+    high[::5] = math.inf
+    low = some.clone()
+    low[1::3] = -math.inf
+    for bias in (None, some, high, low):
+        _check(logits, k, score, bias, groups, top, best)
+        _check(logits, k, score, bias, groups, top, best, renormalize=False)
